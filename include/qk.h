@@ -298,6 +298,129 @@ QK_API qk_status qk_xent_bwd_ex(const void* logits, const int64_t* targets, cons
                                 const float* dloss, void* dlogits, int64_t M, int64_t N,
                                 qk_dtype dtype, const qk_xent_options* options, void* stream);
 
+/*
+ * The norm with the residual's addition.  A decoder's RMSNorm stands behind a
+ * residual addition; these entry points do both in one pass over the rows.
+ * (The article names RMSNorm only; these are that operator as models call it.)
+ *
+ * Forward, for each row i:
+ *   h[i,j] = x[i,j] + residual[i,j], rounded to dtype once: the residual
+ *            stream as it is kept.  The norm is of that kept h, so the result
+ *            is qk_rmsnorm_fwd's on h, and the backward pass needs h only.
+ *   rstd[i] = 1 / sqrt(mean_j h[i,j]^2 + eps),  y[i,j] = h[i,j] * rstd[i] * w[j].
+ *
+ *   x, residual  [M, N] dtype, read once.   w [N] dtype.
+ *   y      [M, N] dtype; may be x or residual exactly.
+ *   h      [M, N] dtype; may be x or residual exactly, but not y.
+ *   rstd   [M] float32, may be NULL.
+ *   Other overlaps are QK_ERR_INVALID_ARG.  Any N >= 1.
+ */
+QK_API qk_status qk_add_rmsnorm_fwd(const void* x, const void* residual, const void* w, void* y,
+                                    void* h, float* rstd, int64_t M, int64_t N, float eps,
+                                    qk_dtype dtype, void* stream);
+
+/*
+ * Backward of qk_add_rmsnorm_fwd: x and residual get the same gradient,
+ *   dx[i,j] = dh[i,j] + rstd_i dy[i,j] w_j - h[i,j] rstd_i^3 (1/N) sum_k dy[i,k] w_k h[i,k]
+ *   dw[j]   = sum_i dy[i,j] h[i,j] rstd_i          (overwritten; summed in a fixed order)
+ *   h, dy  [M, N] dtype;  w [N] dtype;  rstd [M] float32, as the forward wrote it.
+ *   dh     [M, N] dtype: the gradient that reaches h by the residual stream; NULL for none.
+ *   dx     [M, N] dtype; may be h, dy or dh exactly.
+ *   dw     [N] float32; all zeros when M == 0.
+ *   workspace  at least qk_add_rmsnorm_bwd_workspace_size() bytes of device
+ *              memory, 16-byte aligned, scratch (fp32 partial sums of dw).
+ *   Any N >= 1.
+ */
+QK_API qk_status qk_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t N, qk_dtype dtype,
+                                                   size_t* bytes);
+QK_API qk_status qk_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, const void* dy,
+                                    const void* dh, void* dx, float* dw, void* workspace,
+                                    size_t workspace_bytes, int64_t M, int64_t N, qk_dtype dtype,
+                                    void* stream);
+
+/* 8-bit output types: QK_E4M3 (4 exponent bits, 3 of mantissa, largest value
+ * 448) and QK_INT8 (-127 ... 127). */
+typedef enum { QK_E4M3 = 0, QK_INT8 = 1 } qk_qtype;
+
+/*
+ * RMSNorm (with or without the residual's addition) with an output in 8 bits.
+ * h, rstd and the unrounded y as in qk_add_rmsnorm_fwd (h = x without a
+ * residual); then, for each row and each group of `group` columns (0: the
+ * whole row), with qmax = 448 (QK_E4M3) or 127 (QK_INT8):
+ *   scale[i,c] = max(max_{j in group c} |y[i,j]|, 2^-100) / qmax
+ *   q[i,j]     = y[i,j] / scale[i,c], rounded to nearest even
+ * so that q * scale stands for y.  A group of zeros has a positive scale.  A
+ * group with an infinite or NaN y gets scale = NaN, and so does everything
+ * that its q stand for.
+ *
+ *   x        [M, N] dtype; residual [M, N] dtype or NULL; w [N] dtype.
+ *   q        [M, N] bytes; overlaps no other buffer.
+ *   scale    [M, ceil(N / group)] float32 ([M] when group is 0); the last
+ *            group of a row may be short.
+ *   h        [M, N] dtype; may be x or residual exactly; NULL when not wanted.
+ *            Without a residual it must be NULL.
+ *   rstd     [M] float32, may be NULL.
+ *   group    0, 32, 64 or 128.   Any N >= 1.
+ */
+QK_API qk_status qk_rmsnorm_quant_fwd(const void* x, const void* residual, const void* w, void* q,
+                                      float* scale, void* h, float* rstd, int64_t M, int64_t N,
+                                      float eps, int64_t group, qk_dtype dtype, qk_qtype qtype,
+                                      void* stream);
+
+/*
+ * Linear cross-entropy: the loss of a model's last product without its logits.
+ * For hidden rows h [M, K] and a vocabulary's weights w [V, K],
+ *   logits[i,v] = sum_k h[i,k] w[v,k]   (formed in pieces of the vocabulary, never stored whole),
+ *   lse[i]  = log sum_v exp(logits[i,v]),
+ *   loss[i] = lse[i] - logits[i, t_i] + z * lse[i]^2,
+ * with options, ignored rows, out-of-range targets and mean_loss as in
+ * qk_xent_fwd_ex; logits are not rounded to dtype.  (The article names
+ * cross-entropy on given logits; this is that operator taken together with
+ * the product in front of it, whose output is the largest array of a training
+ * step.)
+ *
+ *   h [M, K], w [V, K] dtype; targets [M] int64.
+ *   loss [M] float32; lse [M] float32 (may be NULL); mean_loss one float32
+ *   (may be NULL; NaN when no row counts, so also when M == 0).
+ *   workspace  at least qk_linear_xent_fwd_workspace_size() bytes of device
+ *              memory, 256-byte aligned, scratch.
+ *   M, V, K at most 2^31 - 1.  Products and sums are float32; float32 inputs
+ *   are multiplied as sums of bfloat16 parts whose error is below float32's.
+ *   A NaN or infinity in h or w makes the losses NaN or infinite; which of
+ *   the two is not specified for infinities.
+ *   The buffers must not overlap (h and w may be read by both).
+ */
+QK_API qk_status qk_linear_xent_fwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype,
+                                                   size_t* bytes);
+QK_API qk_status qk_linear_xent_fwd(const void* h, const void* w, const int64_t* targets, float* loss,
+                                    float* lse, float* mean_loss, void* workspace,
+                                    size_t workspace_bytes, int64_t M, int64_t V, int64_t K,
+                                    qk_dtype dtype, const qk_xent_options* options, void* stream);
+
+/*
+ * Backward of qk_linear_xent_fwd.  With
+ *   g[i,v] = dloss_i * ((1 + 2 z lse_i) * exp(logits[i,v] - lse_i) - [v == t_i])
+ * (zero on ignored rows, NaN where the target is out of range), formed again
+ * from h and w in pieces of the vocabulary:
+ *   dh[i,k] = sum_v g[i,v] w[v,k],   dw[v,k] = sum_i g[i,v] h[i,k].
+ *
+ *   lse    [M] float32 from qk_linear_xent_fwd; dloss [M] float32 or NULL for 1.
+ *   dh     [M, K] dtype, or NULL when not wanted.
+ *   dw     [V, K] dtype, or NULL when not wanted; zeros when M == 0.
+ *   workspace  at least qk_linear_xent_bwd_workspace_size() bytes, 256-byte
+ *              aligned, scratch.  It does not grow with M * V.
+ *   bfloat16: g / max |dloss| is rounded to bfloat16 for the two products;
+ *   their sums are float32 and the outputs are rounded once.  Results do not
+ *   change from run to run.
+ */
+QK_API qk_status qk_linear_xent_bwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype,
+                                                   size_t* bytes);
+QK_API qk_status qk_linear_xent_bwd(const void* h, const void* w, const int64_t* targets,
+                                    const float* lse, const float* dloss, void* dh, void* dw,
+                                    void* workspace, size_t workspace_bytes, int64_t M, int64_t V,
+                                    int64_t K, qk_dtype dtype, const qk_xent_options* options,
+                                    void* stream);
+
 /* Static English description of a status code; never NULL. */
 QK_API const char* qk_status_string(qk_status s);
 

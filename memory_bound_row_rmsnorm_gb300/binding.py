@@ -7,7 +7,9 @@ if the library is missing every call raises.
 
 The ``softmax_fwd`` / ``rmsnorm_fwd`` / ``layernorm_fwd`` / ``xent_fwd`` helpers take
 and return CUDA tensors (they allocate the outputs with PyTorch and then call
-the C entry points).
+the C entry points), and so do ``add_rmsnorm_fwd`` / ``add_rmsnorm_bwd`` /
+``rmsnorm_quant_fwd`` / ``linear_xent_fwd`` / ``linear_xent_bwd``, which allocate
+their workspaces too.
 """
 from __future__ import annotations
 
@@ -29,13 +31,17 @@ QK_ERR_MISALIGNED = 3
 QK_ERR_LAUNCH = 4
 QK_ERR_TIMEOUT = 5
 QK_ERR_NO_DEVICE = 6
+QK_E4M3, QK_INT8 = 0, 1
 
 _EXPORTS = (
     "qk_softmax_fwd", "qk_rmsnorm_fwd", "qk_xent_fwd", "qk_status_string",
     "qk_get_device_status", "qk_max_row_elements", "qk_get_plan",
     "qk_set_plan_override", "qk_test_wait_timeout", "qk_softmax_bwd", "qk_rmsnorm_bwd",
     "qk_rmsnorm_bwd_workspace_size", "qk_xent_bwd", "qk_rmsnorm_bwd_noalloc",
-    "qk_xent_fwd_ex", "qk_xent_bwd_ex", "qk_layernorm_fwd",
+    "qk_xent_fwd_ex", "qk_xent_bwd_ex", "qk_layernorm_fwd", "qk_add_rmsnorm_fwd",
+    "qk_add_rmsnorm_bwd", "qk_add_rmsnorm_bwd_workspace_size", "qk_rmsnorm_quant_fwd",
+    "qk_linear_xent_fwd", "qk_linear_xent_fwd_workspace_size", "qk_linear_xent_bwd",
+    "qk_linear_xent_bwd_workspace_size",
 )
 
 
@@ -99,11 +105,22 @@ def load_library(path: str = LIBRARY):
         lib.qk_xent_fwd_ex.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, op, vp]
         lib.qk_xent_bwd_ex.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, op, vp]
         lib.qk_layernorm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, ctypes.c_float, i32, vp]
+        sp, f32 = ctypes.POINTER(ctypes.c_size_t), ctypes.c_float
+        lib.qk_add_rmsnorm_fwd.argtypes = [vp] * 6 + [i64, i64, f32, i32, vp]
+        lib.qk_add_rmsnorm_bwd_workspace_size.argtypes = [i64, i64, i32, sp]
+        lib.qk_add_rmsnorm_bwd.argtypes = [vp] * 8 + [ctypes.c_size_t, i64, i64, i32, vp]
+        lib.qk_rmsnorm_quant_fwd.argtypes = [vp] * 7 + [i64, i64, f32, i64, i32, i32, vp]
+        lib.qk_linear_xent_fwd_workspace_size.argtypes = [i64, i64, i64, i32, sp]
+        lib.qk_linear_xent_fwd.argtypes = [vp] * 7 + [ctypes.c_size_t, i64, i64, i64, i32, op, vp]
+        lib.qk_linear_xent_bwd_workspace_size.argtypes = [i64, i64, i64, i32, sp]
+        lib.qk_linear_xent_bwd.argtypes = [vp] * 8 + [ctypes.c_size_t, i64, i64, i64, i32, op, vp]
         for name in ("qk_softmax_fwd", "qk_rmsnorm_fwd", "qk_xent_fwd", "qk_get_device_status",
                      "qk_get_plan", "qk_set_plan_override", "qk_test_wait_timeout",
                      "qk_softmax_bwd", "qk_rmsnorm_bwd_workspace_size", "qk_rmsnorm_bwd",
                      "qk_xent_bwd", "qk_rmsnorm_bwd_noalloc", "qk_xent_fwd_ex", "qk_xent_bwd_ex",
-                     "qk_layernorm_fwd"):
+                     "qk_layernorm_fwd", "qk_add_rmsnorm_fwd", "qk_add_rmsnorm_bwd_workspace_size",
+                     "qk_add_rmsnorm_bwd", "qk_rmsnorm_quant_fwd", "qk_linear_xent_fwd_workspace_size",
+                     "qk_linear_xent_fwd", "qk_linear_xent_bwd_workspace_size", "qk_linear_xent_bwd"):
             getattr(lib, name).restype = i32
         del fp
         _lib = lib
@@ -211,6 +228,65 @@ def qk_xent_bwd_ex(logits, targets, lse, dloss, dlogits, M: int, N: int, dtype: 
     _check(load_library().qk_xent_bwd_ex(_ptr(logits), _ptr(targets), _ptr(lse), _ptr(dloss),
                                          _ptr(dlogits), M, N, dtype, _options(ignore_index, z_loss),
                                          _stream(stream)), "qk_xent_bwd_ex")
+
+
+def qk_add_rmsnorm_fwd(x, residual, w, y, h, rstd, M: int, N: int, eps: float, dtype: int,
+                       stream=None) -> None:
+    _check(load_library().qk_add_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(y), _ptr(h),
+                                             _ptr(rstd), M, N, eps, dtype, _stream(stream)),
+           "qk_add_rmsnorm_fwd")
+
+
+def qk_add_rmsnorm_bwd_workspace_size(M: int, N: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().qk_add_rmsnorm_bwd_workspace_size(M, N, dtype, ctypes.byref(n)),
+           "qk_add_rmsnorm_bwd_workspace_size")
+    return n.value
+
+
+def qk_add_rmsnorm_bwd(h, w, rstd, dy, dh, dx, dw, workspace, workspace_bytes: int, M: int, N: int,
+                       dtype: int, stream=None) -> None:
+    _check(load_library().qk_add_rmsnorm_bwd(_ptr(h), _ptr(w), _ptr(rstd), _ptr(dy), _ptr(dh), _ptr(dx),
+                                             _ptr(dw), _ptr(workspace), int(workspace_bytes), M, N, dtype,
+                                             _stream(stream)), "qk_add_rmsnorm_bwd")
+
+
+def qk_rmsnorm_quant_fwd(x, residual, w, q, scale, h, rstd, M: int, N: int, eps: float, group: int,
+                         dtype: int, qtype: int, stream=None) -> None:
+    _check(load_library().qk_rmsnorm_quant_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(q), _ptr(scale),
+                                               _ptr(h), _ptr(rstd), M, N, eps, group, dtype, qtype,
+                                               _stream(stream)), "qk_rmsnorm_quant_fwd")
+
+
+def qk_linear_xent_fwd_workspace_size(M: int, V: int, K: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().qk_linear_xent_fwd_workspace_size(M, V, K, dtype, ctypes.byref(n)),
+           "qk_linear_xent_fwd_workspace_size")
+    return n.value
+
+
+def qk_linear_xent_fwd(h, w, targets, loss, lse, mean_loss, workspace, workspace_bytes: int, M: int,
+                       V: int, K: int, dtype: int, ignore_index=None, z_loss: float = 0.0,
+                       stream=None) -> None:
+    _check(load_library().qk_linear_xent_fwd(_ptr(h), _ptr(w), _ptr(targets), _ptr(loss), _ptr(lse),
+                                             _ptr(mean_loss), _ptr(workspace), int(workspace_bytes), M, V,
+                                             K, dtype, _options(ignore_index, z_loss), _stream(stream)),
+           "qk_linear_xent_fwd")
+
+
+def qk_linear_xent_bwd_workspace_size(M: int, V: int, K: int, dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().qk_linear_xent_bwd_workspace_size(M, V, K, dtype, ctypes.byref(n)),
+           "qk_linear_xent_bwd_workspace_size")
+    return n.value
+
+
+def qk_linear_xent_bwd(h, w, targets, lse, dloss, dh, dw, workspace, workspace_bytes: int, M: int, V: int,
+                       K: int, dtype: int, ignore_index=None, z_loss: float = 0.0, stream=None) -> None:
+    _check(load_library().qk_linear_xent_bwd(_ptr(h), _ptr(w), _ptr(targets), _ptr(lse), _ptr(dloss),
+                                             _ptr(dh), _ptr(dw), _ptr(workspace), int(workspace_bytes), M,
+                                             V, K, dtype, _options(ignore_index, z_loss), _stream(stream)),
+           "qk_linear_xent_bwd")
 
 
 def qk_status_string(status: int) -> str:
@@ -353,3 +429,165 @@ def xent_bwd(logits, targets, lse, dloss=None, ignore_index=None, z_loss: float 
     qk_xent_bwd_ex(logits, targets, lse, dloss, dx, M, N, _dtype_code(logits), ignore_index, z_loss,
                    stream)
     return dx
+
+
+def _like(name, t, ref, shape, dtype=None):
+    """t checked to be a contiguous tensor of that shape on ref's device (of ref's type, or dtype)."""
+    if t.dtype != (dtype or ref.dtype) or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype or ref.dtype} tensor of shape {tuple(shape)}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+    return t
+
+
+def _on_current_device(t):
+    """The C entry points launch on the current device: refuse a tensor of another one."""
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _workspace(nbytes: int, ref, stream):
+    """Scratch memory for one call.  When the call goes to a stream other than
+    the one that torch allocates on, the allocator is told that this stream uses
+    the block, so that it is not handed out again before the kernels are done."""
+    import torch
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=ref.device)
+    return _used_on(stream, ws)
+
+
+def _used_on(stream, *tensors):
+    import torch
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+    return tensors[0] if len(tensors) == 1 else tensors
+
+
+def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, want_rstd: bool = True,
+                    stream=None):
+    """h = x + residual and its RMSNorm over the last dimension; returns
+    (y, h, rstd) (rstd is None if not wanted).  out and out_h may be x or
+    residual (out_h=residual keeps the residual stream in place)."""
+    import torch
+    M, N = _rows(x)
+    code = _dtype_code(x)
+    _on_current_device(x)
+    _like("residual", residual, x, x.shape)
+    _like("w", w, x, (N,))
+    y = torch.empty_like(x) if out is None else _like("out", out, x, x.shape)
+    h = torch.empty_like(x) if out_h is None else _like("out_h", out_h, x, x.shape)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
+    qk_add_rmsnorm_fwd(x, residual, w, y, h, rstd, M, N, eps, code, stream)
+    _used_on(stream, y, h, rstd)
+    return y, h, rstd
+
+
+def add_rmsnorm_bwd(h, w, rstd, dy, dh=None, out=None, stream=None):
+    """Backward of add_rmsnorm_fwd; returns (dx, dw): dx is the gradient of x
+    and of residual alike, dw is float32.  dh is the gradient that reaches h by
+    the residual stream (None: none).  out may be h, dy or dh."""
+    import torch
+    M, N = _rows(h)
+    code = _dtype_code(h)
+    _on_current_device(h)
+    _like("w", w, h, (N,))
+    _like("rstd", rstd, h, h.shape[:-1], torch.float32)
+    _like("dy", dy, h, h.shape)
+    if dh is not None:
+        _like("dh", dh, h, h.shape)
+    dx = torch.empty_like(h) if out is None else _like("out", out, h, h.shape)
+    dw = torch.empty(N, dtype=torch.float32, device=h.device)
+    nbytes = qk_add_rmsnorm_bwd_workspace_size(M, N, code)
+    ws = _workspace(nbytes, h, stream)
+    qk_add_rmsnorm_bwd(h, w, rstd, dy, dh, dx, dw, ws, nbytes, M, N, code, stream)
+    _used_on(stream, dx, dw)
+    return dx, dw
+
+
+def rmsnorm_quant_fwd(x, w, residual=None, eps: float = 1e-6, group: int = 0, qdtype=None, out_h=None,
+                      want_h: bool = True, want_rstd: bool = True, stream=None):
+    """RMSNorm over the last dimension (of x, or of h = x + residual) with an
+    output in 8 bits; returns (q, scale, h, rstd).  q is a qdtype tensor
+    (torch.float8_e4m3fn by default, or torch.int8) that stands for
+    q * scale; scale has one float32 a row (group 0) or one for each group of
+    32, 64 or 128 columns.  h is None without a residual or if not wanted."""
+    import torch
+    M, N = _rows(x)
+    code = _dtype_code(x)
+    _on_current_device(x)
+    qdtype = qdtype or torch.float8_e4m3fn
+    if qdtype not in (torch.float8_e4m3fn, torch.int8):
+        raise TypeError(f"unsupported qdtype {qdtype}: torch.float8_e4m3fn or torch.int8 expected")
+    if group not in (0, 32, 64, 128):
+        raise ValueError("group must be 0 (the whole row), 32, 64 or 128")
+    _like("w", w, x, (N,))
+    h = None
+    if residual is not None:
+        _like("residual", residual, x, x.shape)
+        if want_h:
+            h = torch.empty_like(x) if out_h is None else _like("out_h", out_h, x, x.shape)
+    elif out_h is not None:
+        raise ValueError("out_h needs a residual")
+    q = torch.empty(x.shape, dtype=qdtype, device=x.device)
+    groups = -(-N // group) if group else 1
+    scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
+    qk_rmsnorm_quant_fwd(x, residual, w, q, scale, h, rstd, M, N, eps, group, code,
+                         QK_INT8 if qdtype == torch.int8 else QK_E4M3, stream)
+    _used_on(stream, q, scale, h, rstd)
+    return q, scale, h, rstd
+
+
+def _linear_xent_sizes(h, w, targets):
+    import torch
+    M, K = _rows(h)
+    _on_current_device(h)
+    if w.dim() != 2:
+        raise ValueError("w must have two dimensions, [vocabulary, hidden]")
+    _like("w", w, h, (w.shape[0], K))
+    _like("targets", targets, h, h.shape[:-1], torch.int64)
+    return M, w.shape[0], K
+
+
+def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_loss: float = 0.0,
+                    want_mean: bool = False, stream=None):
+    """Per-row cross-entropy of the logits h @ w.T, which are never stored;
+    returns (loss, lse) (lse is None if not wanted), or (loss, lse, mean) with
+    want_mean.  Options as in xent_fwd."""
+    import torch
+    M, V, K = _linear_xent_sizes(h, w, targets)
+    code = _dtype_code(h)
+    loss = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
+    lse = torch.empty_like(loss) if want_lse else None
+    mean = torch.empty((), dtype=torch.float32, device=h.device) if want_mean else None
+    nbytes = qk_linear_xent_fwd_workspace_size(M, V, K, code)
+    ws = _workspace(nbytes, h, stream)
+    qk_linear_xent_fwd(h, w, targets, loss, lse, mean, ws, nbytes, M, V, K, code, ignore_index, z_loss, stream)
+    _used_on(stream, loss, lse, mean)
+    return (loss, lse, mean) if want_mean else (loss, lse)
+
+
+def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: float = 0.0,
+                    want_dh: bool = True, want_dw: bool = True, stream=None):
+    """Backward of linear_xent_fwd; returns (dh, dw) (None if not wanted).
+    dloss is the float32 gradient of each row's loss (None: 1)."""
+    import torch
+    M, V, K = _linear_xent_sizes(h, w, targets)
+    code = _dtype_code(h)
+    _like("lse", lse, h, h.shape[:-1], torch.float32)
+    if dloss is not None:
+        _like("dloss", dloss, h, h.shape[:-1], torch.float32)
+    dh = torch.empty_like(h) if want_dh else None
+    dw = torch.empty_like(w) if want_dw else None
+    nbytes = qk_linear_xent_bwd_workspace_size(M, V, K, code)
+    ws = _workspace(nbytes, h, stream)
+    qk_linear_xent_bwd(h, w, targets, lse, dloss, dh, dw, ws, nbytes, M, V, K, code, ignore_index, z_loss,
+                       stream)
+    _used_on(stream, dh, dw)
+    return dh, dw

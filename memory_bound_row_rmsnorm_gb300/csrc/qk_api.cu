@@ -19,6 +19,7 @@
 #include "../../include/qk.h"
 #include "qk_bwd_kernels.cuh"
 #include "qk_device.cuh"
+#include "qk_host.h"
 #include "qk_internal.h"
 
 namespace qk {
@@ -38,7 +39,6 @@ __global__ void wait_timeout_kernel(uint64_t timeout_ns, int* status) {
 
 namespace {
 
-constexpr uint64_t kWaitTimeoutNs = 1000000000ull;  // 1 s bound on any in-kernel wait
 constexpr int kMaxDevices = 64;
 constexpr int kRingMaxVectorsPerCta = 4096;  // 256 threads x 16 vectors, or 512 x 8
 constexpr int64_t kMaxRowBytes = int64_t(kMaxCluster) * kRingMaxVectorsPerCta * 16;  // 1 MiB
@@ -207,8 +207,6 @@ qk_status occupancy(int dev, const KernelEntry& k, int smem, int cluster, int* o
   *out = n;
   return QK_OK;
 }
-
-int elem_size(int dt) { return dt == QK_F32 ? 4 : 2; }
 
 int next_pow2(int64_t v) {
   int p = 1;
@@ -853,22 +851,12 @@ qk_status launch(const Plan& p, void* args, void* stream) {
 // direct kernel (everything else, and shifted rows beyond its capacity).
 enum RowPath : int { kPathDirect = 0, kPathRing = 1, kPathShifted = 2 };
 
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 bool same_mod16(const void* a, const void* b) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15u) == 0;
 }
 int row_path(bool fast, bool same_alignment) {
   return fast ? kPathRing : same_alignment ? kPathShifted : kPathDirect;
 }
-bool aligned_to(const void* ptr, size_t n) { return (reinterpret_cast<uintptr_t>(ptr) % n) == 0; }
-
-// [a, a+na) and [b, b+nb) share a byte.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + uintptr_t(nb) && pb < pa + uintptr_t(na);
-}
-
 qk_status check_sizes(int op, int dt, int64_t M, int64_t N) {
   if (dt != QK_F32 && dt != QK_BF16) return QK_ERR_INVALID_ARG;
   if (M < 0 || N <= 0) return QK_ERR_INVALID_ARG;
@@ -1030,6 +1018,17 @@ qk_status run_bwd(int op, int dt, BwdArgs a, float* dw, size_t workspace_bytes, 
 }
 
 }  // namespace
+
+qk_status current_device(CurrentDevice* out) {
+  DeviceInfo* d;
+  const qk_status st = device_info(&out->index, &d);
+  if (st != QK_OK) return st;
+  out->sms = d->sms;
+  out->smem_optin = d->smem_optin;
+  out->status = d->status;
+  return QK_OK;
+}
+
 }  // namespace qk
 
 using namespace qk;
