@@ -4,128 +4,85 @@
 //   logits = h w^T;  lse = log sum exp(logits);  loss = lse - logits[t] + z lse^2
 //   g = dloss ((1 + 2 z lse) exp(logits - lse) - onehot(t));  dh = g w;  dw = g^T h
 //
-// The vocabulary is walked in pieces: a piece's logits (fp32) are formed in the
-// workspace, folded into each row's running (maximum, sum) pair or turned into
-// g, and overwritten by the next piece's.
+// Forward: one product whose epilogue folds each 256-column tile of a row into
+// a (maximum, sum of exponentials) pair, then a join of the pairs of a row.
+// Backward, for one piece of the vocabulary after the other: a product whose
+// epilogue turns logits into g (bf16, in the workspace), dh += g w[piece] in
+// fp32, and dw[piece] = g^T h, complete at once.  A piece is as wide as keeps
+// its g within kPieceBytes, so the workspace does not grow with the vocabulary.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/qk.h"
 #include "qk_host.h"
 #include "qk_kernels.cuh"  // xent_mean_kernel
+#include "qk_product_kernel.cuh"
 
 namespace qk {
 namespace {
 
 constexpr int64_t kMaxDim = INT32_MAX;
-constexpr int64_t kPieceBytes = int64_t(256) << 20;  // a piece's logits in the workspace
+constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece
+constexpr int64_t kStageCopyBytes = int64_t(64) << 20;  // copied or split weights of one piece
+constexpr int kPairs = 76;  // CTA pairs of a GB300; only the number of k splits follows it
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-struct XentRow {  // what an epilogue needs of a row
-  float lse, g, zf;
-  int32_t target;  // -1: none
-};
+int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
 // ---------------------------------------------------------------------------
-// C[i,j] (+)= sum_k A(i,k) B(j,k) in fp32: 64 x 64 tiles, 16 of k at a time in
-// shared memory, 4 x 4 results a thread.  Element (i,k) of A is at
-// i * a_row + k * a_col, of B at j * b_row + k * b_col.
+// Small kernels around the products
 // ---------------------------------------------------------------------------
-struct ProductArgs {
-  const void* a;
-  const void* b;
-  void* c;
-  int64_t a_row, a_col, b_row, b_col, c_row;
-  int64_t rows, cols, depth;
-  int32_t add;        // add to C
-  const float* scale; // factor on the result (device), may be null
-};
 
-template <typename TA, typename TB, typename TC>
-__global__ void __launch_bounds__(256) product_kernel(const ProductArgs p) {
-  __shared__ float as[16][65], bs[16][65];
+// Rows of T into rows of bf16 planes whose row length is a multiple of 8 (what
+// TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.
+template <typename T>
+__global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, int64_t cols, __nv_bfloat16* out,
+                                                     int64_t ld, int64_t plane_stride) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t i0 = int64_t(blockIdx.y) * 64, j0 = int64_t(blockIdx.x) * 64;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.depth; k0 += 16) {
-    for (int e = tid; e < 64 * 16; e += 256) {
-      const int kk = e & 15, rr = e >> 4;
-      const int64_t k = k0 + kk;
-      as[kk][rr] = i0 + rr < p.rows && k < p.depth
-                       ? Vec16<TA>::load1(static_cast<const TA*>(p.a) + (i0 + rr) * p.a_row + k * p.a_col) : 0.f;
-      bs[kk][rr] = j0 + rr < p.cols && k < p.depth
-                       ? Vec16<TB>::load1(static_cast<const TB*>(p.b) + (j0 + rr) * p.b_row + k * p.b_col) : 0.f;
+  for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < rows * cols; e += int64_t(gridDim.x) * 256) {
+    const int64_t i = e / cols, j = e % cols;
+    if constexpr (sizeof(T) == 2) {
+      out[i * ld + j] = in[e];
+    } else {
+      __nv_bfloat16 b[3];
+      split3(in[e], b);
+      for (int pl = 0; pl < 3; ++pl) out[pl * plane_stride + i * ld + j] = b[pl];
     }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(as[kk][ty + 16 * u], bs[kk][tx + 16 * v], acc[u][v]);
-    __syncthreads();
   }
-  const float f = p.scale != nullptr ? *p.scale : 1.f;
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i >= p.rows || j >= p.cols) continue;
-      TC* c = static_cast<TC*>(p.c) + i * p.c_row + j;
-      const float r = acc[u][v] * f;
-      Vec16<TC>::store1(c, p.add ? Vec16<TC>::load1(c) + r : r);
-    }
 }
 
-template <typename TA, typename TB, typename TC>
-qk_status product(const ProductArgs& p, void* stream) {
-  const dim3 grid(unsigned((p.cols + 63) / 64), unsigned((p.rows + 63) / 64));
-  return launch_pdl(product_kernel<TA, TB, TC>, grid, 256, 0, stream, p);
-}
-
-// Folds a piece's logits into each row's (maximum, sum) pair; one CTA a row.
-__global__ void __launch_bounds__(256) fold_kernel(const float* logits, int64_t ld, int64_t v0, int64_t width,
-                                                   const int64_t* targets, float2* state, float* at_target) {
-  __shared__ float2 red[8];
+// Joins a row's pairs, one for each column tile: lanes are rows, the CTA's
+// warps take every eighth tile, in a fixed order.
+__global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t part_ld, int64_t n_tiles,
+                                                   const float* at_target, const int64_t* targets, int64_t M,
+                                                   int64_t V, int has_ignore, int64_t ignore_index, float z,
+                                                   float* loss, float* lse) {
+  __shared__ float2 red[8][33];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t row = blockIdx.x;
-  const float* x = logits + row * ld;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = int64_t(blockIdx.x) * 32 + lane;
   float m = kNegInf, s = 0.f;
-  for (int64_t j = threadIdx.x; j < width; j += 256) m = fmaxf(m, x[j]);
-  for (int64_t j = threadIdx.x; j < width; j += 256)
-    if (x[j] != kNegInf) s += exp2_approx((x[j] - m) * kLog2e);
-  group_ms<32>(m, s);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(m, s);
+  auto fold = [&](float2 b) {  // an empty (-inf) side adds its sum, 0 or NaN
+    const float mn = fmaxf(m, b.x);
+    s = (m == kNegInf ? s : s * exp2_approx((m - mn) * kLog2e)) +
+        (b.x == kNegInf ? b.y : b.y * exp2_approx((b.x - mn) * kLog2e));
+    m = mn;
+  };
+  if (row < M)
+    for (int64_t t = warp; t < n_tiles; t += 8) fold(part[t * part_ld + row]);
+  red[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  float2 t = v0 > 0 ? state[row] : make_float2(kNegInf, 0.f);
-  for (int i = 0; i < 8; ++i) {
-    const float mn = fmaxf(t.x, red[i].x);
-    t.y = (t.x == kNegInf ? t.y : t.y * exp2_approx((t.x - mn) * kLog2e)) +
-          (red[i].x == kNegInf ? red[i].y : red[i].y * exp2_approx((red[i].x - mn) * kLog2e));
-    t.x = mn;
-  }
-  state[row] = t;
-  const int64_t c = targets[row] - v0;
-  if (c >= 0 && c < width) at_target[row] = x[c];
-}
-
-__global__ void __launch_bounds__(256) loss_kernel(const float2* state, const float* at_target,
-                                                   const int64_t* targets, int64_t M, int64_t V, int has_ignore,
-                                                   int64_t ignore_index, float z, float* loss, float* lse) {
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int64_t row = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (row >= M) return;
-  const float l = state[row].x + logf(state[row].y);
+  if (warp != 0 || row >= M) return;
+  m = kNegInf, s = 0.f;
+  for (int i = 0; i < 8; ++i) fold(red[i][lane]);
+  const float l = m + logf(s);
   const int64_t t = targets[row];
   if (lse != nullptr) lse[row] = l;
   loss[row] = has_ignore && t == ignore_index ? 0.f
@@ -133,49 +90,112 @@ __global__ void __launch_bounds__(256) loss_kernel(const float2* state, const fl
                                               : __int_as_float(0x7fc00000);
 }
 
-// A piece's logits into its g, in place.
-__global__ void __launch_bounds__(256) grad_kernel(float* logits, int64_t ld, int64_t v0, int64_t width, int64_t V,
-                                                   const int64_t* targets, const float* lse, const float* dloss,
-                                                   int has_ignore, int64_t ignore_index, float z) {
+// What the gradient needs of each row.  g is dloss over the largest |dloss| of
+// the rows that count, which `scale` keeps for the outputs: the mean's constant
+// gradient then is 1, and g's bf16 rounding does not see its size.  One CTA.
+__global__ void __launch_bounds__(1024) rows_kernel(const int64_t* targets, const float* lse, const float* dloss,
+                                                    int64_t M, int64_t V, int has_ignore, int64_t ignore_index,
+                                                    float z, XentRow* row, float* scale) {
+  __shared__ float red[32];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t row = blockIdx.x;
-  float* x = logits + row * ld;
-  const int64_t t = targets[row];
-  const bool ignored = has_ignore && t == ignore_index;
-  const float l = lse[row], zf = fmaf(2.f * z, l, 1.f);
-  const float g = t >= 0 && t < V ? (dloss != nullptr ? dloss[row] : 1.f) : __int_as_float(0x7fc00000);
-  for (int64_t j = threadIdx.x; j < width; j += 256) {
-    const float p = exp2_approx((x[j] - l) * kLog2e) * zf - (v0 + j == t ? 1.f : 0.f);
-    x[j] = ignored ? 0.f : g * p;
+  auto ignored = [&](int64_t t) { return has_ignore && t == ignore_index; };
+  float c = 1.f;
+  if (dloss != nullptr) {
+    c = 0.f;
+    for (int64_t i = threadIdx.x; i < M; i += 1024)
+      if (!ignored(targets[i])) c = fmaxf(c, fabsf(dloss[i]));
+    c = group_max<32>(c);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = group_max<32>(red[threadIdx.x & 31]);
+    if (!(c > 0.f && c < __int_as_float(0x7f800000))) c = 1.f;
+  }
+  if (threadIdx.x == 0) *scale = c;
+  for (int64_t i = threadIdx.x; i < M; i += 1024) {
+    const int64_t t = targets[i];
+    const bool ok = t >= 0 && t < V;
+    XentRow r;
+    r.lse = lse[i];
+    r.g = !ok ? __int_as_float(0x7fc00000) : dloss != nullptr ? dloss[i] / c : 1.f;
+    r.zf = fmaf(2.f * z, r.lse, 1.f);
+    r.target = ignored(t) ? -2 : ok ? int32_t(t) : -1;
+    row[i] = r;
   }
 }
 
+// dh from its fp32 sums: the splits in order, times the scale, rounded once.
 template <typename T>
-__global__ void __launch_bounds__(256) round_kernel(const float* in, T* out, int64_t n) {
+__global__ void __launch_bounds__(256) finish_kernel(const float* sum, int64_t ld, int64_t split_stride, int splits,
+                                                     const float* scale, T* out, int64_t rows, int64_t cols) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) Vec16<T>::store1(out + i, in[i]);
+  const float f = *scale;
+  for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < rows * cols; e += int64_t(gridDim.x) * 256) {
+    const float* s = sum + e / cols * ld + e % cols;
+    float v = s[0];
+    for (int k = 1; k < splits; ++k) v += s[k * split_stride];
+    Vec16<T>::store1(out + e, v * f);
+  }
 }
 
+// ---------------------------------------------------------------------------
+// Plans: pieces, splits, workspace
+// ---------------------------------------------------------------------------
 struct Layout {
-  int64_t piece;  // vocabulary rows of one piece
-  int64_t logits, state, at_target, dh, total;  // byte offsets
+  int planes;
+  int64_t kp;          // row length of copied operands and of dh's sums
+  int64_t piece;       // vocabulary rows of one piece, a multiple of 256 unless it is all
+  int64_t ld_g;        // row length of g
+  int splits, split_steps;  // k splits of dh's product
+  // byte offsets
+  int64_t h, w, part, at_target, row, scale, g, sum, total;
 };
-Layout layout(int64_t M, int64_t V, int64_t K) {
-  Layout l;
-  l.piece = std::min(V, std::max<int64_t>(64, kPieceBytes / 4 / M / 64 * 64));
+
+// Pieces of at most `most` vocabulary rows, of even widths.
+int64_t even_piece(int64_t V, int64_t most) {
+  most = std::max<int64_t>(256, most / 256 * 256);
+  const int64_t n = ceil_div(V, most);
+  return n == 1 ? V : round_up(ceil_div(V, n), 256);
+}
+
+// `copied`: h and w go through the workspace (float32, or rows that TMA cannot read in place).
+Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied) {
+  Layout l = {};
+  l.planes = dtype == QK_F32 ? 3 : 1;
+  l.kp = round_up(K, 8);
+  int64_t most = round_up(V, 256);
+  if (copied) most = std::min<int64_t>(most, kStageCopyBytes / (l.kp * 2 * l.planes));
+  if (bwd) most = std::min<int64_t>(most, kPieceBytes / (M * 2 * l.planes));
+  l.piece = even_piece(V, most);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
     at += round_up(bytes, 256);
     return o;
   };
-  l.logits = take(M * l.piece * 4);
-  l.state = take(M * 8);
-  l.at_target = take(M * 4);
-  l.dh = take(M * K * 4);
+  if (copied) {
+    l.h = take(l.planes * M * l.kp * 2);
+    l.w = take(l.planes * l.piece * l.kp * 2);
+  }
+  if (!bwd) {
+    l.part = take(ceil_div(V, kTileN) * M * 8);
+    l.at_target = take(M * 4);
+  } else {
+    l.row = take(M * int64_t(sizeof(XentRow)));
+    l.scale = take(4);
+    l.ld_g = round_up(l.piece, 8);
+    l.g = take(l.planes * M * l.ld_g * 2);
+    // dh's product sums over the vocabulary: with few tiles (few rows, or a
+    // narrow model) the axis is split, each split with its own fp32 sums, until
+    // every pair of CTAs has work; a split keeps at least 16 steps of 64.
+    const int64_t tiles = ceil_div(M, kTileM) * ceil_div(K, kTileN);
+    const int64_t steps = ceil_div(l.piece, kStepK) * (l.planes == 3 ? 6 : 1);
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kPairs / std::min<int64_t>(tiles, kPairs), steps / 16));
+    l.split_steps = int(ceil_div(steps, splits));
+    l.splits = int(ceil_div(steps, l.split_steps));
+    l.sum = take(int64_t(l.splits) * M * l.kp * 4);
+  }
   l.total = at;
   return l;
 }
@@ -197,64 +217,193 @@ struct Call {
   float z;
   char* ws;
   void* stream;
+  CurrentDevice dev;
 };
 
+// ---------------------------------------------------------------------------
+// Tensor maps and launches
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A bf16 operand [planes][rows][ld] of which the first `inner` columns count.
+struct Operand {
+  const void* base;
+  int64_t inner, rows, ld, planes, plane_stride;  // elements
+};
+
+// Boxes of 64 x box_rows in 128-byte swizzle; what lies outside reads as zero.
+bool make_map(CUtensorMap* map, const Operand& o, int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(o.inner), cuuint64_t(o.rows), cuuint64_t(o.planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(o.ld) * 2, cuuint64_t(o.planes > 1 ? o.plane_stride : o.ld * o.rows) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// C [rows, cols] = A B^T over `depth`; the epilogue's fields of p are set by the caller.
+template <int EPI, bool A_MN, bool B_MN, typename T>
+qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const Operand& b, int64_t rows,
+                         int64_t cols, int64_t depth, int splits, int split_steps) {
+  const auto kernel = product_kernel<EPI, A_MN, B_MN, T>;
+  static std::atomic<uint64_t> prepared{0};  // one bit a device
+  const uint64_t bit = uint64_t(1) << (c.dev.index & 63);
+  if (!(prepared.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return QK_ERR_LAUNCH;
+    }
+    prepared.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  p.rows = int32_t(rows);
+  p.cols = int32_t(cols);
+  p.bn = kTileN;
+  p.planes = int32_t(a.planes);
+  p.steps = int32_t(ceil_div(depth, kStepK));
+  p.m_tiles = int32_t(ceil_div(rows, kTileM));
+  p.n_tiles = int32_t(ceil_div(cols, p.bn));
+  const int64_t total = int64_t(p.steps) * (p.planes == 3 ? 6 : 1);
+  if (total > INT32_MAX) return QK_ERR_UNSUPPORTED;
+  p.split_steps = splits == 1 ? int32_t(total) : split_steps;
+  p.splits = int32_t(ceil_div(total, p.split_steps));
+  p.timeout_ns = kWaitTimeoutNs;
+  p.status = c.dev.status;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, a, A_MN ? kStepK : 128) || !make_map(&mb, b, B_MN ? kStepK : p.bn / 2)) return QK_ERR_LAUNCH;
+  const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles * p.splits;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(tiles, c.dev.sms / 2)), 1, 1);
+  cfg.blockDim = dim3(kProductThreads, 1, 1);
+  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.stream = static_cast<cudaStream_t>(c.stream);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, p) != cudaSuccess) {
+    cudaGetLastError();
+    return QK_ERR_LAUNCH;
+  }
+  return QK_OK;
+}
+
+unsigned blocks(const Call& c, int64_t n) { return unsigned(std::min<int64_t>(ceil_div(n, 256), 32 * c.dev.sms)); }
+
+// Rows that TMA reads where they are: bf16, 16-byte aligned.
+bool in_place(const void* h, const void* w, int64_t K, int dtype) {
+  return dtype == QK_BF16 && K % 8 == 0 && aligned16(h) && aligned16(w);
+}
+
+// `rows` rows of h or w as an operand, by way of the workspace at `at` if `copied`.
 template <typename T>
-qk_status logits_piece(const Call& c, const Layout& l, int64_t v0, int64_t width) {
+qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int64_t rows, char* at, Operand* o) {
+  *o = {src, c.K, rows, c.K, 1, 0};
+  if (!copied) return QK_OK;
+  *o = {at, c.K, rows, l.kp, l.planes, rows * l.kp};
+  return launch_pdl(planes_kernel<T>, dim3(blocks(c, rows * c.K)), 256, 0, c.stream, src, rows, c.K,
+                    reinterpret_cast<__nv_bfloat16*>(at), l.kp, rows * l.kp);
+}
+
+template <typename T>
+qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
+  const bool copied = !in_place(c.h, c.w, c.K, dtype);
+  const Layout l = layout(false, c.M, c.V, c.K, dtype, copied);
+  Operand h, w;
+  qk_status st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
   ProductArgs p = {};
-  p.a = c.h, p.a_row = c.K, p.a_col = 1;
-  p.b = static_cast<const T*>(c.w) + v0 * c.K, p.b_row = c.K, p.b_col = 1;
-  p.c = c.ws + l.logits, p.c_row = l.piece;
-  p.rows = c.M, p.cols = width, p.depth = c.K;
-  return product<T, T, float>(p, c.stream);
-}
-
-template <typename T>
-qk_status forward(const Call& c, float* loss, float* lse) {
-  const Layout l = layout(c.M, c.V, c.K);
-  float2* state = reinterpret_cast<float2*>(c.ws + l.state);
-  float* at = reinterpret_cast<float*>(c.ws + l.at_target);
-  for (int64_t v0 = 0; v0 < c.V; v0 += l.piece) {
-    const int64_t width = std::min(l.piece, c.V - v0);
-    qk_status st = logits_piece<T>(c, l, v0, width);
+  p.targets = c.targets;
+  p.part = reinterpret_cast<float2*>(c.ws + l.part);
+  p.part_ld = c.M;
+  p.at_target = reinterpret_cast<float*>(c.ws + l.at_target);
+  for (p.v0 = 0; p.v0 < c.V && st == QK_OK; p.v0 += l.piece) {
+    const int64_t width = std::min(l.piece, c.V - p.v0);
+    st = operand(c, l, copied, static_cast<const T*>(c.w) + p.v0 * c.K, width, c.ws + l.w, &w);
     if (st == QK_OK)
-      st = launch_pdl(fold_kernel, dim3(unsigned(c.M)), 256, 0, c.stream,
-                      reinterpret_cast<const float*>(c.ws + l.logits), l.piece, v0, width, c.targets, state, at);
-    if (st != QK_OK) return st;
+      st = launch_product<kEpiLse, false, false, __nv_bfloat16>(c, p, h, w, c.M, width, c.K, 1, 0);
   }
-  return launch_pdl(loss_kernel, dim3(unsigned((c.M + 255) / 256)), 256, 0, c.stream, state, at, c.targets, c.M,
-                    c.V, c.has_ignore, c.ignore, c.z, loss, lse);
+  if (st != QK_OK) return st;
+  return launch_pdl(join_kernel, dim3(unsigned(ceil_div(c.M, 32))), 256, 0, c.stream, p.part, p.part_ld,
+                    ceil_div(c.V, kTileN), p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
 }
 
 template <typename T>
-qk_status backward(const Call& c, const float* lse, const float* dloss, void* dh, void* dw) {
-  const Layout l = layout(c.M, c.V, c.K);
-  float* g = reinterpret_cast<float*>(c.ws + l.logits);
-  float* sum = reinterpret_cast<float*>(c.ws + l.dh);
-  for (int64_t v0 = 0; v0 < c.V; v0 += l.piece) {
+qk_status backward(const Call& c, int dtype, const float* lse, const float* dloss, void* dh, void* dw) {
+  const bool copied = !in_place(c.h, c.w, c.K, dtype);
+  const Layout l = layout(true, c.M, c.V, c.K, dtype, copied);
+  XentRow* row = reinterpret_cast<XentRow*>(c.ws + l.row);
+  float* scale = reinterpret_cast<float*>(c.ws + l.scale);
+  float* sum = reinterpret_cast<float*>(c.ws + l.sum);
+  const bool direct = l.piece >= c.V && l.splits == 1;  // dh is complete in one product
+  Operand h, w;
+  qk_status st = launch_pdl(rows_kernel, dim3(1), 1024, 0, c.stream, c.targets, lse, dloss, c.M, c.V, c.has_ignore,
+                            c.ignore, c.z, row, scale);
+  if (st == QK_OK) st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
+  for (int64_t v0 = 0; v0 < c.V && st == QK_OK; v0 += l.piece) {
     const int64_t width = std::min(l.piece, c.V - v0);
-    qk_status st = logits_piece<T>(c, l, v0, width);
-    if (st == QK_OK)
-      st = launch_pdl(grad_kernel, dim3(unsigned(c.M)), 256, 0, c.stream, g, l.piece, v0, width, c.V, c.targets,
-                      lse, dloss, c.has_ignore, c.ignore, c.z);
+    st = operand(c, l, copied, static_cast<const T*>(c.w) + v0 * c.K, width, c.ws + l.w, &w);
     ProductArgs p = {};
-    p.a = g, p.a_row = l.piece, p.a_col = 1;
-    p.b = static_cast<const T*>(c.w) + v0 * c.K, p.b_row = 1, p.b_col = c.K;
-    p.c = sum, p.c_row = c.K;
-    p.rows = c.M, p.cols = c.K, p.depth = width;
-    p.add = v0 > 0;
-    if (st == QK_OK && dh != nullptr) st = product<float, T, float>(p, c.stream);
-    p.a_row = 1, p.a_col = l.piece;
-    p.b = c.h;
-    p.c = static_cast<T*>(dw) + v0 * c.K;
-    p.rows = width, p.depth = c.M;
-    p.add = 0;
-    if (st == QK_OK && dw != nullptr) st = product<float, T, T>(p, c.stream);
-    if (st != QK_OK) return st;
+    p.v0 = v0;
+    p.row = row;
+    p.out = c.ws + l.g;
+    p.ld = l.ld_g;
+    p.plane_stride = c.M * l.ld_g;
+    if (st == QK_OK) st = launch_product<kEpiGrad, false, false, T>(c, p, h, w, c.M, width, c.K, 1, 0);
+    const Operand g = {c.ws + l.g, width, c.M, l.ld_g, l.planes, c.M * l.ld_g};
+    p = ProductArgs{};
+    p.scale = scale;
+    if (st == QK_OK && dh != nullptr) {
+      p.out = direct ? dh : sum;
+      p.ld = direct ? c.K : l.kp;
+      p.vec = aligned16(dh) && c.K * int64_t(sizeof(T)) % 16 == 0;
+      p.first = v0 == 0;
+      st = direct ? launch_product<kEpiStore, false, true, T>(c, p, g, w, c.M, c.K, width, 1, 0)
+                  : launch_product<kEpiAccum, false, true, float>(c, p, g, w, c.M, c.K, width, l.splits, l.split_steps);
+    }
+    if (st == QK_OK && dw != nullptr) {
+      p.out = static_cast<T*>(dw) + v0 * c.K;
+      p.ld = c.K;
+      p.vec = aligned16(dw) && c.K * int64_t(sizeof(T)) % 16 == 0;
+      st = launch_product<kEpiStore, true, true, T>(c, p, g, h, width, c.K, c.M, 1, 0);
+    }
   }
-  if (dh == nullptr) return QK_OK;
-  return launch_pdl(round_kernel<T>, dim3(unsigned((c.M * c.K + 255) / 256)), 256, 0, c.stream,
-                    reinterpret_cast<const float*>(sum), static_cast<T*>(dh), c.M * c.K);
+  if (st != QK_OK || dh == nullptr || direct) return st;
+  return launch_pdl(finish_kernel<T>, dim3(blocks(c, c.M * c.K)), 256, 0, c.stream, sum, l.kp, c.M * l.kp, l.splits,
+                    scale, static_cast<T*>(dh), c.M, c.K);
+}
+
+// Bytes that these sizes may need, whichever way the pointers are aligned.
+qk_status workspace_size(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, size_t* bytes) {
+  if (bytes == nullptr) return QK_ERR_INVALID_ARG;
+  *bytes = 0;
+  const qk_status st = check_linear(dtype, M, V, K);
+  if (st != QK_OK || M == 0) return st;
+  *bytes = size_t(layout(bwd, M, V, K, dtype, true).total);
+  if (dtype == QK_BF16) *bytes = std::max(*bytes, size_t(layout(bwd, M, V, K, dtype, false).total));
+  return QK_OK;
 }
 
 }  // namespace
@@ -265,16 +414,11 @@ using namespace qk;
 extern "C" {
 
 qk_status qk_linear_xent_fwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype, size_t* bytes) {
-  if (bytes == nullptr) return QK_ERR_INVALID_ARG;
-  *bytes = 0;
-  const qk_status st = check_linear(dtype, M, V, K);
-  if (st != QK_OK || M == 0) return st;
-  *bytes = size_t(layout(M, V, K).total);
-  return QK_OK;
+  return workspace_size(false, M, V, K, dtype, bytes);
 }
 
 qk_status qk_linear_xent_bwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype, size_t* bytes) {
-  return qk_linear_xent_fwd_workspace_size(M, V, K, dtype, bytes);
+  return workspace_size(true, M, V, K, dtype, bytes);
 }
 
 qk_status qk_linear_xent_fwd(const void* h, const void* w, const int64_t* targets, float* loss, float* lse,
@@ -313,8 +457,8 @@ qk_status qk_linear_xent_fwd(const void* h, const void* w, const int64_t* target
   CurrentDevice d;
   st = current_device(&d);
   if (st != QK_OK) return st;
-  const Call c = {h, w, targets, M, V, K, has_ignore, ignore, z, static_cast<char*>(workspace), stream};
-  if (M > 0) st = dtype == QK_F32 ? forward<float>(c, loss, lse) : forward<__nv_bfloat16>(c, loss, lse);
+  const Call c = {h, w, targets, M, V, K, has_ignore, ignore, z, static_cast<char*>(workspace), stream, d};
+  if (M > 0) st = dtype == QK_F32 ? forward<float>(c, dtype, loss, lse) : forward<__nv_bfloat16>(c, dtype, loss, lse);
   if (st != QK_OK || mean_loss == nullptr) return st;
   return launch_pdl(xent_mean_kernel<0>, dim3(1), 1024, 0, stream, loss, targets, M, has_ignore, ignore,
                     mean_loss);
@@ -365,9 +509,9 @@ qk_status qk_linear_xent_bwd(const void* h, const void* w, const int64_t* target
     cudaGetLastError();
     return QK_ERR_LAUNCH;
   }
-  const Call c = {h, w, targets, M, V, K, has_ignore, ignore, z, static_cast<char*>(workspace), stream};
-  return dtype == QK_F32 ? backward<float>(c, lse, dloss, dh, dw)
-                         : backward<__nv_bfloat16>(c, lse, dloss, dh, dw);
+  const Call c = {h, w, targets, M, V, K, has_ignore, ignore, z, static_cast<char*>(workspace), stream, d};
+  return dtype == QK_F32 ? backward<float>(c, dtype, lse, dloss, dh, dw)
+                         : backward<__nv_bfloat16>(c, dtype, lse, dloss, dh, dw);
 }
 
 }  // extern "C"
