@@ -4,7 +4,7 @@
 //   logits = h w^T;  lse = log sum exp(logits);  loss = lse - logits[t] + z lse^2
 //   g = dloss ((1 + 2 z lse) exp(logits - lse) - onehot(t));  dh = g w;  dw = g^T h
 //
-// Forward: one product whose epilogue folds each 256-column tile of a row into
+// Forward: one product whose epilogue folds each 128 columns of a row into
 // a (maximum, sum of exponentials) pair, then a join of the pairs of a row.
 // Backward, for one piece of the vocabulary after the other: a product whose
 // epilogue turns logits into g (bf16, in the workspace), dh += g w[piece] in
@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, 
   }
 }
 
-// Joins a row's pairs, one for each column tile: lanes are rows, the CTA's
-// warps take every eighth tile, in a fixed order.
+// Joins a row's pairs, one for each 128 columns: lanes are rows, the CTA's
+// warps take every eighth pair, in a fixed order.
 __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t part_ld, int64_t n_tiles,
                                                    const float* at_target, const int64_t* targets, int64_t M,
                                                    int64_t V, int has_ignore, int64_t ignore_index, float z,
@@ -179,7 +179,7 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     l.w = take(l.planes * l.piece * l.kp * 2);
   }
   if (!bwd) {
-    l.part = take(ceil_div(V, kTileN) * M * 8);
+    l.part = take(2 * ceil_div(V, kTileN) * M * 8);
     l.at_target = take(M * 4);
   } else {
     l.row = take(M * int64_t(sizeof(XentRow)));
@@ -276,11 +276,10 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   }
   p.rows = int32_t(rows);
   p.cols = int32_t(cols);
-  p.bn = kTileN;
   p.planes = int32_t(a.planes);
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));
-  p.n_tiles = int32_t(ceil_div(cols, p.bn));
+  p.n_tiles = int32_t(ceil_div(cols, kTileN));
   const int64_t total = int64_t(p.steps) * (p.planes == 3 ? 6 : 1);
   if (total > INT32_MAX) return QK_ERR_UNSUPPORTED;
   p.split_steps = splits == 1 ? int32_t(total) : split_steps;
@@ -288,7 +287,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.timeout_ns = kWaitTimeoutNs;
   p.status = c.dev.status;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, A_MN ? kStepK : 128) || !make_map(&mb, b, B_MN ? kStepK : p.bn / 2)) return QK_ERR_LAUNCH;
+  if (!make_map(&ma, a, A_MN ? kStepK : 128) || !make_map(&mb, b, B_MN ? kStepK : kTileN / 2)) return QK_ERR_LAUNCH;
   const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles * p.splits;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -347,7 +346,7 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
   }
   if (st != QK_OK) return st;
   return launch_pdl(join_kernel, dim3(unsigned(ceil_div(c.M, 32))), 256, 0, c.stream, p.part, p.part_ld,
-                    ceil_div(c.V, kTileN), p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
+                    2 * ceil_div(c.V, kTileN), p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
 }
 
 template <typename T>

@@ -6,9 +6,15 @@
 // What bounds it: the tensor cores.  A pair of CTAs forms a 256 x 256 tile; a
 // step of 64 k is 4 products of 16 k and 64 KB of operands through TMA, so each
 // byte that reaches shared memory is used 128 times.  Warp 0 keeps TMA loads
-// six steps ahead, warp 1 of the leading CTA issues the products, warps 4-7
-// turn the finished sums (TMEM holds two tiles) into outputs while the next
-// tile is being summed.  The grid is persistent: one CTA an SM.
+// six steps ahead, warp 1 of the leading CTA issues the products, warps 4-11
+// take finished sums out of TMEM (which holds two sets) and turn them into
+// outputs while the next ones are formed.  The grid is persistent: one CTA an SM.
+//
+// The tensor core adds to a sum by cutting off what does not fit, always toward
+// zero: a chain of n products of 16 k is short by about n 2^-25.5 of itself (a
+// sum over 8192 k measured 1e-5 off, where rounding to nearest gives 1e-6).  So
+// a chain ends after kChunkSteps * 64 = 512 k, and the chains of a tile are
+// added in registers, to nearest.
 //
 // An operand is stored with k innermost (K-major) or with its rows innermost
 // (MN-major): h, w and g serve as either, without a transposed copy.
@@ -24,10 +30,11 @@
 
 namespace qk {
 
-constexpr int kProductThreads = 256;
+constexpr int kProductThreads = 384;  // 4 warps that feed the tensor cores, 8 for the sums
 constexpr int kTileM = 256;       // rows of a pair's tile
 constexpr int kTileN = 256;       // most columns of one
 constexpr int kStepK = 64;        // k of one pipeline step: 128 bytes
+constexpr int kChunkSteps = 8;    // steps of one chain of products
 constexpr int kStages = 6;
 constexpr int kOperandBytes = 128 * kStepK * 2;  // one CTA's part of A (or of B at 256 columns)
 constexpr int kStageBytes = 2 * kOperandBytes;
@@ -46,13 +53,12 @@ struct ProductArgs {
   int32_t planes;            // 1 (bf16) or 3 (float32)
   int32_t m_tiles, n_tiles;
   int32_t splits, split_steps;  // the k axis in pieces of split_steps steps
-  int32_t bn;                // columns of a tile
   uint64_t timeout_ns;
   int* status;
   // epilogues; v0: vocabulary index of column 0
   int64_t v0;
   const int64_t* targets;    // lse
-  float2* part;              // lse: [column tile][part_ld] running (maximum, sum)
+  float2* part;              // lse: [half column tile][part_ld] (maximum, sum)
   int64_t part_ld;
   float* at_target;          // lse: logit of the target
   const XentRow* row;        // grad
@@ -115,8 +121,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(empty0 + 8 * s, 1);  // a commit of the leader's products
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(done0 + 8 * i, 1);  // a commit: the tile is summed
-      mbar_init(free0 + 8 * i, 8);  // four epilogue warps of each CTA have read it
+      mbar_init(done0 + 8 * i, 1);   // a commit: the chain is summed
+      mbar_init(free0 + 8 * i, 16);  // eight epilogue warps of each CTA have read it
     }
     fence_mbar_init();
     prefetch_tensor_map(&map_a);
@@ -142,14 +148,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     return false;
   };
 
+  // Registers: the launch holds 384 x 168 = 64512; 128 x 72 + 256 x 208 = 62464
+  // of them go to the warps that feed and to those that keep sums.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each step's operands ----
-    const int half_n = p.bn / 2;
-    const uint32_t bytes = 2u * uint32_t(kOperandBytes + half_n * kStepK * 2);
+    constexpr int half_n = kTileN / 2;
+    constexpr uint32_t bytes = 2u * uint32_t(kOperandBytes + half_n * kStepK * 2);
     int64_t q = 0;  // steps issued
     for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
-      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * p.bn + int(rank) * half_n;
+      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * kTileN + int(rank) * half_n;
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       for (int s = s0; s < s1; ++s, ++q) {
         const int st = int(q % kStages);
@@ -182,152 +192,165 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         mbar_wait<true>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products of both CTAs ----
-    const uint32_t idesc = instruction_desc(A_MN, B_MN, uint32_t(p.bn));
+    constexpr uint32_t idesc = instruction_desc(A_MN, B_MN, kTileN);
     constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
     constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
-    int64_t q = 0;
-    int it = 0;
-    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step, ++it) {
+    int64_t q = 0, it = 0;  // steps and chains begun
+    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
-      const int acc = it & 1;
-      if (!wait(free0 + 8 * acc, ((uint32_t(it) >> 1) & 1u) ^ 1u)) break;
-      tcgen05_fence_after();
-      const uint32_t d = tmem + uint32_t(acc) * kTileN;
-      for (int s = s0; s < s1; ++s, ++q) {
-        const int st = int(q % kStages);
-        if (!wait(full0 + 8 * st, uint32_t(q / kStages) & 1u)) break;
+      for (int c0 = s0; c0 < s1 && !failed; c0 += kChunkSteps, ++it) {
+        const uint32_t acc = uint32_t(it) & 1u;
+        if (!wait(free0 + 8 * acc, (uint32_t(it >> 1) & 1u) ^ 1u)) break;
         tcgen05_fence_after();
-        const uint32_t sa = ring + uint32_t(st) * kStageBytes;
-        const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kOperandBytes, B_MN ? kLbo : 0);
+        const uint32_t d = tmem + acc * kTileN;
+        const int c1 = min(s1, c0 + kChunkSteps);
+        for (int s = c0; s < c1; ++s, ++q) {
+          const int st = int(q % kStages);
+          if (!wait(full0 + 8 * st, uint32_t(q / kStages) & 1u)) break;
+          tcgen05_fence_after();
+          const uint32_t sa = ring + uint32_t(st) * kStageBytes;
+          const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kOperandBytes, B_MN ? kLbo : 0);
 #pragma unroll
-        for (int k = 0; k < kStepK / 16; ++k)
-          mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > s0 || k > 0);
-        mma_commit_pair(empty0 + 8 * st);
+          for (int k = 0; k < kStepK / 16; ++k)
+            mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+          mma_commit_pair(empty0 + 8 * st);
+        }
+        if (!failed) mma_commit_pair(done0 + 8 * acc);
       }
-      if (!failed) mma_commit_pair(done0 + 8 * acc);
     }
-  } else if (warp >= 4) {
-    // ---- epilogue: one row a thread ----
-    const int quarter = warp & 3;
-    int it = 0;
-    for (int64_t t = first_tile; t < tiles; t += tile_step, ++it) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- epilogue: half a row of the tile a thread ----
+    constexpr int kCols = kTileN / 2;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes of a warp: 32 (warp % 4) and up
+    int64_t it = 0;
+    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
-      const int acc = it & 1;
-      if (!wait(done0 + 8 * acc, (uint32_t(it) >> 1) & 1u)) break;
-      tcgen05_fence_after();
+      const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       const int64_t i = int64_t(at.m) * kTileM + rank * 128 + quarter * 32 + lane;
-      const int64_t j0 = int64_t(at.n) * p.bn;
+      const int64_t j0 = int64_t(at.n) * kTileN + half * kCols;
       const bool live = i < p.rows;
-      const int width = int(min(int64_t(p.bn), p.cols - j0));  // columns of C in this tile
-      const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc) * kTileN;
+      const int width = int(min(int64_t(kCols), p.cols - j0));  // this half's columns of C, may be <= 0
 
-      XentRow row = {};
-      int target = -1;  // column of the target in this tile
-      if (live && EPI == kEpiLse) {
-        const int64_t c = p.targets[i] - p.v0 - j0;
-        target = c >= 0 && c < width ? int(c) : -1;
-      }
-      if (live && EPI == kEpiGrad) {
-        row = p.row[i];
-        const int64_t c = row.target - p.v0 - j0;
-        target = row.target >= 0 && c >= 0 && c < width ? int(c) : -1;
-      }
-      float m = kNegInf, sum = 0.f;
-      const float factor = EPI == kEpiStore ? *p.scale : 1.f;
-
-      for (int c0 = 0; c0 < width; c0 += 32) {
-        float v[32];
-        __syncwarp();  // the load is a warp's; rows past the last skipped the output
-        tmem_load_32(src + uint32_t(c0), v);
-        if constexpr (EPI == kEpiLse) {
-          // a running maximum and sum of exponentials; columns past the last are -inf
-          if (width - c0 < 32) {
+      float v[kCols];
+      for (int c0 = s0; c0 < s1; c0 += kChunkSteps, ++it) {
+        const uint32_t acc = uint32_t(it) & 1u;
+        if (!wait(done0 + 8 * acc, uint32_t(it >> 1) & 1u)) break;
+        tcgen05_fence_after();
+        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * kTileN + uint32_t(half * kCols);
+        __syncwarp();  // the loads are the warp's
+        if (c0 == s0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = j < width - c0 ? v[j] : kNegInf;
-          }
-          if (unsigned(target - c0) < 32u) {
+          for (int c = 0; c < kCols; c += 16) tmem_load_16(src + uint32_t(c), v + c);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == target - c0) p.at_target[i] = v[j];
-          }
-          float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          // All -inf so far: shift by 0, so that a NaN among them still shows.
-          const float base = mn == kNegInf ? 0.f : mn * kLog2e;
-          float s[4] = {};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j & 3] += exp2_approx(fmaf(v[j], kLog2e, -base));
-          sum = (m == kNegInf ? sum : sum * exp2_approx(fmaf(m, kLog2e, -base))) + ((s[0] + s[1]) + (s[2] + s[3]));
-          m = mn;
-        } else if constexpr (EPI == kEpiGrad) {
-          if (live) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float g = exp2_approx((v[j] - row.lse) * kLog2e) * row.zf;
-              if (j == target - c0) g -= 1.f;
-              v[j] = row.target == -2 ? 0.f : g * row.g;
-            }
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + i * p.ld + j0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (c0 + j >= width) break;  // ld is a multiple of 8: whole vectors stay inside the row
-              if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4*>(out + j) = Vec16<__nv_bfloat16>::pack(v + j);
-              } else {
-                __nv_bfloat16 b[8][3];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) split3(v[j + e], b[e]);
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl) {
-                  __align__(16) __nv_bfloat16 o[8];
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) o[e] = b[e][pl];
-                  *reinterpret_cast<uint4*>(out + pl * p.plane_stride + j) = *reinterpret_cast<const uint4*>(o);
-                }
-              }
-            }
-          }
-        } else if constexpr (EPI == kEpiAccum) {
-          if (live) {
-            float* out = static_cast<float*>(p.out) + (int64_t(at.split) * p.rows + i) * p.ld + j0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              if (c0 + j >= width) break;  // ld is a multiple of 4
-              float4* o = reinterpret_cast<float4*>(out + j);
-              float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-              if (!p.first) {
-                const float4 y = *o;
-                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-              }
-              *o = x;
-            }
-          }
+          for (int c = 0; c < kCols; c += 16) tmem_load_wait(v + c);
         } else {
-          if (live) {
-            T* out = static_cast<T*>(p.out) + i * p.ld + j0 + c0;
-            constexpr int E = Vec16<T>::kElems;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= factor;
-            if (p.vec) {
+          for (int c = 0; c < kCols; c += 16) {
+            float x[16];
+            tmem_load_16(src + uint32_t(c), x);
+            tmem_load_wait(x);
 #pragma unroll
-              for (int j = 0; j < 32; j += E)
-                if (c0 + j < width) *reinterpret_cast<uint4*>(out + j) = Vec16<T>::pack(v + j);
-            } else {
+            for (int j = 0; j < 16; ++j) v[c + j] += x[j];
+          }
+        }
+        tcgen05_fence_before();
+        __syncwarp();  // all lanes have read their sums
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * acc, 0));
+      }
+      if (failed) break;
+
+      if constexpr (EPI == kEpiLse) {
+        // (maximum, sum of exponentials) of the half row; columns past the last count as -inf
+        if (!live) continue;
+        const int64_t target = p.targets[i] - p.v0 - j0;
+        if (target >= 0 && target < width) {
+          float x = 0.f;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c0 + j < width) Vec16<T>::store1(out + j, v[j]);
+          for (int j = 0; j < kCols; ++j)  // as PTX: in C++ it becomes an indexed load, and v leaves the registers
+            asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\t@p mov.f32 %0, %1;\n\t}"
+                : "+f"(x)
+                : "f"(v[j]), "r"(int(target)), "r"(j));
+          p.at_target[i] = x;
+        }
+        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, sum[4] = {};
+        if (width < kCols) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = j < width ? v[j] : kNegInf;
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // All -inf: shift by 0, so that a NaN among them still shows.
+        const float base = m == kNegInf ? 0.f : m * kLog2e;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sum[j & 3] += exp2_approx(fmaf(v[j], kLog2e, -base));
+        p.part[(2 * (p.v0 / kTileN + at.n) + half) * p.part_ld + i] =
+            make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      } else if constexpr (EPI == kEpiGrad) {
+        if (!live) continue;
+        const XentRow row = p.row[i];
+        const int64_t at_t = row.target >= 0 ? row.target - p.v0 - j0 : -1;
+        const int target = at_t >= 0 && at_t < width ? int(at_t) : -1;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + i * p.ld + j0;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          float g = exp2_approx((v[j] - row.lse) * kLog2e) * row.zf;
+          if (j == target) g -= 1.f;
+          v[j] = row.target == -2 ? 0.f : g * row.g;
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; j += 8) {
+          if (j >= width) break;  // ld is a multiple of 8: whole vectors stay inside the row
+          if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(out + j) = Vec16<__nv_bfloat16>::pack(v + j);
+          } else {
+            __nv_bfloat16 b[8][3];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split3(v[j + e], b[e]);
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+              __align__(16) __nv_bfloat16 o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = b[e][pl];
+              *reinterpret_cast<uint4*>(out + pl * p.plane_stride + j) = *reinterpret_cast<const uint4*>(o);
             }
           }
         }
+      } else if constexpr (EPI == kEpiAccum) {
+        if (!live) continue;
+        float* out = static_cast<float*>(p.out) + (int64_t(at.split) * p.rows + i) * p.ld + j0;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          if (j >= width) continue;  // ld is a multiple of 4
+          // Later pieces add at L2, which spares the loads: this launch is the
+          // only adder of an element, so the bits do not depend on any order.
+          asm volatile(
+              "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
+              "@p st.global.v4.f32 [%0], {%1, %2, %3, %4};\n\t"
+              "@!p red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(out + j),
+              "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "r"(p.first)
+              : "memory");
+        }
+      } else {
+        if (!live) continue;
+        T* out = static_cast<T*>(p.out) + i * p.ld + j0;
+        constexpr int E = Vec16<T>::kElems;
+        const float factor = *p.scale;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) v[j] *= factor;
+        if (p.vec) {
+#pragma unroll
+          for (int j = 0; j < kCols; j += E)
+            if (j < width) *reinterpret_cast<uint4*>(out + j) = Vec16<T>::pack(v + j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j < width) Vec16<T>::store1(out + j, v[j]);
+        }
       }
-      tcgen05_fence_before();
-      __syncwarp();  // all lanes have read their sums
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * acc, 0));
-      if (EPI == kEpiLse && live)
-        p.part[(p.v0 / p.bn + at.n) * p.part_ld + i] = make_float2(m, sum);
     }
   }
   __syncwarp();
