@@ -124,18 +124,17 @@ __global__ void __launch_bounds__(1024) rows_kernel(const int64_t* targets, cons
   }
 }
 
-// dh from its fp32 sums: the splits in order, times the scale, rounded once.
+// dh from its fp32 sums: the splits in order, rounded once.
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const float* sum, int64_t ld, int64_t split_stride, int splits,
-                                                     const float* scale, T* out, int64_t rows, int64_t cols) {
+                                                     T* out, int64_t rows, int64_t cols) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const float f = *scale;
   for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < rows * cols; e += int64_t(gridDim.x) * 256) {
     const float* s = sum + e / cols * ld + e % cols;
     float v = s[0];
     for (int k = 1; k < splits; ++k) v += s[k * split_stride];
-    Vec16<T>::store1(out + e, v * f);
+    Vec16<T>::store1(out + e, v);
   }
 }
 
@@ -152,11 +151,41 @@ struct Layout {
   int64_t h, w, part, at_target, row, scale, g, sum, total;
 };
 
-// Pieces of at most `most` vocabulary rows, of even widths.
-int64_t even_piece(int64_t V, int64_t most) {
-  most = std::max<int64_t>(256, most / 256 * 256);
-  const int64_t n = ceil_div(V, most);
-  return n == 1 ? V : round_up(ceil_div(V, n), 256);
+// Launches are waves of kPairs tiles; a wave takes as long as its tiles have
+// steps of 64 k, about 0.27 us each at full rate.
+int64_t waves(int64_t tiles) { return ceil_div(tiles, kPairs); }
+
+// Vocabulary rows of a piece, at most `most` (or 256) of them and whole tiles.
+// What the last wave of a piece's two products over the vocabulary's tiles (g,
+// dw) leaves idle depends on the number of tiles, and a launch costs some 10
+// steps: the cheapest count by that, from half of the most on.  (8192 x 32000 x
+// 4096: 63 + 62 tiles wide take 27 + 27 and 14 + 13 waves.)
+int64_t choose_piece(int64_t M, int64_t V, int64_t K, int64_t most) {
+  const int64_t all = ceil_div(V, kTileN), mt = ceil_div(M, kTileM), kt = ceil_div(K, kTileN);
+  const int64_t top = std::max<int64_t>(1, most / kTileN);
+  if (top >= all) return V;
+  int64_t best = top, best_cost = INT64_MAX;
+  for (int64_t w = top; w >= (top + 1) / 2; --w) {
+    const int64_t full = all / w, rest = all % w;
+    auto cost = [&](int64_t n) { return n == 0 ? 0 : waves(n * mt) * ceil_div(K, kStepK) + waves(n * kt) * ceil_div(M, kStepK) + 30; };
+    const int64_t c = full * cost(w) + cost(rest);
+    if (c < best_cost) best = w, best_cost = c;
+  }
+  return best * kTileN;
+}
+
+// k splits of dh's product over a piece: with few tiles (few rows, or a narrow
+// model) they give every pair work, with many they even out the last wave; each
+// costs a pass of fp32 sums through memory (written, and read once more).
+int choose_splits(int64_t M, int64_t K, int64_t steps) {
+  const int64_t tiles = ceil_div(M, kTileM) * ceil_div(K, kTileN);
+  int best = 1;
+  double best_us = 1e30;
+  for (int s = 1; s <= kPairs && int64_t(s) * 16 <= std::max<int64_t>(steps, 16); ++s) {
+    const double us = double(waves(tiles * s)) * double(ceil_div(steps, s)) * 0.27 + (s > 1 ? s : 0) * (double(M) * double(K) * 8 / 6.0e6);
+    if (us < 0.97 * best_us) best = s, best_us = us;
+  }
+  return best;
 }
 
 // `copied`: h and w go through the workspace (float32, or rows that TMA cannot read in place).
@@ -167,7 +196,7 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
   int64_t most = round_up(V, 256);
   if (copied) most = std::min<int64_t>(most, kStageCopyBytes / (l.kp * 2 * l.planes));
   if (bwd) most = std::min<int64_t>(most, kPieceBytes / (M * 2 * l.planes));
-  l.piece = even_piece(V, most);
+  l.piece = bwd ? choose_piece(M, V, K, most) : std::min<int64_t>(V, std::max<int64_t>(kTileN, most / kTileN * kTileN));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -186,12 +215,8 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     l.scale = take(4);
     l.ld_g = round_up(l.piece, 8);
     l.g = take(l.planes * M * l.ld_g * 2);
-    // dh's product sums over the vocabulary: with few tiles (few rows, or a
-    // narrow model) the axis is split, each split with its own fp32 sums, until
-    // every pair of CTAs has work; a split keeps at least 16 steps of 64.
-    const int64_t tiles = ceil_div(M, kTileM) * ceil_div(K, kTileN);
     const int64_t steps = ceil_div(l.piece, kStepK) * (l.planes == 3 ? 6 : 1);
-    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kPairs / std::min<int64_t>(tiles, kPairs), steps / 16));
+    const int splits = choose_splits(M, K, steps);
     l.split_steps = int(ceil_div(steps, splits));
     l.splits = int(ceil_div(steps, l.split_steps));
     l.sum = take(int64_t(l.splits) * M * l.kp * 4);
@@ -391,7 +416,7 @@ qk_status backward(const Call& c, int dtype, const float* lse, const float* dlos
   }
   if (st != QK_OK || dh == nullptr || direct) return st;
   return launch_pdl(finish_kernel<T>, dim3(blocks(c, c.M * c.K)), 256, 0, c.stream, sum, l.kp, c.M * l.kp, l.splits,
-                    scale, static_cast<T*>(dh), c.M, c.K);
+                    static_cast<T*>(dh), c.M, c.K);
 }
 
 // Bytes that these sizes may need, whichever way the pointers are aligned.
