@@ -1,0 +1,11 @@
+// Ring kernels of one norm operator and type (qk_norm_ring.cuh).
+#include "qk_norm_ring.cuh"
+
+namespace qk {
+NormTable norm_shapes_quant_f32(bool vec) {
+  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kNormQuant, float), QK_NORM_SHAPE(kNormQuant, float, 512, 512, 8, true)};
+  static const NormShape elements[] = {QK_NORM_ELEMENT_SHAPES(kNormQuant, float)};
+  return vec ? NormTable{vectors, int(sizeof(vectors) / sizeof(NormShape))}
+             : NormTable{elements, int(sizeof(elements) / sizeof(NormShape))};
+}
+}  // namespace qk

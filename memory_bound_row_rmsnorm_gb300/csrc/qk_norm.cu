@@ -5,11 +5,16 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "../../include/qk.h"
 #include "qk_bwd_kernels.cuh"  // dw_reduce_kernel
 #include "qk_host.h"
 #include "qk_norm_kernels.cuh"
+#include "qk_norm_ring.cuh"
 
 namespace qk {
 namespace {
@@ -33,19 +38,156 @@ qk_status launch_any(const CurrentDevice& d, int dtype, const NormArgs& a, void*
                          : launch_pdl(norm_any_kernel<OP, __nv_bfloat16>, grid, kNormAnyThreads, 0, stream, a);
 }
 
+// How a call runs: a ring kernel, or the any-row kernel (func == nullptr).
+struct NormPlan {
+  const void* func = nullptr;
+  int threads = 0, slots = 0, smem = 0;
+  uint32_t slot_bytes = 0;
+  int64_t items = 0, grid = 0;
+};
+
+std::mutex g_norm_mu;
+std::map<std::tuple<int, const void*, int>, int> g_norm_occ;  // (device, kernel, smem) -> CTAs an SM
+
+// Resident CTAs an SM; opts the kernel into the device's shared memory first.
+qk_status norm_occupancy(const CurrentDevice& d, const void* func, int threads, int smem, int* out) {
+  std::lock_guard<std::mutex> lock(g_norm_mu);
+  const auto key = std::make_tuple(d.index, func, smem);
+  const auto it = g_norm_occ.find(key);
+  if (it == g_norm_occ.end()) {
+    int n = 0;
+    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_optin - kNormStaticSmem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, size_t(smem)) != cudaSuccess) {
+      cudaGetLastError();
+      return QK_ERR_LAUNCH;
+    }
+    *out = g_norm_occ[key] = n;
+  } else {
+    *out = it->second;
+  }
+  return QK_OK;
+}
+
+NormTable shapes_of(int op, int dtype, bool vec) {
+  switch (op * 2 + (dtype == QK_BF16)) {
+    case 2 * kAddNorm: return norm_shapes_add_f32(vec);
+    case 2 * kAddNorm + 1: return norm_shapes_add_bf16(vec);
+    case 2 * kNormQuant: return norm_shapes_quant_f32(vec);
+    case 2 * kNormQuant + 1: return norm_shapes_quant_bf16(vec);
+    case 2 * kAddNormBwd: return norm_shapes_bwd_f32(vec);
+    default: return norm_shapes_bwd_bf16(vec);
+  }
+}
+
+// The first shape that holds the row; a ring of up to three items (two while
+// that keeps another CTA resident), a grid of every resident CTA.
+qk_status plan_norm(const CurrentDevice& d, int op, int dtype, int64_t M, int64_t N, bool vec, int inputs,
+                    NormPlan* p) {
+  *p = NormPlan{};
+  const int es = elem_size(dtype);
+  const int64_t units = vec ? N * es / 16 : N;
+  const NormTable t = shapes_of(op, dtype, vec);
+  const NormShape* s = nullptr;
+  for (int i = 0; i < t.count && s == nullptr; ++i)
+    if (units <= t.shapes[i].units) s = &t.shapes[i];
+  if (s == nullptr) {
+    p->grid = any_grid(d, M);
+    return QK_OK;
+  }
+  const int R = s->threads / s->row_threads;
+  p->func = s->func;
+  p->threads = s->threads;
+  p->items = (M + R - 1) / R;
+  p->slot_bytes = uint32_t((int64_t(R) * N * es + (vec ? 0 : 31) + 127) / 128 * 128);
+  int best = 0;
+  for (int slots = 3; slots >= 1; --slots) {
+    const int64_t smem = kSmemHeader + int64_t(slots) * inputs * p->slot_bytes;
+    if (smem > d.smem_optin - kNormStaticSmem) continue;
+    int occ = 0;
+    const qk_status st = norm_occupancy(d, s->func, s->threads, int(smem), &occ);
+    if (st != QK_OK) return st;
+    if (occ > best) {
+      best = occ;
+      p->slots = slots;
+      p->smem = int(smem);
+    }
+    if (slots == 2 && best > 0) break;
+  }
+  if (best == 0) return QK_ERR_UNSUPPORTED;
+  p->grid = std::min<int64_t>(p->items, int64_t(best) * d.sms);
+  return QK_OK;
+}
+
+// The plan of a call, kept per thread for the last shape of each operator and type.
+qk_status norm_plan(const CurrentDevice& d, int op, int dtype, int64_t M, int64_t N, bool vec, int inputs,
+                    NormPlan* out) {
+  struct Cached {
+    int dev = -1, inputs = 0;
+    int64_t M = -1, N = -1;
+    NormPlan plan;
+  };
+  thread_local Cached cache[3][2][2];
+  Cached& c = cache[op][dtype == QK_BF16][vec];
+  if (!(c.dev == d.index && c.M == M && c.N == N && c.inputs == inputs)) {
+    NormPlan p;
+    const qk_status st = plan_norm(d, op, dtype, M, N, vec, inputs, &p);
+    if (st != QK_OK) return st;
+    c.dev = d.index, c.M = M, c.N = N, c.inputs = inputs, c.plan = p;
+  }
+  *out = c.plan;
+  return QK_OK;
+}
+
+// Whether the rows of all these pointers are whole 16-byte vectors (the 8-bit
+// output's: whole groups of the 4 or 8 bytes that belong to one).
+bool whole_vectors(int dtype, int64_t N, std::initializer_list<const void*> ptrs) {
+  if (N * int64_t(elem_size(dtype)) % 16 != 0) return false;
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
 template <int OP>
-qk_status run_norm(int dtype, NormArgs& a, void* stream) {
-  CurrentDevice d;
-  const qk_status st = current_device(&d);
+qk_status run_norm(const CurrentDevice& d, int dtype, NormArgs& a, bool vec, void* stream) {
+  NormPlan p;
+  const int inputs = 1 + (a.r != nullptr) + (a.r2 != nullptr);
+  const qk_status st = norm_plan(d, OP, dtype, a.M, a.N, vec, inputs, &p);
   if (st != QK_OK) return st;
   a.inv_n = float(1.0 / double(a.N));
   a.timeout_ns = kWaitTimeoutNs;
   a.status = d.status;
-  return launch_any<OP>(d, dtype, a, stream);
+  if (p.func == nullptr) return launch_any<OP>(d, dtype, a, stream);
+  a.slots = p.slots;
+  a.slot_bytes = p.slot_bytes;
+  a.num_items = p.items;
+  return launch_pdl(reinterpret_cast<void (*)(NormArgs)>(const_cast<void*>(p.func)), dim3(unsigned(p.grid)),
+                    p.threads, size_t(p.smem), stream, a);
 }
 
-// Rows of dw partials of a backward launch.
-int64_t bwd_partial_rows(const CurrentDevice& d, int64_t M) { return any_grid(d, M); }
+// Rows of dw partials of a backward launch: the most that either way of it
+// takes (kept per thread for the last shape).
+qk_status bwd_partial_rows(const CurrentDevice& d, int dtype, int64_t M, int64_t N, int64_t* rows) {
+  thread_local struct {
+    int dev = -1, dtype = 0;
+    int64_t M = 0, N = 0, rows = 0;
+  } last;
+  if (last.dev == d.index && last.dtype == dtype && last.M == M && last.N == N) {
+    *rows = last.rows;
+    return QK_OK;
+  }
+  *rows = 0;
+  for (int inputs = 2; inputs <= 3; ++inputs)
+    for (const bool vec : {false, true}) {
+      if (vec && N * int64_t(elem_size(dtype)) % 16 != 0) continue;
+      NormPlan p;
+      const qk_status st = plan_norm(d, kAddNormBwd, dtype, M, N, vec, inputs, &p);
+      if (st != QK_OK) return st;
+      *rows = std::max(*rows, p.grid);
+    }
+  last.dev = d.index, last.dtype = dtype, last.M = M, last.N = N, last.rows = *rows;
+  return QK_OK;
+}
 
 }  // namespace
 }  // namespace qk
@@ -85,7 +227,10 @@ qk_status qk_add_rmsnorm_fwd(const void* x, const void* residual, const void* w,
   a.M = M;
   a.N = N;
   a.eps = eps;
-  return run_norm<kAddNorm>(dtype, a, stream);
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  return run_norm<kAddNorm>(d, dtype, a, whole_vectors(dtype, N, {x, residual, w, y, h}), stream);
 }
 
 qk_status qk_rmsnorm_quant_fwd(const void* x, const void* residual, const void* w, void* q, float* scale,
@@ -131,7 +276,11 @@ qk_status qk_rmsnorm_quant_fwd(const void* x, const void* residual, const void* 
   a.group = int32_t(group);
   a.groups = groups;
   a.qtype = qtype;
-  return run_norm<kNormQuant>(dtype, a, stream);
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  const bool vec = whole_vectors(dtype, N, {x, residual, w, h}) && aligned_to(q, 16 / es);
+  return run_norm<kNormQuant>(d, dtype, a, vec, stream);
 }
 
 qk_status qk_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t N, qk_dtype dtype, size_t* bytes) {
@@ -142,8 +291,10 @@ qk_status qk_add_rmsnorm_bwd_workspace_size(int64_t M, int64_t N, qk_dtype dtype
   CurrentDevice d;
   st = current_device(&d);
   if (st != QK_OK) return st;
-  *bytes = size_t(bwd_partial_rows(d, M)) * size_t(N) * 4;
-  return QK_OK;
+  int64_t rows = 0;
+  st = bwd_partial_rows(d, dtype, M, N, &rows);
+  *bytes = size_t(rows) * size_t(N) * 4;
+  return st;
 }
 
 qk_status qk_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, const void* dy, const void* dh,
@@ -181,7 +332,11 @@ qk_status qk_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, co
     cudaGetLastError();
     return QK_ERR_LAUNCH;
   }
-  const int64_t rows = bwd_partial_rows(d, M);
+  const bool vec = whole_vectors(dtype, N, {h, w, dy, dh, dx});
+  NormPlan p;
+  st = norm_plan(d, kAddNormBwd, dtype, M, N, vec, dh != nullptr ? 3 : 2, &p);
+  if (st != QK_OK) return st;
+  const int64_t rows = p.grid;
   if (workspace_bytes < size_t(rows) * size_t(N) * 4) return QK_ERR_INVALID_ARG;
   NormArgs a = {};
   a.x = h;
@@ -193,7 +348,7 @@ qk_status qk_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, co
   a.dw_partial = static_cast<float*>(workspace);
   a.M = M;
   a.N = N;
-  st = run_norm<kAddNormBwd>(dtype, a, stream);
+  st = run_norm<kAddNormBwd>(d, dtype, a, vec, stream);
   if (st != QK_OK) return st;
   const float* part = a.dw_partial;
   return launch_pdl(dw_reduce_kernel<0>, dim3(unsigned((N + 31) / 32)), kDwReduceThreads, 0, stream, part, dw,

@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
           bad = cta_max<TH>(bad, red[2]);
           const float s = scale_of(m, bad > 0.f, a.qtype);
           if (tid == 0) sc[0] = s;
-          for (int64_t j = tid; j < N; j += TH) q[j] = uint8_t(quantise(normed(j) / s, a.qtype));
+          const float inv = 1.f / s;
+          for (int64_t j = tid; j < N; j += TH) q[j] = uint8_t(quantise(normed(j) * inv, a.qtype));
         } else {
           __syncthreads();  // a warp reads what others kept of h
           for (int64_t g = warp; g < a.groups; g += TH / 32) {
@@ -171,10 +172,11 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
             m = group_max<32>(m);
             const float s = scale_of(m, __any_sync(0xffffffffu, bad), a.qtype);
             if (lane == 0) sc[g] = s;
+            const float inv = 1.f / s;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int64_t j = g * a.group + lane + 32 * k;
-              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(v[k] / s, a.qtype));
+              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(v[k] * inv, a.qtype));
             }
           }
         }
