@@ -431,42 +431,62 @@ def xent_bwd(logits, targets, lse, dloss=None, ignore_index=None, z_loss: float 
     return dx
 
 
-def _like(name, t, ref, shape, dtype=None):
-    """t checked to be a contiguous tensor of that shape on ref's device (of ref's type, or dtype)."""
-    if t.dtype != (dtype or ref.dtype) or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype or ref.dtype} tensor of shape {tuple(shape)}")
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+# The helpers below serve calls of a few microseconds (a decoding step's norm),
+# so their checks are few and cheap: identities, integers, no temporary objects,
+# and torch looked up once (_matrix, which every helper calls first, does it).
+torch = None
+
+
+def _matrix(x):
+    """(M, N, dtype code, device index) of a contiguous CUDA tensor on the
+    current device, where the C entry points launch."""
+    global torch
+    if torch is None:
+        import torch as _torch
+        torch = _torch
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if not x.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if x.dtype is torch.bfloat16:
+        code = QK_BF16
+    elif x.dtype is torch.float32:
+        code = QK_F32
+    else:
+        raise TypeError(f"unsupported dtype {x.dtype}: float32 or bfloat16 expected")
+    N = x.shape[-1] if x.dim() > 0 else 1
+    return x.numel() // max(N, 1), N, code, dev
+
+
+def _same(name, t, shape, dtype, dev):
+    """t, checked to be a contiguous tensor of that shape, type and device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     return t
 
 
-def _on_current_device(t):
-    """The C entry points launch on the current device: refuse a tensor of another one."""
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-
-
-def _workspace(nbytes: int, ref, stream):
-    """Scratch memory for one call.  When the call goes to a stream other than
-    the one that torch allocates on, the allocator is told that this stream uses
-    the block, so that it is not handed out again before the kernels are done."""
-    import torch
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=ref.device)
-    return _used_on(stream, ws)
+def _stream_on(stream, dev):
+    """The stream handle of a call on device dev (None: torch's current stream)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) or None
+    return _stream(stream)
 
 
 def _used_on(stream, *tensors):
-    import torch
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-    return tensors[0] if len(tensors) == 1 else tensors
+    """Tells torch's allocator that a call on `stream` uses tensors that were
+    allocated on the current one, so that their memory is not handed out again
+    before the kernels are done."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, want_rstd: bool = True,
@@ -474,17 +494,18 @@ def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, wan
     """h = x + residual and its RMSNorm over the last dimension; returns
     (y, h, rstd) (rstd is None if not wanted).  out and out_h may be x or
     residual (out_h=residual keeps the residual stream in place)."""
-    import torch
-    M, N = _rows(x)
-    code = _dtype_code(x)
-    _on_current_device(x)
-    _like("residual", residual, x, x.shape)
-    _like("w", w, x, (N,))
-    y = torch.empty_like(x) if out is None else _like("out", out, x, x.shape)
-    h = torch.empty_like(x) if out_h is None else _like("out_h", out_h, x, x.shape)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
-    qk_add_rmsnorm_fwd(x, residual, w, y, h, rstd, M, N, eps, code, stream)
-    _used_on(stream, y, h, rstd)
+    M, N, code, dev = _matrix(x)
+    shape, dtype = x.shape, x.dtype
+    _same("residual", residual, shape, dtype, dev)
+    _same("w", w, (N,), dtype, dev)
+    y = torch.empty_like(x) if out is None else _same("out", out, shape, dtype, dev)
+    h = torch.empty_like(x) if out_h is None else _same("out_h", out_h, shape, dtype, dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
+    _check(load_library().qk_add_rmsnorm_fwd(
+        x.data_ptr(), residual.data_ptr(), w.data_ptr(), y.data_ptr(), h.data_ptr(),
+        rstd.data_ptr() if want_rstd else None, M, N, eps, code, _stream_on(stream, dev)), "qk_add_rmsnorm_fwd")
+    if stream is not None:
+        _used_on(stream, y, h, rstd)
     return y, h, rstd
 
 
@@ -492,21 +513,23 @@ def add_rmsnorm_bwd(h, w, rstd, dy, dh=None, out=None, stream=None):
     """Backward of add_rmsnorm_fwd; returns (dx, dw): dx is the gradient of x
     and of residual alike, dw is float32.  dh is the gradient that reaches h by
     the residual stream (None: none).  out may be h, dy or dh."""
-    import torch
-    M, N = _rows(h)
-    code = _dtype_code(h)
-    _on_current_device(h)
-    _like("w", w, h, (N,))
-    _like("rstd", rstd, h, h.shape[:-1], torch.float32)
-    _like("dy", dy, h, h.shape)
+    M, N, code, dev = _matrix(h)
+    shape, dtype = h.shape, h.dtype
+    _same("w", w, (N,), dtype, dev)
+    _same("rstd", rstd, shape[:-1], torch.float32, dev)
+    _same("dy", dy, shape, dtype, dev)
     if dh is not None:
-        _like("dh", dh, h, h.shape)
-    dx = torch.empty_like(h) if out is None else _like("out", out, h, h.shape)
+        _same("dh", dh, shape, dtype, dev)
+    dx = torch.empty_like(h) if out is None else _same("out", out, shape, dtype, dev)
     dw = torch.empty(N, dtype=torch.float32, device=h.device)
     nbytes = qk_add_rmsnorm_bwd_workspace_size(M, N, code)
-    ws = _workspace(nbytes, h, stream)
-    qk_add_rmsnorm_bwd(h, w, rstd, dy, dh, dx, dw, ws, nbytes, M, N, code, stream)
-    _used_on(stream, dx, dw)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+    _check(load_library().qk_add_rmsnorm_bwd(
+        h.data_ptr(), w.data_ptr(), rstd.data_ptr(), dy.data_ptr(), None if dh is None else dh.data_ptr(),
+        dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, M, N, code, _stream_on(stream, dev)),
+        "qk_add_rmsnorm_bwd")
+    if stream is not None:
+        _used_on(stream, dx, dw, ws)
     return dx, dw
 
 
@@ -517,42 +540,46 @@ def rmsnorm_quant_fwd(x, w, residual=None, eps: float = 1e-6, group: int = 0, qd
     (torch.float8_e4m3fn by default, or torch.int8) that stands for
     q * scale; scale has one float32 a row (group 0) or one for each group of
     32, 64 or 128 columns.  h is None without a residual or if not wanted."""
-    import torch
-    M, N = _rows(x)
-    code = _dtype_code(x)
-    _on_current_device(x)
-    qdtype = qdtype or torch.float8_e4m3fn
-    if qdtype not in (torch.float8_e4m3fn, torch.int8):
+    M, N, code, dev = _matrix(x)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if qdtype is None or qdtype is torch.float8_e4m3fn:
+        qdtype, qcode = torch.float8_e4m3fn, QK_E4M3
+    elif qdtype is torch.int8:
+        qcode = QK_INT8
+    else:
         raise TypeError(f"unsupported qdtype {qdtype}: torch.float8_e4m3fn or torch.int8 expected")
     if group not in (0, 32, 64, 128):
         raise ValueError("group must be 0 (the whole row), 32, 64 or 128")
-    _like("w", w, x, (N,))
+    _same("w", w, (N,), dtype, dev)
     h = None
     if residual is not None:
-        _like("residual", residual, x, x.shape)
-        if want_h:
-            h = torch.empty_like(x) if out_h is None else _like("out_h", out_h, x, x.shape)
+        _same("residual", residual, shape, dtype, dev)
+        if out_h is not None:
+            h = _same("out_h", out_h, shape, dtype, dev)
+        elif want_h:
+            h = torch.empty_like(x)
     elif out_h is not None:
         raise ValueError("out_h needs a residual")
-    q = torch.empty(x.shape, dtype=qdtype, device=x.device)
-    groups = -(-N // group) if group else 1
-    scale = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
-    qk_rmsnorm_quant_fwd(x, residual, w, q, scale, h, rstd, M, N, eps, group, code,
-                         QK_INT8 if qdtype == torch.int8 else QK_E4M3, stream)
-    _used_on(stream, q, scale, h, rstd)
+    q = torch.empty(shape, dtype=qdtype, device=device)
+    scale = torch.empty(shape[:-1] + (-(-N // group) if group else 1,), dtype=torch.float32, device=device)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device) if want_rstd else None
+    _check(load_library().qk_rmsnorm_quant_fwd(
+        x.data_ptr(), None if residual is None else residual.data_ptr(), w.data_ptr(), q.data_ptr(),
+        scale.data_ptr(), None if h is None else h.data_ptr(), rstd.data_ptr() if want_rstd else None, M, N, eps,
+        group, code, qcode, _stream_on(stream, dev)), "qk_rmsnorm_quant_fwd")
+    if stream is not None:
+        _used_on(stream, q, scale, h, rstd)
     return q, scale, h, rstd
 
 
 def _linear_xent_sizes(h, w, targets):
-    import torch
-    M, K = _rows(h)
-    _on_current_device(h)
+    M, K, code, dev = _matrix(h)
     if w.dim() != 2:
         raise ValueError("w must have two dimensions, [vocabulary, hidden]")
-    _like("w", w, h, (w.shape[0], K))
-    _like("targets", targets, h, h.shape[:-1], torch.int64)
-    return M, w.shape[0], K
+    V = w.shape[0]
+    _same("w", w, (V, K), h.dtype, dev)
+    _same("targets", targets, h.shape[:-1], torch.int64, dev)
+    return M, V, K, code, dev
 
 
 def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_loss: float = 0.0,
@@ -560,16 +587,18 @@ def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_l
     """Per-row cross-entropy of the logits h @ w.T, which are never stored;
     returns (loss, lse) (lse is None if not wanted), or (loss, lse, mean) with
     want_mean.  Options as in xent_fwd."""
-    import torch
-    M, V, K = _linear_xent_sizes(h, w, targets)
-    code = _dtype_code(h)
+    M, V, K, code, dev = _linear_xent_sizes(h, w, targets)
     loss = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
     lse = torch.empty_like(loss) if want_lse else None
     mean = torch.empty((), dtype=torch.float32, device=h.device) if want_mean else None
     nbytes = qk_linear_xent_fwd_workspace_size(M, V, K, code)
-    ws = _workspace(nbytes, h, stream)
-    qk_linear_xent_fwd(h, w, targets, loss, lse, mean, ws, nbytes, M, V, K, code, ignore_index, z_loss, stream)
-    _used_on(stream, loss, lse, mean)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+    _check(load_library().qk_linear_xent_fwd(
+        h.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr() if want_lse else None,
+        mean.data_ptr() if want_mean else None, ws.data_ptr(), nbytes, M, V, K, code, _options(ignore_index, z_loss),
+        _stream_on(stream, dev)), "qk_linear_xent_fwd")
+    if stream is not None:
+        _used_on(stream, loss, lse, mean, ws)
     return (loss, lse, mean) if want_mean else (loss, lse)
 
 
@@ -577,17 +606,18 @@ def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: f
                     want_dh: bool = True, want_dw: bool = True, stream=None):
     """Backward of linear_xent_fwd; returns (dh, dw) (None if not wanted).
     dloss is the float32 gradient of each row's loss (None: 1)."""
-    import torch
-    M, V, K = _linear_xent_sizes(h, w, targets)
-    code = _dtype_code(h)
-    _like("lse", lse, h, h.shape[:-1], torch.float32)
+    M, V, K, code, dev = _linear_xent_sizes(h, w, targets)
+    _same("lse", lse, h.shape[:-1], torch.float32, dev)
     if dloss is not None:
-        _like("dloss", dloss, h, h.shape[:-1], torch.float32)
+        _same("dloss", dloss, h.shape[:-1], torch.float32, dev)
     dh = torch.empty_like(h) if want_dh else None
     dw = torch.empty_like(w) if want_dw else None
     nbytes = qk_linear_xent_bwd_workspace_size(M, V, K, code)
-    ws = _workspace(nbytes, h, stream)
-    qk_linear_xent_bwd(h, w, targets, lse, dloss, dh, dw, ws, nbytes, M, V, K, code, ignore_index, z_loss,
-                       stream)
-    _used_on(stream, dh, dw)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+    _check(load_library().qk_linear_xent_bwd(
+        h.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), None if dloss is None else dloss.data_ptr(),
+        dh.data_ptr() if want_dh else None, dw.data_ptr() if want_dw else None, ws.data_ptr(), nbytes, M, V, K, code,
+        _options(ignore_index, z_loss), _stream_on(stream, dev)), "qk_linear_xent_bwd")
+    if stream is not None:
+        _used_on(stream, dh, dw, ws)
     return dh, dw

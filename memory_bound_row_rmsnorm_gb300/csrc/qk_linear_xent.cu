@@ -29,7 +29,12 @@ namespace {
 constexpr int64_t kMaxDim = INT32_MAX;
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece
 constexpr int64_t kStageCopyBytes = int64_t(64) << 20;  // copied or split weights of one piece
-constexpr int kPairs = 76;  // CTA pairs of a GB300; only the number of k splits follows it
+constexpr int kPairs = 76;  // CTA pairs of a GB300
+// Up to this many tokens the forward puts the vocabulary on the tile's rows and
+// the tokens on its 16 to 64 columns.  With tokens on the 256 rows the tensor
+// cores work through 240 empty ones at 16 tokens, 34 us at 32000 x 4096 where
+// reading w takes 39 us at the copy's rate; the columns cost them nothing.
+constexpr int64_t kFewTokens = 64;
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
@@ -57,9 +62,11 @@ __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, 
   }
 }
 
-// Joins a row's pairs, one for each 128 columns: lanes are rows, the CTA's
-// warps take every eighth pair, in a fixed order.
-__global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t part_ld, int64_t n_tiles,
+// Joins a row's n pairs, in a fixed order.  ROW_LANES: lanes are rows and the
+// CTA's warps take every eighth pair, four loads in flight.  Otherwise (few
+// rows) a warp is a row and its lanes take every 32nd pair.
+template <bool ROW_LANES>
+__global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t part_ld, int64_t n,
                                                    const float* at_target, const int64_t* targets, int64_t M,
                                                    int64_t V, int has_ignore, int64_t ignore_index, float z,
                                                    float* loss, float* lse) {
@@ -67,7 +74,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t p
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = int64_t(blockIdx.x) * 32 + lane;
+  const int64_t row = ROW_LANES ? int64_t(blockIdx.x) * 32 + lane : int64_t(blockIdx.x) * 8 + warp;
   float m = kNegInf, s = 0.f;
   auto fold = [&](float2 b) {  // an empty (-inf) side adds its sum, 0 or NaN
     const float mn = fmaxf(m, b.x);
@@ -75,13 +82,29 @@ __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t p
         (b.x == kNegInf ? b.y : b.y * exp2_approx((b.x - mn) * kLog2e));
     m = mn;
   };
-  if (row < M)
-    for (int64_t t = warp; t < n_tiles; t += 8) fold(part[t * part_ld + row]);
-  red[warp][lane] = make_float2(m, s);
-  __syncthreads();
-  if (warp != 0 || row >= M) return;
-  m = kNegInf, s = 0.f;
-  for (int i = 0; i < 8; ++i) fold(red[i][lane]);
+  constexpr int kStep = ROW_LANES ? 8 : 32, kDepth = 4;
+  if (row < M) {
+    for (int64_t t = ROW_LANES ? warp : lane; t < n; t += kDepth * kStep) {
+      float2 b[kDepth];
+#pragma unroll
+      for (int k = 0; k < kDepth; ++k)
+        b[k] = t + k * kStep < n ? part[(t + k * kStep) * part_ld + row] : make_float2(kNegInf, 0.f);
+#pragma unroll
+      for (int k = 0; k < kDepth; ++k) fold(b[k]);
+    }
+  }
+  if constexpr (ROW_LANES) {
+    red[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0 || row >= M) return;
+    m = kNegInf, s = 0.f;
+    for (int i = 0; i < 8; ++i) fold(red[i][lane]);
+  } else {
+    const float mx = group_max<32>(m);
+    s = group_sum<32>(m == kNegInf ? s : s * exp2_approx((m - mx) * kLog2e));
+    m = mx;
+    if (lane != 0 || row >= M) return;
+  }
   const float l = m + logf(s);
   const int64_t t = targets[row];
   if (lse != nullptr) lse[row] = l;
@@ -208,7 +231,9 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     l.w = take(l.planes * l.piece * l.kp * 2);
   }
   if (!bwd) {
-    l.part = take(2 * ceil_div(V, kTileN) * M * 8);
+    const int64_t pairs = M > kFewTokens ? 2 * ceil_div(V, kTileN)
+                                         : 8 * std::min<int64_t>(ceil_div(V, kTileM), kPairs * ceil_div(V, l.piece));
+    l.part = take(pairs * M * 8);
     l.at_target = take(M * 4);
   } else {
     l.row = take(M * int64_t(sizeof(XentRow)));
@@ -286,14 +311,14 @@ bool make_map(CUtensorMap* map, const Operand& o, int box_rows) {
 }
 
 // C [rows, cols] = A B^T over `depth`; the epilogue's fields of p are set by the caller.
-template <int EPI, bool A_MN, bool B_MN, typename T>
+template <int EPI, bool A_MN, bool B_MN, typename T, int TN = kTileN>
 qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const Operand& b, int64_t rows,
                          int64_t cols, int64_t depth, int splits, int split_steps) {
-  const auto kernel = product_kernel<EPI, A_MN, B_MN, T>;
+  const auto kernel = product_kernel<EPI, A_MN, B_MN, T, TN>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
   const uint64_t bit = uint64_t(1) << (c.dev.index & 63);
   if (!(prepared.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem(TN)) != cudaSuccess) {
       cudaGetLastError();
       return QK_ERR_LAUNCH;
     }
@@ -304,7 +329,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.planes = int32_t(a.planes);
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));
-  p.n_tiles = int32_t(ceil_div(cols, kTileN));
+  p.n_tiles = int32_t(ceil_div(cols, TN));
   const int64_t total = int64_t(p.steps) * (p.planes == 3 ? 6 : 1);
   if (total > INT32_MAX) return QK_ERR_UNSUPPORTED;
   p.split_steps = splits == 1 ? int32_t(total) : split_steps;
@@ -312,13 +337,14 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.timeout_ns = kWaitTimeoutNs;
   p.status = c.dev.status;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, A_MN ? kStepK : 128) || !make_map(&mb, b, B_MN ? kStepK : kTileN / 2)) return QK_ERR_LAUNCH;
+  if (!make_map(&ma, a, A_MN ? kStepK : 128) || !make_map(&mb, b, B_MN ? kStepK : TN / 2)) return QK_ERR_LAUNCH;
   const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles * p.splits;
+  if (tiles > INT32_MAX) return QK_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(tiles, c.dev.sms / 2)), 1, 1);
+  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(tiles, std::min(kPairs, c.dev.sms / 2))), 1, 1);
   cfg.blockDim = dim3(kProductThreads, 1, 1);
-  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.dynamicSmemBytes = product_smem(TN);
   cfg.stream = static_cast<cudaStream_t>(c.stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -363,15 +389,26 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
   p.part = reinterpret_cast<float2*>(c.ws + l.part);
   p.part_ld = c.M;
   p.at_target = reinterpret_cast<float*>(c.ws + l.at_target);
+  int64_t pairs = 2 * ceil_div(c.V, kTileN);  // of a row, for the join
+  if (c.M <= kFewTokens) pairs = 0;
   for (p.v0 = 0; p.v0 < c.V && st == QK_OK; p.v0 += l.piece) {
     const int64_t width = std::min(l.piece, c.V - p.v0);
     st = operand(c, l, copied, static_cast<const T*>(c.w) + p.v0 * c.K, width, c.ws + l.w, &w);
-    if (st == QK_OK)
+    if (st != QK_OK) break;
+    if (c.M > kFewTokens) {
       st = launch_product<kEpiLse, false, false, __nv_bfloat16>(c, p, h, w, c.M, width, c.K, 1, 0);
+      continue;
+    }
+    p.part0 = pairs / 8;
+    st = c.M <= 16   ? launch_product<kEpiLseCols, false, false, __nv_bfloat16, 16>(c, p, w, h, width, c.M, c.K, 1, 0)
+         : c.M <= 32 ? launch_product<kEpiLseCols, false, false, __nv_bfloat16, 32>(c, p, w, h, width, c.M, c.K, 1, 0)
+                     : launch_product<kEpiLseCols, false, false, __nv_bfloat16, 64>(c, p, w, h, width, c.M, c.K, 1, 0);
+    pairs += 8 * std::min<int64_t>(ceil_div(width, kTileM), std::min(kPairs, c.dev.sms / 2));
   }
   if (st != QK_OK) return st;
-  return launch_pdl(join_kernel, dim3(unsigned(ceil_div(c.M, 32))), 256, 0, c.stream, p.part, p.part_ld,
-                    2 * ceil_div(c.V, kTileN), p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
+  return launch_pdl(c.M > kFewTokens ? join_kernel<true> : join_kernel<false>,
+                    dim3(unsigned(ceil_div(c.M, c.M > kFewTokens ? 32 : 8))), 256, 0, c.stream, p.part, p.part_ld,
+                    pairs, p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
 }
 
 template <typename T>

@@ -32,16 +32,22 @@ namespace qk {
 
 constexpr int kProductThreads = 384;  // 4 warps that feed the tensor cores, 8 for the sums
 constexpr int kTileM = 256;       // rows of a pair's tile
-constexpr int kTileN = 256;       // most columns of one
+constexpr int kTileN = 256;       // columns of one, where there are enough
 constexpr int kStepK = 64;        // k of one pipeline step: 128 bytes
 constexpr int kChunkSteps = 8;    // steps of one chain of products
-constexpr int kStages = 6;
-constexpr int kOperandBytes = 128 * kStepK * 2;  // one CTA's part of A (or of B at 256 columns)
-constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kOutBytes = 32 * 128;  // an epilogue warp's 32 rows of 128 bytes on their way out
-constexpr int kProductSmem = kStages * kStageBytes + 8 * kOutBytes + 1024;  // and room to start on 1024 bytes
+constexpr int kABytes = 128 * kStepK * 2;  // one CTA's part of a step of A
+constexpr int kOutBytes = 32 * 128;        // an epilogue warp's 32 rows of 128 bytes on their way out
 
-enum Epilogue : int { kEpiLse = 0, kEpiGrad = 1, kEpiAccum = 2, kEpiStore = 3 };
+// kEpiLseCols: C's columns are the tokens (few), its rows the vocabulary.
+enum Epilogue : int { kEpiLse = 0, kEpiGrad = 1, kEpiAccum = 2, kEpiStore = 3, kEpiLseCols = 4 };
+
+// Shared memory by the tile's columns TN: six stages of 32 KB, or ten of A's
+// 16 KB and B's TN / 2 rows when that is little, and the way out.
+__host__ __device__ constexpr int product_stages(int tn) { return tn == kTileN ? 6 : 10; }
+__host__ __device__ constexpr int product_stage_bytes(int tn) { return kABytes + tn / 2 * kStepK * 2; }
+__host__ __device__ constexpr int product_smem(int tn) {  // and room to start on 1024 bytes
+  return product_stages(tn) * product_stage_bytes(tn) + (tn == kTileN ? 8 * kOutBytes : 0) + 1024;
+}
 
 struct XentRow {   // what the gradient needs of a row
   float lse, g, zf;  // g: dloss / scale (NaN for a bad target); zf = 1 + 2 z lse
@@ -59,8 +65,9 @@ struct ProductArgs {
   // epilogues; v0: vocabulary index of column 0
   int64_t v0;
   const int64_t* targets;    // lse
-  float2* part;              // lse: [half column tile][part_ld] (maximum, sum)
+  float2* part;              // lse: [half column tile, or pair and warp][part_ld] (maximum, sum)
   int64_t part_ld;
+  int64_t part0;             // lse over columns: first pair's place in the list
   float* at_target;          // lse: logit of the target
   const XentRow* row;        // grad
   void* out;                 // grad: bf16 [planes][rows][ld]; accum: fp32 [splits][rows][ld]; store: [rows][ld]
@@ -108,37 +115,43 @@ __device__ __forceinline__ void rows_out(uint32_t buf, int lane, const uint4* u,
 // Tile number -> (split, row tile, column tile).  Eight row tiles are walked
 // together: the pairs that run at one time then share their operands in L2
 // (76 pairs: 8 row tiles x 9.5 column tiles, a quarter of the loads unique).
+// 32-bit: the host refuses more tiles (64-bit divisions cost a thousand cycles
+// a tile, which shows where a tile is a step or two).
 struct TileAt {
   int split, m, n;
 };
-__device__ __forceinline__ TileAt tile_at(const ProductArgs& p, int64_t t) {
-  const int64_t per = int64_t(p.m_tiles) * p.n_tiles;
+__device__ __forceinline__ TileAt tile_at(const ProductArgs& p, uint32_t t) {
+  const uint32_t per = uint32_t(p.m_tiles) * uint32_t(p.n_tiles), band = 8u * uint32_t(p.n_tiles);
   TileAt r;
-  r.split = int(t / per);
-  const int64_t in = t % per;
-  const int64_t group = in / (int64_t(8) * p.n_tiles);
-  const int64_t rest = in % (int64_t(8) * p.n_tiles);
-  const int wide = min(8, p.m_tiles - int(group) * 8);
-  r.m = int(group) * 8 + int(rest % wide);
+  r.split = p.splits == 1 ? 0 : int(t / per);
+  const uint32_t in = t - uint32_t(r.split) * per, group = in / band, rest = in - group * band;
+  const uint32_t wide = min(8u, uint32_t(p.m_tiles) - group * 8u);
   r.n = int(rest / wide);
+  r.m = int(group * 8u + rest - uint32_t(r.n) * wide);
   return r;
 }
 
-template <int EPI, bool A_MN, bool B_MN, typename T>
+template <int EPI, bool A_MN, bool B_MN, typename T, int TN>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const ProductArgs p) {
+  constexpr int kStages = product_stages(TN), kStageBytes = product_stage_bytes(TN);
+  constexpr uint32_t kColumns = TN < 16 ? 32 : 2 * TN;  // TMEM: two sets of sums
+  static_assert(!B_MN || TN == kTileN, "MN-major B comes in boxes of 64 columns");
   extern __shared__ unsigned char dynamic_smem[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
   __shared__ uint32_t tmem_at;
+
+  // Columns of an epilogue thread, and the warps that take part.
+  constexpr int kCols = TN / 2 < 16 ? 16 : TN / 2, kReaders = 4 * (TN / kCols);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kStages, done0 = full0 + 16 * kStages,
                  free0 = done0 + 16;
   const uint32_t ring = (smem_addr(dynamic_smem) + 1023u) & ~1023u;  // the same in both CTAs
-  const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles * p.splits;
-  const int64_t first_tile = cluster_id_x(), tile_step = num_clusters_x();
+  const uint32_t tiles = uint32_t(p.m_tiles) * uint32_t(p.n_tiles) * uint32_t(p.splits);
+  const uint32_t first_tile = cluster_id_x(), tile_step = num_clusters_x();
   const int pairs = p.planes == 3 ? 6 : 1;
   const int total_steps = pairs * p.steps;
 
@@ -149,7 +162,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done0 + 8 * i, 1);   // a commit: the chain is summed
-      mbar_init(free0 + 8 * i, 16);  // eight epilogue warps of each CTA have read it
+      mbar_init(free0 + 8 * i, 2 * kReaders);  // the epilogue warps of both CTAs have read it
     }
     fence_mbar_init();
     prefetch_tensor_map(&map_a);
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   __syncwarp();
   if (warp == 2) {
-    tmem_alloc_pair(smem_addr(&tmem_at), 512);
+    tmem_alloc_pair(smem_addr(&tmem_at), kColumns);
     tmem_relinquish_pair();
   }
   tcgen05_fence_before();
@@ -181,26 +194,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each step's operands ----
-    constexpr int half_n = kTileN / 2;
-    constexpr uint32_t bytes = 2u * uint32_t(kOperandBytes + half_n * kStepK * 2);
+    constexpr int half_n = TN / 2;
+    constexpr uint32_t bytes = 2u * uint32_t(kStageBytes);
     int64_t q = 0;  // steps issued
-    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
+    int st = 0;
+    uint32_t turn = 0;
+    for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
-      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * kTileN + int(rank) * half_n;
+      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * half_n;
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       for (int s = s0; s < s1; ++s, ++q) {
-        const int st = int(q % kStages);
-        if (!wait(empty0 + 8 * st, (uint32_t(q / kStages) & 1u) ^ 1u)) break;
+        if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
         const int pair = s / p.steps, k = (s % p.steps) * kStepK;
         // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0): the small products first
         const int pa = pairs == 1 ? 0 : pair < 3 ? 2 - pair : pair == 3 ? 1 : 0;
         const int pb = pairs == 1 ? 0 : pair < 3 ? pair : pair == 4 ? 1 : 0;
         const uint32_t bar = map_to_rank(full0 + 8 * st, 0);
         if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, bytes);
-        const uint32_t da = ring + uint32_t(st) * kStageBytes, db = da + kOperandBytes;
+        const uint32_t da = ring + uint32_t(st) * kStageBytes, db = da + kABytes;
         if constexpr (A_MN) {
           tma_load_3d(da, &map_a, a0, k, pa, bar);
-          tma_load_3d(da + kOperandBytes / 2, &map_a, a0 + 64, k, pa, bar);
+          tma_load_3d(da + kABytes / 2, &map_a, a0 + 64, k, pa, bar);
         } else {
           tma_load_3d(da, &map_a, k, a0, pa, bar);
         }
@@ -210,6 +224,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         } else {
           tma_load_3d(db, &map_b, k, b0, pb, bar);
         }
+        if (++st == kStages) st = 0, turn ^= 1u;
       }
     }
     // A failed launch leaves once the loads in flight have landed: the leader's
@@ -219,29 +234,30 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         mbar_wait<true>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products of both CTAs ----
-    constexpr uint32_t idesc = instruction_desc(A_MN, B_MN, kTileN);
+    constexpr uint32_t idesc = instruction_desc(A_MN, B_MN, TN);
     constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
     constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
-    int64_t q = 0, it = 0;  // steps and chains begun
-    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
+    int st = 0;
+    uint32_t turn = 0, it = 0;  // it: chains begun
+    for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       for (int c0 = s0; c0 < s1 && !failed; c0 += kChunkSteps, ++it) {
-        const uint32_t acc = uint32_t(it) & 1u;
-        if (!wait(free0 + 8 * acc, (uint32_t(it >> 1) & 1u) ^ 1u)) break;
+        const uint32_t acc = it & 1u;
+        if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
         tcgen05_fence_after();
-        const uint32_t d = tmem + acc * kTileN;
+        const uint32_t d = tmem + acc * TN;
         const int c1 = min(s1, c0 + kChunkSteps);
-        for (int s = c0; s < c1; ++s, ++q) {
-          const int st = int(q % kStages);
-          if (!wait(full0 + 8 * st, uint32_t(q / kStages) & 1u)) break;
+        for (int s = c0; s < c1; ++s) {
+          if (!wait(full0 + 8 * st, turn)) break;
           tcgen05_fence_after();
           const uint32_t sa = ring + uint32_t(st) * kStageBytes;
-          const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kOperandBytes, B_MN ? kLbo : 0);
+          const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
 #pragma unroll
           for (int k = 0; k < kStepK / 16; ++k)
             mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
           mma_commit_pair(empty0 + 8 * st);
+          if (++st == kStages) st = 0, turn ^= 1u;
         }
         if (!failed) mma_commit_pair(done0 + 8 * acc);
       }
@@ -250,25 +266,38 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- epilogue: half a row of the tile a thread ----
-    constexpr int kCols = kTileN / 2;
     const int quarter = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes of a warp: 32 (warp % 4) and up
     const uint32_t buf = ring + uint32_t(kStages * kStageBytes) + uint32_t(warp - 4) * kOutBytes;
-    int64_t it = 0;
-    for (int64_t t = first_tile; t < tiles && !failed; t += tile_step) {
+    // kEpiLseCols: each lane's running (maximum, sum) of its tokens over the
+    // vocabulary rows it meets, joined over the lanes once at the end.
+    float run_m[EPI == kEpiLseCols ? kCols : 1], run_s[EPI == kEpiLseCols ? kCols : 1];
+    int run_t[EPI == kEpiLseCols ? kCols : 1];
+    if constexpr (EPI == kEpiLseCols) {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int token = half * kCols + j;
+        run_m[j] = kNegInf;
+        run_s[j] = 0.f;
+        const int64_t tg = token < p.cols ? p.targets[token] : -1;
+        run_t[j] = tg >= p.v0 && tg < p.v0 + p.rows ? int(tg - p.v0) : -1;
+      }
+    }
+    uint32_t it = 0;
+    for (uint32_t t = first_tile; t < tiles && !failed && half * kCols < TN; t += tile_step) {
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       const int64_t i = int64_t(at.m) * kTileM + rank * 128 + quarter * 32 + lane;
-      const int64_t j0 = int64_t(at.n) * kTileN + half * kCols;
+      const int64_t j0 = int64_t(at.n) * TN + half * kCols;
       const bool live = i < p.rows;
       const int rows_left = int(min(int64_t(32), p.rows - (i - lane)));  // this warp's rows of C, may be <= 0
       const int width = int(min(int64_t(kCols), p.cols - j0));  // this half's columns of C, may be <= 0
 
       float v[kCols];
       for (int c0 = s0; c0 < s1; c0 += kChunkSteps, ++it) {
-        const uint32_t acc = uint32_t(it) & 1u;
-        if (!wait(done0 + 8 * acc, uint32_t(it >> 1) & 1u)) break;
+        const uint32_t acc = it & 1u;
+        if (!wait(done0 + 8 * acc, (it >> 1) & 1u)) break;
         tcgen05_fence_after();
-        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * kTileN + uint32_t(half * kCols);
+        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * TN + uint32_t(half * kCols);
         __syncwarp();  // the loads are the warp's
         if (c0 == s0) {
 #pragma unroll
@@ -291,7 +320,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       if (failed) break;
 
-      if constexpr (EPI == kEpiLse) {
+      if constexpr (EPI == kEpiLseCols) {
+        if (!live) continue;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          if (run_t[j] == int(i)) p.at_target[half * kCols + j] = v[j];
+          const float mn = fmaxf(run_m[j], v[j]);
+          // All -inf so far: shift by 0, so that a NaN still shows.
+          const float base = mn == kNegInf ? 0.f : mn * kLog2e;
+          run_s[j] = (run_m[j] == kNegInf ? run_s[j] : run_s[j] * exp2_approx(fmaf(run_m[j], kLog2e, -base))) +
+                     exp2_approx(fmaf(v[j], kLog2e, -base));
+          run_m[j] = mn;
+        }
+      } else if constexpr (EPI == kEpiLse) {
         // (maximum, sum of exponentials) of the half row; columns past the last count as -inf
         if (!live) continue;
         const int64_t target = p.targets[i] - p.v0 - j0;
@@ -316,7 +357,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const float base = m == kNegInf ? 0.f : m * kLog2e;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) sum[j & 3] += exp2_approx(fmaf(v[j], kLog2e, -base));
-        p.part[(2 * (p.v0 / kTileN + at.n) + half) * p.part_ld + i] =
+        p.part[(2 * (p.v0 / TN + at.n) + half) * p.part_ld + i] =
             make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (EPI == kEpiGrad) {
         if (width <= 0) continue;
@@ -410,6 +451,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
     }
+    if constexpr (EPI == kEpiLseCols) {
+      // One pair a warp and token: rows of the join's list are (pair of CTAs, CTA, warp).
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const float m = group_max<32>(run_m[j]);
+        const float s = group_sum<32>(run_m[j] == kNegInf ? run_s[j] : run_s[j] * exp2_approx((run_m[j] - m) * kLog2e));
+        const int token = half * kCols + j;
+        if (lane == 0 && half * kCols < TN && token < p.cols)
+          p.part[((p.part0 + first_tile) * 8 + rank * 4 + quarter) * p.part_ld + token] = make_float2(m, s);
+      }
+    }
   }
   __syncwarp();
   if (__syncthreads_or(failed)) {
@@ -421,7 +474,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   tcgen05_fence_before();
   cluster_sync_all();
   tcgen05_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) tmem_dealloc_pair(tmem, kColumns);
 }
 
 }  // namespace qk
