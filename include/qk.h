@@ -384,8 +384,8 @@ QK_API qk_status qk_rmsnorm_quant_fwd(const void* x, const void* residual, const
  *   (may be NULL; NaN when no row counts, so also when M == 0).
  *   workspace  at least qk_linear_xent_fwd_workspace_size() bytes of device
  *              memory, 256-byte aligned, scratch.
- *   M, V, K at most 2^31 - 1.  Products and sums are float32; float32 inputs
- *   are multiplied as sums of bfloat16 parts whose error is below float32's.
+ *   M, V, K at most 2^31 - 16.  Sums are float32; float32 inputs are multiplied
+ *   as sums of three bfloat16 parts, whose error is below float32's own.
  *   A NaN or infinity in h or w makes the losses NaN or infinite; which of
  *   the two is not specified for infinities.
  *   The buffers must not overlap (h and w may be read by both).

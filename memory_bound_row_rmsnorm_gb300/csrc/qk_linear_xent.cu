@@ -26,7 +26,7 @@
 namespace qk {
 namespace {
 
-constexpr int64_t kMaxDim = INT32_MAX;
+constexpr int64_t kMaxDim = INT32_MAX - 15;  // TMA coordinates, and rows padded to 8, are 32-bit
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece
 constexpr int64_t kStageCopyBytes = int64_t(64) << 20;  // copied or split weights of one piece
 constexpr int kPairs = 76;  // CTA pairs of a GB300
@@ -44,33 +44,50 @@ int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 // ---------------------------------------------------------------------------
 
 // Rows of T into rows of bf16 planes whose row length is a multiple of 8 (what
-// TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.
+// TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.  A
+// thread takes 8 columns of a row; what lies behind the last column is written
+// but read by nobody.
 template <typename T>
-__global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, int64_t cols, __nv_bfloat16* out,
-                                                     int64_t ld, int64_t plane_stride) {
+__global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, int32_t cols, __nv_bfloat16* out,
+                                                     int32_t ld, int64_t plane_stride) {
   grid_dependency_wait();
   allow_dependent_launch();
-  for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < rows * cols; e += int64_t(gridDim.x) * 256) {
-    const int64_t i = e / cols, j = e % cols;
+  const uint32_t per_row = uint32_t(ld) / 8;
+  for (int64_t i0 = blockIdx.x; i0 * 256 < rows * per_row; i0 += gridDim.x) {
+    const int64_t unit = i0 * 256 + threadIdx.x, i = unit / per_row;
+    if (i >= rows) return;
+    const int32_t j = int32_t(unit - i * per_row) * 8;
+    const T* src = in + i * cols + j;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = j + e < cols ? Vec16<T>::load1(src + e) : 0.f;
+    uint4* dst = reinterpret_cast<uint4*>(out + i * ld + j);
     if constexpr (sizeof(T) == 2) {
-      out[i * ld + j] = in[e];
+      *dst = Vec16<__nv_bfloat16>::pack(f);
     } else {
-      __nv_bfloat16 b[3];
-      split3(in[e], b);
-      for (int pl = 0; pl < 3; ++pl) out[pl * plane_stride + i * ld + j] = b[pl];
+      __nv_bfloat16 b[8][3];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split3(f[e], b[e]);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __bfloat162float(b[e][pl]);
+        dst[pl * (plane_stride / 8)] = Vec16<__nv_bfloat16>::pack(x);
+      }
     }
   }
 }
 
 // Joins a row's n pairs, in a fixed order.  ROW_LANES: lanes are rows and the
-// CTA's warps take every eighth pair, four loads in flight.  Otherwise (few
+// CTA's 32 warps take every 32nd pair, four loads in flight.  Otherwise (few
 // rows) a warp is a row and its lanes take every 32nd pair.
 template <bool ROW_LANES>
-__global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t part_ld, int64_t n,
+__global__ void __launch_bounds__(ROW_LANES ? 1024 : 256) join_kernel(const float2* part, int64_t part_ld, int64_t n,
                                                    const float* at_target, const int64_t* targets, int64_t M,
                                                    int64_t V, int has_ignore, int64_t ignore_index, float z,
                                                    float* loss, float* lse) {
-  __shared__ float2 red[8][33];
+  __shared__ float2 red[ROW_LANES ? 32 : 1][33];
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -82,7 +99,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t p
         (b.x == kNegInf ? b.y : b.y * exp2_approx((b.x - mn) * kLog2e));
     m = mn;
   };
-  constexpr int kStep = ROW_LANES ? 8 : 32, kDepth = 4;
+  constexpr int kStep = 32, kDepth = 4;
   if (row < M) {
     for (int64_t t = ROW_LANES ? warp : lane; t < n; t += kDepth * kStep) {
       float2 b[kDepth];
@@ -98,7 +115,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float2* part, int64_t p
     __syncthreads();
     if (warp != 0 || row >= M) return;
     m = kNegInf, s = 0.f;
-    for (int i = 0; i < 8; ++i) fold(red[i][lane]);
+    for (int i = 0; i < 32; ++i) fold(red[i][lane]);
   } else {
     const float mx = group_max<32>(m);
     s = group_sum<32>(m == kNegInf ? s : s * exp2_approx((m - mx) * kLog2e));
@@ -147,17 +164,38 @@ __global__ void __launch_bounds__(1024) rows_kernel(const int64_t* targets, cons
   }
 }
 
-// dh from its fp32 sums: the splits in order, rounded once.
+// dh from its fp32 sums: the splits in order, rounded once.  A thread takes 4
+// columns of a row (the sums' rows are multiples of 8).
 template <typename T>
-__global__ void __launch_bounds__(256) finish_kernel(const float* sum, int64_t ld, int64_t split_stride, int splits,
-                                                     T* out, int64_t rows, int64_t cols) {
+__global__ void __launch_bounds__(256) finish_kernel(const float* sum, int32_t ld, int64_t split_stride, int splits,
+                                                     T* out, int64_t rows, int32_t cols) {
   grid_dependency_wait();
   allow_dependent_launch();
-  for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < rows * cols; e += int64_t(gridDim.x) * 256) {
-    const float* s = sum + e / cols * ld + e % cols;
-    float v = s[0];
-    for (int k = 1; k < splits; ++k) v += s[k * split_stride];
-    Vec16<T>::store1(out + e, v);
+  const uint32_t per_row = uint32_t(ld) / 4;
+  for (int64_t i0 = blockIdx.x; i0 * 256 < rows * per_row; i0 += gridDim.x) {
+    const int64_t unit = i0 * 256 + threadIdx.x, i = unit / per_row;
+    if (i >= rows) return;
+    const int32_t j = int32_t(unit - i * per_row) * 4;
+    const float4* s = reinterpret_cast<const float4*>(sum + i * ld + j);
+    float4 v = s[0];
+    for (int k = 1; k < splits; ++k) {
+      const float4 x = s[k * (split_stride / 4)];
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    T* o = out + i * cols + j;
+    if (cols % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0) {
+      if (j >= cols) continue;
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(Vec16<T>::pack2(f[0], f[1]), Vec16<T>::pack2(f[2], f[3]));
+      } else {
+        *reinterpret_cast<float4*>(o) = v;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < cols) Vec16<T>::store1(o + e, f[e]);
+    }
   }
 }
 
@@ -330,6 +368,11 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));
   p.n_tiles = int32_t(ceil_div(cols, TN));
+  // The last column tile as a product of the columns it has: halves of whole
+  // 8-row groups of B (64-column boxes where B is MN-major).
+  const int64_t rest = cols - int64_t(p.n_tiles - 1) * TN, unit = B_MN ? 128 : 32;
+  p.last_n = TN < 256 ? TN : int32_t(std::min<int64_t>(TN, round_up(rest, unit)));
+  p.n_full = p.last_n == TN ? p.n_tiles : p.n_tiles - 1;
   const int64_t total = int64_t(p.steps) * (p.planes == 3 ? 6 : 1);
   if (total > INT32_MAX) return QK_ERR_UNSUPPORTED;
   p.split_steps = splits == 1 ? int32_t(total) : split_steps;
@@ -374,8 +417,8 @@ qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int
   *o = {src, c.K, rows, c.K, 1, 0};
   if (!copied) return QK_OK;
   *o = {at, c.K, rows, l.kp, l.planes, rows * l.kp};
-  return launch_pdl(planes_kernel<T>, dim3(blocks(c, rows * c.K)), 256, 0, c.stream, src, rows, c.K,
-                    reinterpret_cast<__nv_bfloat16*>(at), l.kp, rows * l.kp);
+  return launch_pdl(planes_kernel<T>, dim3(blocks(c, rows * l.kp / 8)), 256, 0, c.stream, src, rows, int32_t(c.K),
+                    reinterpret_cast<__nv_bfloat16*>(at), int32_t(l.kp), rows * l.kp);
 }
 
 template <typename T>
@@ -407,7 +450,7 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
   }
   if (st != QK_OK) return st;
   return launch_pdl(c.M > kFewTokens ? join_kernel<true> : join_kernel<false>,
-                    dim3(unsigned(ceil_div(c.M, c.M > kFewTokens ? 32 : 8))), 256, 0, c.stream, p.part, p.part_ld,
+                    dim3(unsigned(ceil_div(c.M, c.M > kFewTokens ? 32 : 8))), c.M > kFewTokens ? 1024 : 256, 0, c.stream, p.part, p.part_ld,
                     pairs, p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
 }
 
@@ -452,8 +495,8 @@ qk_status backward(const Call& c, int dtype, const float* lse, const float* dlos
     }
   }
   if (st != QK_OK || dh == nullptr || direct) return st;
-  return launch_pdl(finish_kernel<T>, dim3(blocks(c, c.M * c.K)), 256, 0, c.stream, sum, l.kp, c.M * l.kp, l.splits,
-                    static_cast<T*>(dh), c.M, c.K);
+  return launch_pdl(finish_kernel<T>, dim3(blocks(c, c.M * l.kp / 4)), 256, 0, c.stream, sum, int32_t(l.kp),
+                    c.M * l.kp, l.splits, static_cast<T*>(dh), c.M, int32_t(c.K));
 }
 
 // Bytes that these sizes may need, whichever way the pointers are aligned.

@@ -59,6 +59,7 @@ struct ProductArgs {
   int32_t steps;             // steps of 64 k in one plane pair
   int32_t planes;            // 1 (bf16) or 3 (float32)
   int32_t m_tiles, n_tiles;
+  int32_t n_full, last_n;    // column tiles of TN columns (the first ones); columns of a product in the last
   int32_t splits, split_steps;  // the k axis in pieces of split_steps steps
   uint64_t timeout_ns;
   int* status;
@@ -115,16 +116,25 @@ __device__ __forceinline__ void rows_out(uint32_t buf, int lane, const uint4* u,
 // Tile number -> (split, row tile, column tile).  Eight row tiles are walked
 // together: the pairs that run at one time then share their operands in L2
 // (76 pairs: 8 row tiles x 9.5 column tiles, a quarter of the loads unique).
+// A last column tile of fewer columns comes after all others, as a narrower
+// product: what is short goes where the last wave has room.
 // 32-bit: the host refuses more tiles (64-bit divisions cost a thousand cycles
 // a tile, which shows where a tile is a step or two).
 struct TileAt {
   int split, m, n;
 };
 __device__ __forceinline__ TileAt tile_at(const ProductArgs& p, uint32_t t) {
-  const uint32_t per = uint32_t(p.m_tiles) * uint32_t(p.n_tiles), band = 8u * uint32_t(p.n_tiles);
   TileAt r;
+  const uint32_t full = uint32_t(p.n_full), per = uint32_t(p.m_tiles) * full, all = per * uint32_t(p.splits);
+  if (t >= all) {
+    const uint32_t in = t - all;
+    r.split = int(in / uint32_t(p.m_tiles));
+    r.m = int(in - uint32_t(r.split) * uint32_t(p.m_tiles));
+    r.n = int(full);
+    return r;
+  }
   r.split = p.splits == 1 ? 0 : int(t / per);
-  const uint32_t in = t - uint32_t(r.split) * per, group = in / band, rest = in - group * band;
+  const uint32_t in = t - uint32_t(r.split) * per, band = 8u * full, group = in / band, rest = in - group * band;
   const uint32_t wide = min(8u, uint32_t(p.m_tiles) - group * 8u);
   r.n = int(rest / wide);
   r.m = int(group * 8u + rest - uint32_t(r.n) * wide);
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
   bool failed = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (mbar_wait<true>(bar, parity, p.timeout_ns)) return true;
+    if (mbar_wait<false>(bar, parity, p.timeout_ns)) return true;
     report_status(p.status, 5);
     failed = true;
     return false;
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t turn = 0;
     for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
-      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * half_n;
+      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * (at.n < p.n_full ? half_n : p.last_n / 2);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       for (int s = s0; s < s1; ++s, ++q) {
         if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
@@ -231,10 +241,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // barriers count those of both CTAs.
     if (failed && rank == 0)
       for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
-        mbar_wait<true>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
+        mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products of both CTAs ----
-    constexpr uint32_t idesc = instruction_desc(A_MN, B_MN, TN);
     constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
     constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
     int st = 0;
@@ -242,6 +251,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+      const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
       for (int c0 = s0; c0 < s1 && !failed; c0 += kChunkSteps, ++it) {
         const uint32_t acc = it & 1u;
         if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
@@ -282,6 +292,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         run_t[j] = tg >= p.v0 && tg < p.v0 + p.rows ? int(tg - p.v0) : -1;
       }
     }
+    float factor = 1.f;
+    if constexpr (EPI == kEpiAccum || EPI == kEpiStore) factor = *p.scale;
     uint32_t it = 0;
     for (uint32_t t = first_tile; t < tiles && !failed && half * kCols < TN; t += tile_step) {
       const TileAt at = tile_at(p, t);
@@ -291,6 +303,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const bool live = i < p.rows;
       const int rows_left = int(min(int64_t(32), p.rows - (i - lane)));  // this warp's rows of C, may be <= 0
       const int width = int(min(int64_t(kCols), p.cols - j0));  // this half's columns of C, may be <= 0
+
+      // What the outputs need of the row, asked for while the sums are formed.
+      XentRow row = {0.f, 0.f, 0.f, -2};
+      int64_t row_target = -1;
+      if constexpr (EPI == kEpiGrad) {
+        if (live) row = p.row[i];
+      }
+      if constexpr (EPI == kEpiLse) {
+        if (live) row_target = p.targets[i];
+      }
 
       float v[kCols];
       for (int c0 = s0; c0 < s1; c0 += kChunkSteps, ++it) {
@@ -335,8 +357,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       } else if constexpr (EPI == kEpiLse) {
         // (maximum, sum of exponentials) of the half row; columns past the last count as -inf
         if (!live) continue;
-        const int64_t target = p.targets[i] - p.v0 - j0;
-        if (target >= 0 && target < width) {
+        const int64_t target = row_target - p.v0 - j0;
+        if (row_target >= 0 && target >= 0 && target < width) {
           float x = 0.f;
 #pragma unroll
           for (int j = 0; j < kCols; ++j)  // as PTX: in C++ it becomes an indexed load, and v leaves the registers
@@ -361,7 +383,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (EPI == kEpiGrad) {
         if (width <= 0) continue;
-        const XentRow row = live ? p.row[i] : XentRow{0.f, 0.f, 0.f, -2};
         const int64_t at_t = row.target >= 0 ? row.target - p.v0 - j0 : -1;
         const int target = at_t >= 0 && at_t < width ? int(at_t) : -1;
 #pragma unroll
@@ -396,7 +417,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       } else if constexpr (EPI == kEpiAccum) {
         if (width <= 0) continue;
-        const float factor = *p.scale;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) v[j] *= factor;
         float* out = static_cast<float*>(p.out) + (int64_t(at.split) * p.rows + (i - lane)) * p.ld + j0;
@@ -426,7 +446,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (width <= 0) continue;
         T* out = static_cast<T*>(p.out) + (i - lane) * p.ld + j0;
         constexpr int E = Vec16<T>::kElems;
-        const float factor = *p.scale;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) v[j] *= factor;
 #pragma unroll

@@ -29,9 +29,11 @@ __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// One arrival on a barrier of any CTA of the cluster (a shared::cluster address).
+// One arrival on a barrier of any CTA of the cluster (a shared::cluster
+// address).  It tells that registers were loaded, which needs no release beyond
+// this CTA: at cluster scope it would wait for the thread's global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // TMEM columns for the pair: the same warp of both CTAs allocates and frees.
