@@ -113,6 +113,36 @@ __device__ __forceinline__ void rows_out(uint32_t buf, int lane, const uint4* u,
   __syncwarp();
 }
 
+// The same for rows that start off 16 bytes: put(row, column, x) gets single
+// elements, a warp's lanes on consecutive columns of one row.
+template <typename T, typename F>
+__device__ __forceinline__ void elements_out(uint32_t buf, int lane, const uint4* u, F put) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((k ^ (lane & 7)) * 16)),
+                 "r"(u[k].x), "r"(u[k].y), "r"(u[k].z), "r"(u[k].w)
+                 : "memory");
+  __syncwarp();
+#pragma unroll 8
+  for (int row = 0; row < 32; ++row) {
+#pragma unroll
+    for (int col = lane; col < int(128 / sizeof(T)); col += 32) {
+      const uint32_t byte = uint32_t(col) * sizeof(T);
+      const uint32_t at = buf + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15u);
+      if constexpr (sizeof(T) == 4) {
+        float x;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+        put(row, col, x);
+      } else {
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+        put(row, col, __ushort_as_bfloat16(x));
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // Tile number -> (split, row tile, column tile).  Eight row tiles are walked
 // together: the pairs that run at one time then share their operands in L2
 // (76 pairs: 8 row tiles x 9.5 column tiles, a quarter of the loads unique).
@@ -385,11 +415,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (width <= 0) continue;
         const int64_t at_t = row.target >= 0 ? row.target - p.v0 - j0 : -1;
         const int target = at_t >= 0 && at_t < width ? int(at_t) : -1;
+        // g = dloss (zf exp(x - lse) - onehot): three operations a column, and the
+        // one-hot's only in a warp that holds a target here.
+        const float f = row.zf * row.g, lb = -row.lse * kLog2e;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
-          float g = exp2_approx((v[j] - row.lse) * kLog2e) * row.zf;
-          if (j == target) g -= 1.f;
-          v[j] = row.target == -2 ? 0.f : g * row.g;
+          // bf16: one fused step (lse log2(e) is rounded, 2^-20 of p); float32 subtracts first
+          const float e = sizeof(T) == 2 ? fmaf(v[j], kLog2e, lb) : (v[j] - row.lse) * kLog2e;
+          v[j] = exp2_approx(e) * f;
+        }
+        if (__any_sync(0xffffffffu, target >= 0)) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j == target) v[j] -= row.g;
+        }
+        if (row.target == -2) {  // ignored: zero, whatever its logits are
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = 0.f;
         }
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (i - lane) * p.ld + j0;
 #pragma unroll
@@ -454,19 +496,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           uint4 u[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) u[k] = Vec16<T>::pack(v + c + E * k);
-          rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
-            const int col = c + unit * E;
-            if (r >= rows_left || col >= width) return;
-            T* o = out + r * p.ld + col;
-            if (p.vec) {
-              *reinterpret_cast<uint4*>(o) = x;
-            } else {  // rows that start off 16 bytes, or end inside a vector
-              const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-              for (int k = 0; k < E; ++k)
-                if (col + k < width) o[k] = e[k];
-            }
-          });
+          if (p.vec) {
+            rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+              const int col = c + unit * E;
+              if (r < rows_left && col < width) *reinterpret_cast<uint4*>(out + r * p.ld + col) = x;
+            });
+          } else {  // rows that start off 16 bytes, or end inside a vector
+            elements_out<T>(buf, lane, u, [&](int r, int k, T x) {
+              if (r < rows_left && c + k < width) out[r * p.ld + c + k] = x;
+            });
+          }
         }
       }
     }
