@@ -79,6 +79,36 @@ __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, 
   }
 }
 
+// A plane's rows [rows][ld_in] into [cols][ld_out], 64 x 64 elements a CTA.
+__global__ void __launch_bounds__(256) transpose_kernel(const uint16_t* in, int64_t rows, int64_t cols, int64_t ld_in,
+                                                        int64_t plane_in, uint16_t* out, int64_t ld_out,
+                                                        int64_t plane_out) {
+  __shared__ uint16_t tile[64][66];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t r0 = int64_t(blockIdx.x) * 64, c0 = int64_t(blockIdx.y) * 64;
+  in += blockIdx.z * plane_in;
+  out += blockIdx.z * plane_out;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;  // two elements of a row
+#pragma unroll
+  for (int i = y; i < 64; i += 8) {
+    const int64_t r = r0 + i, c = c0 + 2 * x;
+    // ld_in is a multiple of 8 elements and so is the base: pairs are aligned
+    uint32_t v = 0;
+    if (r < rows && c < cols) v = *reinterpret_cast<const uint32_t*>(in + r * ld_in + c);
+    tile[i][2 * x] = uint16_t(v);
+    tile[i][2 * x + 1] = uint16_t(v >> 16);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = y; i < 64; i += 8) {
+    const int64_t c = c0 + i, r = r0 + 2 * x;
+    if (c < cols && r < ld_out)
+      *reinterpret_cast<uint32_t*>(out + c * ld_out + r) =
+          uint32_t(tile[2 * x][i]) | uint32_t(tile[2 * x + 1][i]) << 16;
+  }
+}
+
 // Joins a row's n pairs, in a fixed order.  ROW_LANES: lanes are rows and the
 // CTA's 32 warps take every 32nd pair, four loads in flight.  Otherwise (few
 // rows) a warp is a row and its lanes take every 32nd pair.
@@ -209,7 +239,8 @@ struct Layout {
   int64_t ld_g;        // row length of g
   int splits, split_steps;  // k splits of dh's product
   // byte offsets
-  int64_t h, w, part, at_target, row, scale, g, sum, total;
+  int64_t h, w, part, at_target, row, scale, g, sum, ht, total;
+  bool turned;         // dw's product reads h as [K][M]
 };
 
 // Launches are waves of kPairs tiles; a wave takes as long as its tiles have
@@ -274,6 +305,13 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     l.part = take(pairs * M * 8);
     l.at_target = take(M * 4);
   } else {
+    // dw = g^T h reads both operands MN-major, at which the tensor cores run
+    // slower than on K-major ones.  A copy of h as [K][M] makes one of them
+    // K-major: 5680 -> 5363 us at 8192 x 131072 x 4096, 1509 -> 1430 at 8192 x
+    // 32000 x 4096, but 66 -> 68 at 1001 x 50257 x 768, where the copy costs what
+    // it gains.
+    l.turned = double(M) * double(V) * double(K) > 1e11;
+    if (l.turned) l.ht = take(l.planes * K * round_up(M, 8) * 2);
     l.row = take(M * int64_t(sizeof(XentRow)));
     l.scale = take(4);
     l.ld_g = round_up(l.piece, 8);
@@ -462,10 +500,17 @@ qk_status backward(const Call& c, int dtype, const float* lse, const float* dlos
   float* scale = reinterpret_cast<float*>(c.ws + l.scale);
   float* sum = reinterpret_cast<float*>(c.ws + l.sum);
   const bool direct = l.piece >= c.V && l.splits == 1;  // dh is complete in one product
-  Operand h, w;
+  Operand h, w, ht = {};
   qk_status st = launch_pdl(rows_kernel, dim3(1), 1024, 0, c.stream, c.targets, lse, dloss, c.M, c.V, c.has_ignore,
                             c.ignore, c.z, row, scale);
   if (st == QK_OK) st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
+  if (st == QK_OK && dw != nullptr && l.turned) {
+    const int64_t ld = round_up(c.M, 8);
+    ht = {c.ws + l.ht, c.M, c.K, ld, l.planes, c.K * ld};
+    st = launch_pdl(transpose_kernel, dim3(unsigned(ceil_div(c.M, 64)), unsigned(ceil_div(c.K, 64)), unsigned(l.planes)),
+                    256, 0, c.stream, static_cast<const uint16_t*>(h.base), c.M, c.K, h.ld, h.plane_stride,
+                    reinterpret_cast<uint16_t*>(c.ws + l.ht), ld, c.K * ld);
+  }
   for (int64_t v0 = 0; v0 < c.V && st == QK_OK; v0 += l.piece) {
     const int64_t width = std::min(l.piece, c.V - v0);
     st = operand(c, l, copied, static_cast<const T*>(c.w) + v0 * c.K, width, c.ws + l.w, &w);
@@ -480,21 +525,31 @@ qk_status backward(const Call& c, int dtype, const float* lse, const float* dlos
     p = ProductArgs{};
     p.scale = scale;
     if (st == QK_OK && dh != nullptr) {
-      p.out = direct ? dh : sum;
-      p.ld = direct ? c.K : l.kp;
       p.vec = aligned16(dh) && c.K * int64_t(sizeof(T)) % 16 == 0;
-      p.first = v0 == 0;
-      st = direct ? launch_product<kEpiStore, false, true, T>(c, p, g, w, c.M, c.K, width, 1, 0)
-                  : launch_product<kEpiAccum, false, true, float>(c, p, g, w, c.M, c.K, width, l.splits, l.split_steps);
+      const bool last = l.splits == 1 && v0 + width == c.V;
+      if (direct || last) {  // complete: rounded into dh
+        p.out = dh;
+        p.ld = c.K;
+        p.sum = sum;
+        p.sum_ld = l.kp;
+        st = direct ? launch_product<kEpiStore, false, true, T>(c, p, g, w, c.M, c.K, width, 1, 0)
+                    : launch_product<kEpiFinish, false, true, T>(c, p, g, w, c.M, c.K, width, 1, 0);
+      } else {
+        p.out = sum;
+        p.ld = l.kp;
+        p.first = v0 == 0;
+        st = launch_product<kEpiAccum, false, true, float>(c, p, g, w, c.M, c.K, width, l.splits, l.split_steps);
+      }
     }
     if (st == QK_OK && dw != nullptr) {
       p.out = static_cast<T*>(dw) + v0 * c.K;
       p.ld = c.K;
       p.vec = aligned16(dw) && c.K * int64_t(sizeof(T)) % 16 == 0;
-      st = launch_product<kEpiStore, true, true, T>(c, p, g, h, width, c.K, c.M, 1, 0);
+      st = l.turned ? launch_product<kEpiStore, true, false, T>(c, p, g, ht, width, c.K, c.M, 1, 0)
+                    : launch_product<kEpiStore, true, true, T>(c, p, g, h, width, c.K, c.M, 1, 0);
     }
   }
-  if (st != QK_OK || dh == nullptr || direct) return st;
+  if (st != QK_OK || dh == nullptr || l.splits == 1) return st;
   return launch_pdl(finish_kernel<T>, dim3(blocks(c, c.M * l.kp / 4)), 256, 0, c.stream, sum, int32_t(l.kp),
                     c.M * l.kp, l.splits, static_cast<T*>(dh), c.M, int32_t(c.K));
 }

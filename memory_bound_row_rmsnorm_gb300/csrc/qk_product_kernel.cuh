@@ -39,7 +39,8 @@ constexpr int kABytes = 128 * kStepK * 2;  // one CTA's part of a step of A
 constexpr int kOutBytes = 32 * 128;        // an epilogue warp's 32 rows of 128 bytes on their way out
 
 // kEpiLseCols: C's columns are the tokens (few), its rows the vocabulary.
-enum Epilogue : int { kEpiLse = 0, kEpiGrad = 1, kEpiAccum = 2, kEpiStore = 3, kEpiLseCols = 4 };
+// kEpiFinish: the last addition to fp32 sums, rounded to the output.
+enum Epilogue : int { kEpiLse = 0, kEpiGrad = 1, kEpiAccum = 2, kEpiStore = 3, kEpiLseCols = 4, kEpiFinish = 5 };
 
 // Shared memory by the tile's columns TN: six stages of 32 KB, or ten of A's
 // 16 KB and B's TN / 2 rows when that is little, and the way out.
@@ -74,6 +75,8 @@ struct ProductArgs {
   void* out;                 // grad: bf16 [planes][rows][ld]; accum: fp32 [splits][rows][ld]; store: [rows][ld]
   int64_t ld, plane_stride;  // elements
   int32_t first;             // accum: overwrite
+  const float* sum;          // finish: fp32 [rows][sum_ld]
+  int64_t sum_ld;
   int32_t vec;               // store: rows start on 16 bytes
   const float* scale;        // accum, store: factor (device)
 };
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
     }
     float factor = 1.f;
-    if constexpr (EPI == kEpiAccum || EPI == kEpiStore) factor = *p.scale;
+    if constexpr (EPI == kEpiAccum || EPI == kEpiStore || EPI == kEpiFinish) factor = *p.scale;
     uint32_t it = 0;
     for (uint32_t t = first_tile; t < tiles && !failed && half * kCols < TN; t += tile_step) {
       const TileAt at = tile_at(p, t);
@@ -481,6 +484,39 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                            "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)),
                            "f"(__uint_as_float(x.w))
                            : "memory");
+            }
+          });
+        }
+      } else if constexpr (EPI == kEpiFinish) {
+        if (width <= 0) continue;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) v[j] *= factor;
+        const float* sum = p.sum + (i - lane) * p.sum_ld + j0;
+        T* out = static_cast<T*>(p.out) + (i - lane) * p.ld + j0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          if (c >= width) break;
+          uint4 u[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) u[k] = Vec16<float>::pack(v + c + 4 * k);
+          rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+            const int col = c + unit * 4;
+            if (r >= rows_left || col >= width) return;  // sum_ld is a multiple of 4
+            const float4 y = *reinterpret_cast<const float4*>(sum + r * p.sum_ld + col);
+            float f[4];
+            Vec16<float>::unpack(x, f);
+            f[0] += y.x, f[1] += y.y, f[2] += y.z, f[3] += y.w;
+            T* o = out + r * p.ld + col;
+            if (p.vec) {
+              if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint2*>(o) = make_uint2(Vec16<T>::pack2(f[0], f[1]), Vec16<T>::pack2(f[2], f[3]));
+              } else {
+                *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col + e < width) Vec16<T>::store1(o + e, f[e]);
             }
           });
         }
