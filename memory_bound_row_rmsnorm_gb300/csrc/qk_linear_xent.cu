@@ -309,8 +309,10 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     // slower than on K-major ones.  A copy of h as [K][M] makes one of them
     // K-major: 5680 -> 5363 us at 8192 x 131072 x 4096, 1509 -> 1430 at 8192 x
     // 32000 x 4096, but 66 -> 68 at 1001 x 50257 x 768, where the copy costs what
-    // it gains.
-    l.turned = double(M) * double(V) * double(K) > 1e11;
+    // it gains.  And a K-major operand takes a last column tile of 32 columns
+    // where an MN-major one takes 128 (2047 x 8191 x 513).
+    const int64_t rest = K % kTileN;
+    l.turned = double(M) * double(V) * double(K) > 1e11 || (rest > 0 && rest <= 96);
     if (l.turned) l.ht = take(l.planes * K * round_up(M, 8) * 2);
     l.row = take(M * int64_t(sizeof(XentRow)));
     l.scale = take(4);
@@ -403,6 +405,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.rows = int32_t(rows);
   p.cols = int32_t(cols);
   p.planes = int32_t(a.planes);
+  p.depth = int32_t(depth);
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));
   p.n_tiles = int32_t(ceil_div(cols, TN));

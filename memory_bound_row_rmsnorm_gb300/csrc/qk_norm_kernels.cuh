@@ -54,6 +54,12 @@ __device__ __forceinline__ uint32_t quantise(float v, int qtype) {
   return uint32_t(max(-127, min(127, __float2int_rn(v)))) & 0xffu;  // NaN converts to 0
 }
 
+// Two of them, the first in the low byte.
+__device__ __forceinline__ uint32_t quantise2(float a, float b, int qtype) {
+  if (qtype == 0) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  return quantise(a, 1) | quantise(b, 1) << 8;
+}
+
 // x + r rounded to the rows' type, as a float.
 template <typename T>
 __device__ __forceinline__ float rounded_sum(float x, float r) {

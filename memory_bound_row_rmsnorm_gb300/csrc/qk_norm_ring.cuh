@@ -29,12 +29,14 @@ struct Unit {
   __device__ __forceinline__ static void store(void* p, int64_t i, const Raw& r) {
     __stcs(static_cast<uint4*>(p) + i, r);
   }
-  __device__ __forceinline__ static void store8(void* p, int64_t i, const uint32_t* q) {
+  // E values in 8 bits, as unit i of a row of bytes.
+  __device__ __forceinline__ static void store8(void* p, int64_t i, const float* f, int qtype) {
+    const uint32_t lo = quantise2(f[0], f[1], qtype) | quantise2(f[2], f[3], qtype) << 16;
     if constexpr (E == 8) {
-      __stcs(static_cast<uint2*>(p) + i, make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                                    q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24));
+      const uint32_t hi = quantise2(f[4], f[5], qtype) | quantise2(f[6], f[7], qtype) << 16;
+      __stcs(static_cast<uint2*>(p) + i, make_uint2(lo, hi));
     } else {
-      __stcs(static_cast<uint32_t*>(p) + i, q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24);
+      __stcs(static_cast<uint32_t*>(p) + i, lo);
     }
   }
 };
@@ -47,8 +49,8 @@ struct Unit<T, false> {
   __device__ __forceinline__ static void unpack(const Raw& r, float* f) { f[0] = float(r); }
   __device__ __forceinline__ static Raw pack(const float* f) { return T(f[0]); }
   __device__ __forceinline__ static void store(void* p, int64_t i, const Raw& r) { static_cast<T*>(p)[i] = r; }
-  __device__ __forceinline__ static void store8(void* p, int64_t i, const uint32_t* q) {
-    static_cast<uint8_t*>(p)[i] = uint8_t(q[0]);
+  __device__ __forceinline__ static void store8(void* p, int64_t i, const float* f, int qtype) {
+    static_cast<uint8_t*>(p)[i] = uint8_t(quantise(f[0], qtype));
   }
 };
 
@@ -231,21 +233,20 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         }
       } else {
         // Largest |y| of each unit, as bits: ordered like the numbers, infinity and NaN on top.
-        auto normed = [&](int k, float* f) {
-          float fw[E];
-          U::unpack(va[k], f);
-          U::unpack(wv[k], fw);
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = (f[e] * rs) * fw[e];
-        };
+        float yv[VPT * E];
         uint32_t um[VPT], rowm = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-          float f[E];
-          normed(k, f);
+          float* f = yv + k * E;
+          float fw[E];
+          U::unpack(va[k], f);
+          U::unpack(wv[k], fw);
           um[k] = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) um[k] = max(um[k], __float_as_uint(fabsf(f[e])));
+          for (int e = 0; e < E; ++e) {
+            f[e] = (f[e] * rs) * fw[e];
+            um[k] = max(um[k], __float_as_uint(fabsf(f[e])));
+          }
           rowm = max(rowm, um[k]);
         }
         if (a.group == 0) {
@@ -279,21 +280,27 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         }
         if (!row_ok) continue;
         uint8_t* qrow = static_cast<uint8_t*>(a.y) + row * N;
+        float* srow = a.scale + row * a.groups;
+        float s = 0.f, inv = 0.f;
+        const int shift = 31 - __clz(a.group);  // groups are powers of two
+        if (a.group == 0) {
+          s = scale_of(__uint_as_float(rowm), rowm >= 0x7f800000u, a.qtype);
+          inv = 1.f / s;
+          if (l == 0) srow[0] = s;
+        }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
           const int u = l + k * TPR;
           if (u >= NU) continue;
-          const uint32_t m = a.group == 0 ? rowm : um[k];
-          const float s = scale_of(__uint_as_float(m), m >= 0x7f800000u, a.qtype);
-          if (a.group == 0 ? u == 0 : (u * E) % a.group == 0)
-            a.scale[row * a.groups + (a.group == 0 ? 0 : u * E / a.group)] = s;
-          float f[E];
-          uint32_t qv[E];
-          normed(k, f);
-          const float inv = 1.f / s;
+          if (a.group != 0) {
+            s = scale_of(__uint_as_float(um[k]), um[k] >= 0x7f800000u, a.qtype);
+            inv = 1.f / s;
+            if (((u * E) & (a.group - 1)) == 0) srow[(u * E) >> shift] = s;
+          }
+          float* f = yv + k * E;
 #pragma unroll
-          for (int e = 0; e < E; ++e) qv[e] = quantise(f[e] * inv, a.qtype);
-          U::store8(qrow, u, qv);
+          for (int e = 0; e < E; ++e) f[e] *= inv;
+          U::store8(qrow, u, f, a.qtype);
         }
       }
     }

@@ -13,8 +13,9 @@
 // The tensor core adds to a sum by cutting off what does not fit, always toward
 // zero: a chain of n products of 16 k is short by about n 2^-25.5 of itself (a
 // sum over 8192 k measured 1e-5 off, where rounding to nearest gives 1e-6).  So
-// a chain ends after kChunkSteps * 64 = 512 k, and the chains of a tile are
-// added in registers, to nearest.
+// a chain ends after kChunkSteps * 64 = 1024 k, and the chains of a tile are
+// added in registers, to nearest.  (Shorter chains cost time and power: at 512 k
+// the backward of 8192 x 32000 x 4096 took 4.40 ms in a long run, at 1024 4.31.)
 //
 // An operand is stored with k innermost (K-major) or with its rows innermost
 // (MN-major): h, w and g serve as either, without a transposed copy.
@@ -34,7 +35,7 @@ constexpr int kProductThreads = 384;  // 4 warps that feed the tensor cores, 8 f
 constexpr int kTileM = 256;       // rows of a pair's tile
 constexpr int kTileN = 256;       // columns of one, where there are enough
 constexpr int kStepK = 64;        // k of one pipeline step: 128 bytes
-constexpr int kChunkSteps = 8;    // steps of one chain of products
+constexpr int kChunkSteps = 16;   // steps of one chain of products
 constexpr int kABytes = 128 * kStepK * 2;  // one CTA's part of a step of A
 constexpr int kOutBytes = 32 * 128;        // an epilogue warp's 32 rows of 128 bytes on their way out
 
@@ -58,6 +59,7 @@ struct XentRow {   // what the gradient needs of a row
 struct ProductArgs {
   int32_t rows, cols;        // of C
   int32_t steps;             // steps of 64 k in one plane pair
+  int32_t depth;             // k in one plane pair
   int32_t planes;            // 1 (bf16) or 3 (float32)
   int32_t m_tiles, n_tiles;
   int32_t n_full, last_n;    // column tiles of TN columns (the first ones); columns of a product in the last
@@ -231,10 +233,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     return false;
   };
 
-  // Registers: the launch holds 384 x 168 = 64512; 128 x 72 + 256 x 208 = 62464
+  // Registers: the launch holds 384 x 168 = 64512; 128 x 64 + 256 x 216 = 63488
   // of them go to the warps that feed and to those that keep sums.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each step's operands ----
     constexpr int half_n = TN / 2;
@@ -246,9 +248,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const TileAt at = tile_at(p, t);
       const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * (at.n < p.n_full ? half_n : p.last_n / 2);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+      int pair = s0 / p.steps, in_pair = s0 % p.steps;
       for (int s = s0; s < s1; ++s, ++q) {
         if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
-        const int pair = s / p.steps, k = (s % p.steps) * kStepK;
+        const int k = in_pair * kStepK;
         // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0): the small products first
         const int pa = pairs == 1 ? 0 : pair < 3 ? 2 - pair : pair == 3 ? 1 : 0;
         const int pb = pairs == 1 ? 0 : pair < 3 ? pair : pair == 4 ? 1 : 0;
@@ -268,6 +271,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tma_load_3d(db, &map_b, k, b0, pb, bar);
         }
         if (++st == kStages) st = 0, turn ^= 1u;
+        if (++in_pair == p.steps) in_pair = 0, ++pair;
       }
     }
     // A failed launch leaves once the loads in flight have landed: the leader's
@@ -279,12 +283,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // ---- products of both CTAs ----
     constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
     constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
+    const int tail_parts = (p.depth - (p.steps - 1) * kStepK + 15) / 16;
     int st = 0;
     uint32_t turn = 0, it = 0;  // it: chains begun
     for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
+      int in_pair = s0 % p.steps;
       for (int c0 = s0; c0 < s1 && !failed; c0 += kChunkSteps, ++it) {
         const uint32_t acc = it & 1u;
         if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
@@ -296,9 +302,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tcgen05_fence_after();
           const uint32_t sa = ring + uint32_t(st) * kStageBytes;
           const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
+          const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
+          if (tail) in_pair = 0;
+          if (tail && tail_parts < kStepK / 16) {
+            for (int k = 0; k < tail_parts; ++k)
+              mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+          } else {
 #pragma unroll
-          for (int k = 0; k < kStepK / 16; ++k)
-            mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+            for (int k = 0; k < kStepK / 16; ++k)
+              mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+          }
           mma_commit_pair(empty0 + 8 * st);
           if (++st == kStages) st = 0, turn ^= 1u;
         }
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- epilogue: half a row of the tile a thread ----
     const int quarter = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes of a warp: 32 (warp % 4) and up
     const uint32_t buf = ring + uint32_t(kStages * kStageBytes) + uint32_t(warp - 4) * kOutBytes;
