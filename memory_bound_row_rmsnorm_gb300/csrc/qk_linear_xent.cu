@@ -109,55 +109,92 @@ __global__ void __launch_bounds__(256) transpose_kernel(const uint16_t* in, int6
   }
 }
 
-// Joins a row's n pairs, in a fixed order.  ROW_LANES: lanes are rows and the
-// CTA's 32 warps take every 32nd pair, four loads in flight.  Otherwise (few
-// rows) a warp is a row and its lanes take every 32nd pair.
-template <bool ROW_LANES>
-__global__ void __launch_bounds__(ROW_LANES ? 1024 : 256) join_kernel(const float2* part, int64_t part_ld, int64_t n,
-                                                   const float* at_target, const int64_t* targets, int64_t M,
-                                                   int64_t V, int has_ignore, int64_t ignore_index, float z,
-                                                   float* loss, float* lse) {
-  __shared__ float2 red[ROW_LANES ? 32 : 1][33];
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = ROW_LANES ? int64_t(blockIdx.x) * 32 + lane : int64_t(blockIdx.x) * 8 + warp;
+// A row's (maximum, sum) of exponentials, joined from pairs in a fixed order.
+struct Joined {
   float m = kNegInf, s = 0.f;
-  auto fold = [&](float2 b) {  // an empty (-inf) side adds its sum, 0 or NaN
+  __device__ __forceinline__ void fold(float2 b) {  // an empty (-inf) side adds its sum, 0 or NaN
     const float mn = fmaxf(m, b.x);
     s = (m == kNegInf ? s : s * exp2_approx((m - mn) * kLog2e)) +
         (b.x == kNegInf ? b.y : b.y * exp2_approx((b.x - mn) * kLog2e));
     m = mn;
-  };
-  constexpr int kStep = 32, kDepth = 4;
-  if (row < M) {
-    for (int64_t t = ROW_LANES ? warp : lane; t < n; t += kDepth * kStep) {
-      float2 b[kDepth];
+  }
+  // Pairs t, t + 32, ... of n, four loads in flight.
+  __device__ __forceinline__ void fold_list(const float2* part, int64_t ld, int64_t row, int64_t t, int64_t n) {
+    for (; t < n; t += 4 * 32) {
+      float2 b[4];
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k)
-        b[k] = t + k * kStep < n ? part[(t + k * kStep) * part_ld + row] : make_float2(kNegInf, 0.f);
+      for (int k = 0; k < 4; ++k) b[k] = t + k * 32 < n ? part[(t + k * 32) * ld + row] : make_float2(kNegInf, 0.f);
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) fold(b[k]);
+      for (int k = 0; k < 4; ++k) fold(b[k]);
     }
   }
-  if constexpr (ROW_LANES) {
-    red[warp][lane] = make_float2(m, s);
-    __syncthreads();
-    if (warp != 0 || row >= M) return;
-    m = kNegInf, s = 0.f;
-    for (int i = 0; i < 32; ++i) fold(red[i][lane]);
-  } else {
-    const float mx = group_max<32>(m);
-    s = group_sum<32>(m == kNegInf ? s : s * exp2_approx((m - mx) * kLog2e));
-    m = mx;
-    if (lane != 0 || row >= M) return;
+};
+
+struct LossArgs {
+  const float2* part;
+  int64_t part_ld, n;  // n pairs a row
+  const float* at_target;
+  const int64_t* targets;
+  int64_t M, V;
+  int32_t has_ignore;
+  float z;
+  int64_t ignore_index;
+  float* loss;
+  float* lse;
+  float* mean;
+};
+__device__ __forceinline__ bool ignored(const LossArgs& a, int64_t t) { return a.has_ignore && t == a.ignore_index; }
+// Writes a row's lse and loss; returns the loss.
+__device__ __forceinline__ float put_loss(const LossArgs& a, int64_t row, const Joined& j) {
+  const float l = j.m + logf(j.s);
+  const int64_t t = a.targets[row];
+  const float loss = ignored(a, t)       ? 0.f
+                     : t >= 0 && t < a.V ? fmaf(a.z * l, l, l - a.at_target[row])
+                                         : __int_as_float(0x7fc00000);
+  if (a.lse != nullptr) a.lse[row] = l;
+  a.loss[row] = loss;
+  return loss;
+}
+
+// Lanes are rows and the CTA's 32 warps take every 32nd pair.
+__global__ void __launch_bounds__(1024) join_kernel(const LossArgs a) {
+  __shared__ float2 red[32][33];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = int64_t(blockIdx.x) * 32 + lane;
+  Joined j;
+  if (row < a.M) j.fold_list(a.part, a.part_ld, row, warp, a.n);
+  red[warp][lane] = make_float2(j.m, j.s);
+  __syncthreads();
+  if (warp != 0 || row >= a.M) return;
+  j = Joined{};
+  for (int i = 0; i < 32; ++i) j.fold(red[i][lane]);
+  put_loss(a, row, j);
+}
+
+// Few rows (at most 64), one CTA: a warp is a row, its lanes take every 32nd
+// pair; the mean over the rows that count follows at once.
+__global__ void __launch_bounds__(1024) join_few_kernel(const LossArgs a) {
+  __shared__ float loss[64];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t row = warp; row < a.M; row += 32) {
+    Joined j;
+    j.fold_list(a.part, a.part_ld, row, lane, a.n);
+    const float m = group_max<32>(j.m);
+    j.s = group_sum<32>(j.m == kNegInf ? j.s : j.s * exp2_approx((j.m - m) * kLog2e));
+    j.m = m;
+    if (lane == 0) loss[row] = put_loss(a, row, j);
   }
-  const float l = m + logf(s);
-  const int64_t t = targets[row];
-  if (lse != nullptr) lse[row] = l;
-  loss[row] = has_ignore && t == ignore_index ? 0.f
-              : t >= 0 && t < V               ? fmaf(z * l, l, l - at_target[row])
-                                              : __int_as_float(0x7fc00000);
+  __syncthreads();
+  if (a.mean == nullptr || threadIdx.x != 0) return;
+  float sum = 0.f;
+  int n = 0;
+  for (int64_t row = 0; row < a.M; ++row)
+    if (!ignored(a, a.targets[row])) sum += loss[row], ++n;
+  *a.mean = sum / float(n);  // 0 / 0 = NaN when every row is ignored
 }
 
 // What the gradient needs of each row.  g is dloss over the largest |dloss| of
@@ -301,7 +338,7 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
   }
   if (!bwd) {
     const int64_t pairs = M > kFewTokens ? 2 * ceil_div(V, kTileN)
-                                         : 8 * std::min<int64_t>(ceil_div(V, kTileM), kPairs * ceil_div(V, l.piece));
+                                         : 2 * std::min<int64_t>(ceil_div(V, kTileM), kPairs * ceil_div(V, l.piece));
     l.part = take(pairs * M * 8);
     l.at_target = take(M * 4);
   } else {
@@ -463,7 +500,7 @@ qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int
 }
 
 template <typename T>
-qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
+qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean) {
   const bool copied = !in_place(c.h, c.w, c.K, dtype);
   const Layout l = layout(false, c.M, c.V, c.K, dtype, copied);
   Operand h, w;
@@ -483,16 +520,20 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse) {
       st = launch_product<kEpiLse, false, false, __nv_bfloat16>(c, p, h, w, c.M, width, c.K, 1, 0);
       continue;
     }
-    p.part0 = pairs / 8;
+    p.part0 = pairs / 2;
     st = c.M <= 16   ? launch_product<kEpiLseCols, false, false, __nv_bfloat16, 16>(c, p, w, h, width, c.M, c.K, 1, 0)
          : c.M <= 32 ? launch_product<kEpiLseCols, false, false, __nv_bfloat16, 32>(c, p, w, h, width, c.M, c.K, 1, 0)
                      : launch_product<kEpiLseCols, false, false, __nv_bfloat16, 64>(c, p, w, h, width, c.M, c.K, 1, 0);
-    pairs += 8 * std::min<int64_t>(ceil_div(width, kTileM), std::min(kPairs, c.dev.sms / 2));
+    pairs += 2 * std::min<int64_t>(ceil_div(width, kTileM), std::min(kPairs, c.dev.sms / 2));
   }
   if (st != QK_OK) return st;
-  return launch_pdl(c.M > kFewTokens ? join_kernel<true> : join_kernel<false>,
-                    dim3(unsigned(ceil_div(c.M, c.M > kFewTokens ? 32 : 8))), c.M > kFewTokens ? 1024 : 256, 0, c.stream, p.part, p.part_ld,
-                    pairs, p.at_target, c.targets, c.M, c.V, c.has_ignore, c.ignore, c.z, loss, lse);
+  const LossArgs a = {p.part, p.part_ld, pairs, p.at_target, c.targets, c.M, c.V, c.has_ignore, c.z, c.ignore, loss, lse,
+                      mean};
+  if (c.M <= kFewTokens) return launch_pdl(join_few_kernel, dim3(1), 1024, 0, c.stream, a);
+  st = launch_pdl(join_kernel, dim3(unsigned(ceil_div(c.M, 32))), 1024, 0, c.stream, a);
+  if (st != QK_OK || mean == nullptr) return st;
+  return launch_pdl(xent_mean_kernel<0>, dim3(1), 1024, 0, c.stream, loss, c.targets, c.M, c.has_ignore, c.ignore,
+                    mean);
 }
 
 template <typename T>
@@ -620,8 +661,10 @@ qk_status qk_linear_xent_fwd(const void* h, const void* w, const int64_t* target
   st = current_device(&d);
   if (st != QK_OK) return st;
   const Call c = {h, w, targets, M, V, K, has_ignore, ignore, z, static_cast<char*>(workspace), stream, d};
-  if (M > 0) st = dtype == QK_F32 ? forward<float>(c, dtype, loss, lse) : forward<__nv_bfloat16>(c, dtype, loss, lse);
-  if (st != QK_OK || mean_loss == nullptr) return st;
+  if (M > 0)
+    return dtype == QK_F32 ? forward<float>(c, dtype, loss, lse, mean_loss)
+                           : forward<__nv_bfloat16>(c, dtype, loss, lse, mean_loss);
+  if (mean_loss == nullptr) return QK_OK;
   return launch_pdl(xent_mean_kernel<0>, dim3(1), 1024, 0, stream, loss, targets, M, has_ignore, ignore,
                     mean_loss);
 }

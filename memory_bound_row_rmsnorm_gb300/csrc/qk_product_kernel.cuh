@@ -181,11 +181,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const ProductArgs p) {
   constexpr int kStages = product_stages(TN), kStageBytes = product_stage_bytes(TN);
-  constexpr uint32_t kColumns = TN < 16 ? 32 : 2 * TN;  // TMEM: two sets of sums
+  // A product of few columns waits for the one before it on the same sums, some
+  // 125 cycles where its own work is 32; four sets of sums, one for each 16 k of
+  // a step, keep four under way.
+  constexpr int kParts = TN == kTileN ? 1 : 4, kSet = kParts * TN;
+  constexpr uint32_t kColumns = 2 * kSet;  // TMEM: two sets of sums, or of four times them
   static_assert(!B_MN || TN == kTileN, "MN-major B comes in boxes of 64 columns");
   extern __shared__ unsigned char dynamic_smem[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
   __shared__ uint32_t tmem_at;
+  __shared__ float2 joint[EPI == kEpiLseCols ? 4 : 1][EPI == kEpiLseCols ? TN : 1];
 
   // Columns of an epilogue thread, and the warps that take part.
   constexpr int kCols = TN / 2 < 16 ? 16 : TN / 2, kReaders = 4 * (TN / kCols);
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t acc = it & 1u;
         if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
         tcgen05_fence_after();
-        const uint32_t d = tmem + acc * TN;
+        const uint32_t d = tmem + acc * kSet;
         const int c1 = min(s1, c0 + kChunkSteps);
         for (int s = c0; s < c1; ++s) {
           if (!wait(full0 + 8 * st, turn)) break;
@@ -304,13 +309,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
           const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
           if (tail) in_pair = 0;
-          if (tail && tail_parts < kStepK / 16) {
+          if (kParts == 1 && tail && tail_parts < kStepK / 16) {
             for (int k = 0; k < tail_parts; ++k)
               mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
           } else {
 #pragma unroll
             for (int k = 0; k < kStepK / 16; ++k)
-              mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+              mma_bf16_pair(d + uint32_t(kParts == 1 ? 0 : k * TN), da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep,
+                            idesc, s > c0 || (kParts == 1 && k > 0));
           }
           mma_commit_pair(empty0 + 8 * st);
           if (++st == kStages) st = 0, turn ^= 1u;
@@ -365,9 +371,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t acc = it & 1u;
         if (!wait(done0 + 8 * acc, (it >> 1) & 1u)) break;
         tcgen05_fence_after();
-        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * TN + uint32_t(half * kCols);
+        const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * kSet + uint32_t(half * kCols);
         __syncwarp();  // the loads are the warp's
-        if (c0 == s0) {
+        if constexpr (kParts > 1) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            float x[kParts][16];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) tmem_load_16(src + uint32_t(k * TN + c), x[k]);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) tmem_load_wait(x[k]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float sum = (x[0][j] + x[1][j]) + (x[2][j] + x[3][j]);
+              v[c + j] = c0 == s0 ? sum : v[c + j] + sum;
+            }
+          }
+        } else if (c0 == s0) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 16) tmem_load_16(src + uint32_t(c), v + c);
 #pragma unroll
@@ -559,15 +579,24 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
     }
     if constexpr (EPI == kEpiLseCols) {
-      // One pair a warp and token: rows of the join's list are (pair of CTAs, CTA, warp).
+      // One pair a CTA and token: the lanes of each warp, then the four warps in order.
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const float m = group_max<32>(run_m[j]);
         const float s = group_sum<32>(run_m[j] == kNegInf ? run_s[j] : run_s[j] * exp2_approx((run_m[j] - m) * kLog2e));
-        const int token = half * kCols + j;
-        if (lane == 0 && half * kCols < TN && token < p.cols)
-          p.part[((p.part0 + first_tile) * 8 + rank * 4 + quarter) * p.part_ld + token] = make_float2(m, s);
+        if (lane == 0 && half * kCols < TN) joint[quarter][half * kCols + j] = make_float2(m, s);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight epilogue warps
+      const int token = int(threadIdx.x) - 128;
+      if (token < p.cols) {
+        float m = kNegInf, s = 0.f;
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, joint[k][token].x);
+        for (int k = 0; k < 4; ++k) {
+          const float2 b = joint[k][token];
+          s += b.x == kNegInf ? b.y : b.y * exp2_approx((b.x - m) * kLog2e);
+        }
+        p.part[((p.part0 + first_tile) * 2 + rank) * p.part_ld + token] = make_float2(m, s);
       }
     }
   }
