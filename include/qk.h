@@ -386,8 +386,9 @@ QK_API qk_status qk_rmsnorm_quant_fwd(const void* x, const void* residual, const
  *              memory, 256-byte aligned, scratch.
  *   M, V, K at most 2^31 - 16.  Sums are float32; float32 inputs are multiplied
  *   as sums of three bfloat16 parts, whose error is below float32's own.
- *   A NaN or infinity in h or w makes the losses NaN or infinite; which of
- *   the two is not specified for infinities.
+ *   A NaN or infinity in h or w makes the losses it reaches NaN or infinite;
+ *   which of the two is not specified for infinities, and float32 values beyond
+ *   bfloat16's largest (3.39e38) count as infinite.
  *   The buffers must not overlap (h and w may be read by both).
  */
 QK_API qk_status qk_linear_xent_fwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype,
@@ -411,7 +412,8 @@ QK_API qk_status qk_linear_xent_fwd(const void* h, const void* w, const int64_t*
  *              aligned, scratch.  It does not grow with M * V.
  *   bfloat16: g / max |dloss| is rounded to bfloat16 for the two products;
  *   their sums are float32 and the outputs are rounded once.  Results do not
- *   change from run to run.
+ *   change from run to run.  The h of an ignored row still takes part in dw,
+ *   times a g of zero: it has to be finite.
  */
 QK_API qk_status qk_linear_xent_bwd_workspace_size(int64_t M, int64_t V, int64_t K, qk_dtype dtype,
                                                    size_t* bytes);

@@ -14,6 +14,7 @@ their workspaces too.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -489,6 +490,12 @@ def _used_on(stream, *tensors):
                 t.record_stream(stream)
 
 
+@functools.lru_cache(maxsize=512)
+def _workspace_bytes(size, dev, *sizes):
+    """Bytes that a call of these sizes needs on device dev (`size`: its C function's wrapper)."""
+    return size(*sizes)
+
+
 def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, want_rstd: bool = True,
                     stream=None):
     """h = x + residual and its RMSNorm over the last dimension; returns
@@ -522,7 +529,7 @@ def add_rmsnorm_bwd(h, w, rstd, dy, dh=None, out=None, stream=None):
         _same("dh", dh, shape, dtype, dev)
     dx = torch.empty_like(h) if out is None else _same("out", out, shape, dtype, dev)
     dw = torch.empty(N, dtype=torch.float32, device=h.device)
-    nbytes = qk_add_rmsnorm_bwd_workspace_size(M, N, code)
+    nbytes = _workspace_bytes(qk_add_rmsnorm_bwd_workspace_size, dev, M, N, code)
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
     _check(load_library().qk_add_rmsnorm_bwd(
         h.data_ptr(), w.data_ptr(), rstd.data_ptr(), dy.data_ptr(), None if dh is None else dh.data_ptr(),
@@ -591,7 +598,7 @@ def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_l
     loss = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
     lse = torch.empty_like(loss) if want_lse else None
     mean = torch.empty((), dtype=torch.float32, device=h.device) if want_mean else None
-    nbytes = qk_linear_xent_fwd_workspace_size(M, V, K, code)
+    nbytes = _workspace_bytes(qk_linear_xent_fwd_workspace_size, dev, M, V, K, code)
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
     _check(load_library().qk_linear_xent_fwd(
         h.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr() if want_lse else None,
@@ -612,7 +619,7 @@ def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: f
         _same("dloss", dloss, h.shape[:-1], torch.float32, dev)
     dh = torch.empty_like(h) if want_dh else None
     dw = torch.empty_like(w) if want_dw else None
-    nbytes = qk_linear_xent_bwd_workspace_size(M, V, K, code)
+    nbytes = _workspace_bytes(qk_linear_xent_bwd_workspace_size, dev, M, V, K, code)
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
     _check(load_library().qk_linear_xent_bwd(
         h.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), None if dloss is None else dloss.data_ptr(),

@@ -349,7 +349,7 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
     // it gains.  And a K-major operand takes a last column tile of 32 columns
     // where an MN-major one takes 128 (2047 x 8191 x 513).
     const int64_t rest = K % kTileN;
-    l.turned = double(M) * double(V) * double(K) > 1e11 || (rest > 0 && rest <= 96);
+    l.turned = (double(M) * double(V) * double(K) > 1e11 || (rest > 0 && rest <= 96)) && K <= 65535 * 64;
     if (l.turned) l.ht = take(l.planes * K * round_up(M, 8) * 2);
     l.row = take(M * int64_t(sizeof(XentRow)));
     l.scale = take(4);
@@ -369,6 +369,7 @@ qk_status check_linear(int dtype, int64_t M, int64_t V, int64_t K) {
   if (dtype != QK_F32 && dtype != QK_BF16) return QK_ERR_INVALID_ARG;
   if (M < 0 || V <= 0 || K <= 0) return QK_ERR_INVALID_ARG;
   if (M > kMaxDim || V > kMaxDim || K > kMaxDim) return QK_ERR_UNSUPPORTED;
+  if (std::max(M, V) > INT64_MAX / 1024 / K) return QK_ERR_UNSUPPORTED;  // byte offsets fit int64
   return QK_OK;
 }
 
@@ -433,10 +434,15 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   static std::atomic<uint64_t> prepared{0};  // one bit a device
   const uint64_t bit = uint64_t(1) << (c.dev.index & 63);
   if (!(prepared.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem(TN)) != cudaSuccess) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem(TN)) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
       cudaGetLastError();
       return QK_ERR_LAUNCH;
     }
+    // The warps' register shares are taken from what the launch holds; a build
+    // that holds less would wait for the rest forever.
+    if (fa.numRegs * kProductThreads < kSplitRegisters) return QK_ERR_LAUNCH;
     prepared.fetch_or(bit, std::memory_order_acq_rel);
   }
   p.rows = int32_t(rows);

@@ -50,23 +50,25 @@ std::mutex g_norm_mu;
 std::map<std::tuple<int, const void*, int>, int> g_norm_occ;  // (device, kernel, smem) -> CTAs an SM
 
 // Resident CTAs an SM; opts the kernel into the device's shared memory first.
-qk_status norm_occupancy(const CurrentDevice& d, const void* func, int threads, int smem, int* out) {
+qk_status norm_occupancy(const CurrentDevice& d, const void* func, int threads, int smem, int* out) try {
   std::lock_guard<std::mutex> lock(g_norm_mu);
   const auto key = std::make_tuple(d.index, func, smem);
   const auto it = g_norm_occ.find(key);
-  if (it == g_norm_occ.end()) {
-    int n = 0;
-    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_optin - kNormStaticSmem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, size_t(smem)) != cudaSuccess) {
-      cudaGetLastError();
-      return QK_ERR_LAUNCH;
-    }
-    *out = g_norm_occ[key] = n;
-  } else {
+  if (it != g_norm_occ.end()) {
     *out = it->second;
+    return QK_OK;
   }
+  int n = 0;
+  if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_optin - kNormStaticSmem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, size_t(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return QK_ERR_LAUNCH;
+  }
+  *out = g_norm_occ[key] = n;
   return QK_OK;
+} catch (...) {  // no exception leaves a C entry point
+  return QK_ERR_LAUNCH;
 }
 
 NormTable shapes_of(int op, int dtype, bool vec) {

@@ -37,6 +37,7 @@ constexpr int kTileN = 256;       // columns of one, where there are enough
 constexpr int kStepK = 64;        // k of one pipeline step: 128 bytes
 constexpr int kChunkSteps = 16;   // steps of one chain of products
 constexpr int kABytes = 128 * kStepK * 2;  // one CTA's part of a step of A
+constexpr int kSplitRegisters = 128 * 64 + 256 * 216;  // what the warps' shares add up to
 constexpr int kOutBytes = 32 * 128;        // an epilogue warp's 32 rows of 128 bytes on their way out
 
 // kEpiLseCols: C's columns are the tokens (few), its rows the vocabulary.
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     return false;
   };
 
-  // Registers: the launch holds 384 x 168 = 64512; 128 x 64 + 256 x 216 = 63488
-  // of them go to the warps that feed and to those that keep sums.
+  // Registers: the launch holds 384 x 168 = 64512 (the host checks it); 128 x 64
+  // + 256 x 216 = 63488 of them go to the warps that feed and to those that keep sums.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0 && lane == 0) {
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       } else if constexpr (EPI == kEpiLse) {
         // (maximum, sum of exponentials) of the half row; columns past the last count as -inf
         if (!live) continue;
-        const int64_t target = row_target - p.v0 - j0;
-        if (row_target >= 0 && target >= 0 && target < width) {
+        const int64_t target = row_target >= 0 ? row_target - p.v0 - j0 : -1;  // any int64 may stand there
+        if (target >= 0 && target < width) {
           float x = 0.f;
 #pragma unroll
           for (int j = 0; j < kCols; ++j)  // as PTX: in C++ it becomes an indexed load, and v leaves the registers

@@ -150,7 +150,8 @@ def test_both_passes(cuda, dtype, M, V, K):
 @gpu
 @pytest.mark.parametrize("dtype,M,V,K", [("bf16", 1000, 2048, 1024), ("bf16", 4100, 40000, 64), ("f32", 2050, 20000, 40),
                                          ("bf16", 40, 33000, 512), ("f32", 24, 9000, 520), ("bf16", 2048, 300, 2056),
-                                         ("bf16", 70000, 600, 32), ("bf16", 9000, 33000, 16)])
+                                         ("bf16", 70000, 600, 32), ("bf16", 9000, 33000, 16), ("f32", 24, 50000, 520),
+                                         ("bf16", 16, 20000, 2049), ("f32", 65, 30000, 513), ("bf16", 64, 19457, 1032)])
 def test_larger(cuda, dtype, M, V, K):
     """Several pieces of the vocabulary, long sums, many tokens on few columns and the reverse."""
     c = make(M, V, K, dtype, 77)
@@ -399,6 +400,7 @@ def test_forward_refusals(lib):
         assert call(p, **kw) == qb.QK_ERR_INVALID_ARG, kw
     for kw in (dict(M=2 ** 31), dict(V=2 ** 31), dict(K=2 ** 31)):
         assert call(p, **kw) == qb.QK_ERR_UNSUPPORTED, kw
+    assert call(p, M=2 ** 30, K=2 ** 30) == qb.QK_ERR_UNSUPPORTED  # more bytes than an int64 counts
     for z in (float("nan"), float("inf")):
         assert call(p, o=ctypes.byref(qb.qk_xent_options(0, z, 0))) == qb.QK_ERR_INVALID_ARG
     for i in (0, 1, 2, 3, 6):
