@@ -3,7 +3,7 @@
 
 namespace qk {
 NormTable norm_shapes_add_f32(bool vec) {
-  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kAddNorm, float), QK_NORM_SHAPE(kAddNorm, float, 512, 512, 8, true)};
+  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kAddNorm, float)};
   static const NormShape elements[] = {QK_NORM_ELEMENT_SHAPES(kAddNorm, float)};
   return vec ? NormTable{vectors, int(sizeof(vectors) / sizeof(NormShape))}
              : NormTable{elements, int(sizeof(elements) / sizeof(NormShape))};

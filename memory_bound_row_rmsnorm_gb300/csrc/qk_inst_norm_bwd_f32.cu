@@ -3,7 +3,7 @@
 
 namespace qk {
 NormTable norm_shapes_bwd_f32(bool vec) {
-  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kAddNormBwd, float)};
+  static const NormShape vectors[] = {QK_NORM_BWD_VECTOR_SHAPES(kAddNormBwd, float)};
   static const NormShape elements[] = {QK_NORM_ELEMENT_SHAPES(kAddNormBwd, float)};
   return vec ? NormTable{vectors, int(sizeof(vectors) / sizeof(NormShape))}
              : NormTable{elements, int(sizeof(elements) / sizeof(NormShape))};

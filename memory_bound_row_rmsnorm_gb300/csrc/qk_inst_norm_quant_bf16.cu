@@ -3,7 +3,7 @@
 
 namespace qk {
 NormTable norm_shapes_quant_bf16(bool vec) {
-  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kNormQuant, __nv_bfloat16), QK_NORM_SHAPE(kNormQuant, __nv_bfloat16, 512, 512, 8, true)};
+  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kNormQuant, __nv_bfloat16)};
   static const NormShape elements[] = {QK_NORM_ELEMENT_SHAPES(kNormQuant, __nv_bfloat16)};
   return vec ? NormTable{vectors, int(sizeof(vectors) / sizeof(NormShape))}
              : NormTable{elements, int(sizeof(elements) / sizeof(NormShape))};

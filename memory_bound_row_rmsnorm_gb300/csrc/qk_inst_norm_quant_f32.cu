@@ -3,7 +3,7 @@
 
 namespace qk {
 NormTable norm_shapes_quant_f32(bool vec) {
-  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kNormQuant, float), QK_NORM_SHAPE(kNormQuant, float, 512, 512, 8, true)};
+  static const NormShape vectors[] = {QK_NORM_VECTOR_SHAPES(kNormQuant, float)};
   static const NormShape elements[] = {QK_NORM_ELEMENT_SHAPES(kNormQuant, float)};
   return vec ? NormTable{vectors, int(sizeof(vectors) / sizeof(NormShape))}
              : NormTable{elements, int(sizeof(elements) / sizeof(NormShape))};

@@ -82,8 +82,8 @@ NormTable shapes_of(int op, int dtype, bool vec) {
   }
 }
 
-// The first shape that holds the row; a ring of up to three items (two while
-// that keeps another CTA resident), a grid of every resident CTA.
+// The first shape that holds the row, a ring of one or two items, a grid of
+// every resident CTA.
 qk_status plan_norm(const CurrentDevice& d, int op, int dtype, int64_t M, int64_t N, bool vec, int inputs,
                     NormPlan* p) {
   *p = NormPlan{};
@@ -102,19 +102,35 @@ qk_status plan_norm(const CurrentDevice& d, int op, int dtype, int64_t M, int64_
   p->threads = s->threads;
   p->items = (M + R - 1) / R;
   p->slot_bytes = uint32_t((int64_t(R) * N * es + (vec ? 0 : 31) + 127) / 128 * 128);
+  // Ring slots, from runs of 1 to 4 at nine shapes.  Two by default (three and
+  // four cost the backward 3 to 6 % at 16384 x 4096 and 8192 x 8192 in bf16, and
+  // change the forward by 1 %); one for the 8-bit output of rows of up to 1024
+  // vectors in launches of at least 8 items a CTA, whose registers and
+  // arithmetic want more CTAs an SM (16384 x 4096 bf16, a scale a row: 82 us
+  // with two, 75 with one; 4096 x 4096: 18.7 and 19.6); three for the backward
+  // of aligned rows in launches of fewer than 8 items a CTA, where fewer CTAs
+  // leave fewer partial rows of dw to sum (2049 x 2048 fp32: 18.9 us, 14.6).
+  auto with_slots = [&](int slots, int* smem, int* occ) {
+    const int64_t bytes = kSmemHeader + int64_t(slots) * inputs * p->slot_bytes;
+    *smem = int(bytes);
+    *occ = 0;
+    return bytes > d.smem_optin - kNormStaticSmem ? QK_OK : norm_occupancy(d, s->func, s->threads, *smem, occ);
+  };
   int best = 0;
-  for (int slots = 3; slots >= 1; --slots) {
-    const int64_t smem = kSmemHeader + int64_t(slots) * inputs * p->slot_bytes;
-    if (smem > d.smem_optin - kNormStaticSmem) continue;
-    int occ = 0;
-    const qk_status st = norm_occupancy(d, s->func, s->threads, int(smem), &occ);
+  for (int slots = 2; slots >= 1; --slots) {
+    int smem, occ;
+    const qk_status st = with_slots(slots, &smem, &occ);
     if (st != QK_OK) return st;
-    if (occ > best) {
-      best = occ;
-      p->slots = slots;
-      p->smem = int(smem);
-    }
-    if (slots == 2 && best > 0) break;
+    if (occ == 0) continue;
+    const bool one = op == kNormQuant && units <= 1024 && p->items >= 8 * int64_t(occ) * d.sms;
+    if (best == 0 || one) best = occ, p->slots = slots, p->smem = smem;
+    if (!one) break;
+  }
+  if (op == kAddNormBwd && vec && p->slots == 2 && p->items < 8 * int64_t(best) * d.sms) {
+    int smem, occ;
+    const qk_status st = with_slots(3, &smem, &occ);
+    if (st != QK_OK) return st;
+    if (occ > 0) best = occ, p->slots = 3, p->smem = smem;
   }
   if (best == 0) return QK_ERR_UNSUPPORTED;
   p->grid = std::min<int64_t>(p->items, int64_t(best) * d.sms);

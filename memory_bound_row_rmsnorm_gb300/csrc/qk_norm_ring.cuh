@@ -66,7 +66,10 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
   float* red = reinterpret_cast<float*>(smem + 512);             // [2][16] warp sums
   uint32_t* redm = reinterpret_cast<uint32_t*>(smem + 640);      // [2][16] warp maxima
   unsigned char* ring = smem + kSmemHeader;
-  __shared__ uint32_t blk[OP == kNormQuant && !VEC ? 2 : 1][OP == kNormQuant && !VEC ? 256 : 1];  // maxima of 32 columns
+  // 8-bit output by elements: maxima of 32 columns, and a group's 1 / scale
+  constexpr bool kBlocks = OP == kNormQuant && !VEC;
+  __shared__ uint32_t blk[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
+  __shared__ float invs[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = tid / TPR, l = tid % TPR;
@@ -262,21 +265,26 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
 #pragma unroll
           for (int k = 0; k < VPT; ++k)
             for (int o = lanes / 2; o > 0; o >>= 1) um[k] = max(um[k], __shfl_xor_sync(0xffffffffu, um[k], o));
-        } else {  // a warp's 32 elements of one k lie in one group; a group is 1, 2 or 4 such blocks
-          const int per_row = (NU + 31) / 32;
+        } else {
+          // A warp's 32 elements of one k lie in one group, and a group is 1, 2 or
+          // 4 such blocks: block maxima, then a thread a group turns them into its
+          // scale, whose reciprocal the row's threads read.
+          const int per_row = (NU + 31) / 32, groups = int(a.groups);
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
             um[k] = __reduce_max_sync(0xffffffffu, um[k]);
             if (lane == 0 && l + k * TPR < NU) blk[bit][g * per_row + (l + k * TPR) / 32] = um[k];
           }
           __syncthreads();
-#pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            const int first = (l + k * TPR) / a.group * (a.group / 32);
-            um[k] = 0;
-            for (int b = first; b < min(per_row, first + a.group / 32); ++b)
-              um[k] = max(um[k], blk[bit][g * per_row + b]);
+          for (int c = l; c < groups; c += TPR) {
+            const int blocks = a.group / 32, first = c * blocks;
+            uint32_t m = 0;
+            for (int b = first; b < min(per_row, first + blocks); ++b) m = max(m, blk[bit][g * per_row + b]);
+            const float s = scale_of(__uint_as_float(m), m >= 0x7f800000u, a.qtype);
+            if (row_ok) a.scale[row * a.groups + c] = s;
+            invs[bit][g * groups + c] = 1.f / s;
           }
+          __syncthreads();
         }
         if (!row_ok) continue;
         uint8_t* qrow = static_cast<uint8_t*>(a.y) + row * N;
@@ -292,7 +300,9 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         for (int k = 0; k < VPT; ++k) {
           const int u = l + k * TPR;
           if (u >= NU) continue;
-          if (a.group != 0) {
+          if (!VEC && a.group != 0) {
+            inv = invs[bit][g * int(a.groups) + (u >> shift)];
+          } else if (a.group != 0) {
             s = scale_of(__uint_as_float(um[k]), um[k] >= 0x7f800000u, a.qtype);
             inv = 1.f / s;
             if (((u * E) & (a.group - 1)) == 0) srow[(u * E) >> shift] = s;
@@ -354,20 +364,27 @@ struct NormTable {
 #define QK_NORM_SHAPE(OP, T, TH, TPR, VPT, VEC) \
   { TPR * VPT, TH, TPR, VPT, reinterpret_cast<const void*>(&norm_ring_kernel<OP, T, TH, TPR, VPT, VEC>) }
 // Vectors: rows of up to 4096 (bf16 32768, fp32 16384 elements), 2048 in the
-// backward, which holds three inputs.
+// backward.  The backward holds three inputs, the weight and dw in registers:
+// two vectors a thread where a row is short (at four, one 256-thread CTA an SM
+// fits: 32768 x 1024 bf16 ran at 65 % of the copy's rate).
 #define QK_NORM_VECTOR_SHAPES(OP, T)                                                         \
   QK_NORM_SHAPE(OP, T, 256, 32, 1, true), QK_NORM_SHAPE(OP, T, 256, 32, 2, true),            \
       QK_NORM_SHAPE(OP, T, 256, 32, 4, true), QK_NORM_SHAPE(OP, T, 256, 64, 4, true),        \
       QK_NORM_SHAPE(OP, T, 128, 128, 4, true), QK_NORM_SHAPE(OP, T, 256, 256, 4, true),      \
-      QK_NORM_SHAPE(OP, T, 512, 512, 4, true)
+      QK_NORM_SHAPE(OP, T, 512, 512, 4, true), QK_NORM_SHAPE(OP, T, 512, 512, 8, true)
 #define QK_NORM_ELEMENT_SHAPES(OP, T)                                                        \
   QK_NORM_SHAPE(OP, T, 256, 32, 4, false), QK_NORM_SHAPE(OP, T, 256, 32, 8, false),          \
       QK_NORM_SHAPE(OP, T, 256, 32, 16, false), QK_NORM_SHAPE(OP, T, 256, 64, 16, false),    \
       QK_NORM_SHAPE(OP, T, 256, 128, 16, false), QK_NORM_SHAPE(OP, T, 256, 256, 16, false),  \
       QK_NORM_SHAPE(OP, T, 512, 512, 16, false)
+#define QK_NORM_BWD_VECTOR_SHAPES(OP, T)                                                     \
+  QK_NORM_SHAPE(OP, T, 256, 32, 1, true), QK_NORM_SHAPE(OP, T, 256, 32, 2, true),            \
+      QK_NORM_SHAPE(OP, T, 256, 64, 2, true), QK_NORM_SHAPE(OP, T, 256, 128, 2, true),       \
+      QK_NORM_SHAPE(OP, T, 128, 128, 4, true), QK_NORM_SHAPE(OP, T, 256, 256, 4, true),      \
+      QK_NORM_SHAPE(OP, T, 512, 512, 4, true)
 
-// Static shared memory of the kernels (the block maxima of the 8-bit output), kept free beside the ring.
-constexpr int kNormStaticSmem = 2048 + 16;
+// Static shared memory of the kernels (the block maxima and scales of the 8-bit output), kept free beside the ring.
+constexpr int kNormStaticSmem = 4096 + 16;
 
 // Defined by the instantiation translation units: (operator, type) x (vectors, elements).
 NormTable norm_shapes_add_f32(bool vec);
