@@ -448,6 +448,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   p.rows = int32_t(rows);
   p.cols = int32_t(cols);
   p.planes = int32_t(a.planes);
+  p.chunk = a.planes == 3 ? 8 : 16;
   p.depth = int32_t(depth);
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));

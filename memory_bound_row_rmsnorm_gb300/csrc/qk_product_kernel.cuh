@@ -13,9 +13,12 @@
 // The tensor core adds to a sum by cutting off what does not fit, always toward
 // zero: a chain of n products of 16 k is short by about n 2^-25.5 of itself (a
 // sum over 8192 k measured 1e-5 off, where rounding to nearest gives 1e-6).  So
-// a chain ends after kChunkSteps * 64 = 1024 k, and the chains of a tile are
-// added in registers, to nearest.  (Shorter chains cost time and power: at 512 k
-// the backward of 8192 x 32000 x 4096 took 4.40 ms in a long run, at 1024 4.31.)
+// a chain ends after `chunk` steps of 64 k, and the chains of a tile are added in
+// registers, to nearest.  16 steps for bf16 (lse 3e-7 off at K = 4096), whose
+// outputs of consequence are bf16; 8 for float32, whose gradients measured
+// 1.3e-6 off with 16 and 7e-7 with 8, against 0.8 to 1.6e-6 of fp32 products.
+// Shorter chains cost time and power: with 8 steps the bf16 backward of 8192 x
+// 32000 x 4096 took 4.40 ms in a long run, with 16 4.31.
 //
 // An operand is stored with k innermost (K-major) or with its rows innermost
 // (MN-major): h, w and g serve as either, without a transposed copy.
@@ -35,7 +38,6 @@ constexpr int kProductThreads = 384;  // 4 warps that feed the tensor cores, 8 f
 constexpr int kTileM = 256;       // rows of a pair's tile
 constexpr int kTileN = 256;       // columns of one, where there are enough
 constexpr int kStepK = 64;        // k of one pipeline step: 128 bytes
-constexpr int kChunkSteps = 16;   // steps of one chain of products
 constexpr int kABytes = 128 * kStepK * 2;  // one CTA's part of a step of A
 constexpr int kSplitRegisters = 128 * 64 + 256 * 216;  // what the warps' shares add up to
 constexpr int kOutBytes = 32 * 128;        // an epilogue warp's 32 rows of 128 bytes on their way out
@@ -64,6 +66,7 @@ struct ProductArgs {
   int32_t planes;            // 1 (bf16) or 3 (float32)
   int32_t m_tiles, n_tiles;
   int32_t n_full, last_n;    // column tiles of TN columns (the first ones); columns of a product in the last
+  int32_t chunk;             // steps of one chain of products
   int32_t splits, split_steps;  // the k axis in pieces of split_steps steps
   uint64_t timeout_ns;
   int* status;
@@ -183,8 +186,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                    const ProductArgs p) {
   constexpr int kStages = product_stages(TN), kStageBytes = product_stage_bytes(TN);
   // A product of few columns waits for the one before it on the same sums, some
-  // 125 cycles where its own work is 32; four sets of sums, one for each 16 k of
-  // a step, keep four under way.
+  // 125 cycles where its own work is 16 to 64; so a step's products of 16 k go to
+  // four sets of sums (two at 128 columns), which the epilogue adds.  Tiles of TN
+  // columns below 256 do so always, g's product in a narrow last column tile.
   constexpr int kParts = TN == kTileN ? 1 : 4, kSet = kParts * TN;
   constexpr uint32_t kColumns = 2 * kSet;  // TMEM: two sets of sums, or of four times them
   static_assert(!B_MN || TN == kTileN, "MN-major B comes in boxes of 64 columns");
@@ -231,6 +235,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   grid_dependency_wait();
   allow_dependent_launch();
 
+  auto parts_of = [&](int n) {
+    // Only g's product: a narrow tile of dw or dh waits for A's steps all the
+    // same (2047 x 8191 x 513 fp32: 148 us without, 151 with), and the forward's
+    // loop is 3 % slower with the choice in it.
+    if (TN < kTileN || EPI != kEpiGrad) return kParts;
+    return n < p.n_full || p.last_n > 128 ? 1 : p.last_n > 64 ? 2 : 4;
+  };
   bool failed = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_wait<false>(bar, parity, p.timeout_ns)) return true;
@@ -296,13 +307,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const TileAt at = tile_at(p, t);
       const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
       const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
+      const int parts = parts_of(at.n);
+      const uint32_t stride = uint32_t(kSet / parts);
       int in_pair = s0 % p.steps;
-      for (int c0 = s0; c0 < s1 && !failed; c0 += kChunkSteps, ++it) {
+      for (int c0 = s0; c0 < s1 && !failed; c0 += p.chunk, ++it) {
         const uint32_t acc = it & 1u;
         if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
         tcgen05_fence_after();
         const uint32_t d = tmem + acc * kSet;
-        const int c1 = min(s1, c0 + kChunkSteps);
+        const int c1 = min(s1, c0 + p.chunk);
         for (int s = c0; s < c1; ++s) {
           if (!wait(full0 + 8 * st, turn)) break;
           tcgen05_fence_after();
@@ -310,14 +323,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
           const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
           if (tail) in_pair = 0;
-          if (kParts == 1 && tail && tail_parts < kStepK / 16) {
+          if (parts == 1 && tail && tail_parts < kStepK / 16) {
             for (int k = 0; k < tail_parts; ++k)
               mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
           } else {
 #pragma unroll
             for (int k = 0; k < kStepK / 16; ++k)
-              mma_bf16_pair(d + uint32_t(kParts == 1 ? 0 : k * TN), da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep,
-                            idesc, s > c0 || (kParts == 1 && k > 0));
+              mma_bf16_pair(d + uint32_t(k & (parts - 1)) * stride, da + uint64_t(k) * kAStep,
+                            db + uint64_t(k) * kBStep, idesc, s > c0 || k >= parts);
           }
           mma_commit_pair(empty0 + 8 * st);
           if (++st == kStages) st = 0, turn ^= 1u;
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
 
       float v[kCols];
-      for (int c0 = s0; c0 < s1; c0 += kChunkSteps, ++it) {
+      for (int c0 = s0; c0 < s1; c0 += p.chunk, ++it) {
         const uint32_t acc = it & 1u;
         if (!wait(done0 + 8 * acc, (it >> 1) & 1u)) break;
         tcgen05_fence_after();
@@ -401,6 +414,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             tmem_load_wait(x);
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[c + j] += x[j];
+          }
+        }
+        if (const int parts = parts_of(at.n); EPI == kEpiGrad && parts > 1 && half == 0) {
+          const int stride = kTileN / parts;  // all the columns of such a tile are this half's
+          for (int k = 1; k < parts; ++k) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+              if (c >= stride) continue;
+              float x[16];
+              tmem_load_16(src + uint32_t(k * stride + c), x);
+              tmem_load_wait(x);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[c + j] += x[j];
+            }
           }
         }
         tcgen05_fence_before();
