@@ -318,7 +318,7 @@ int choose_splits(int64_t M, int64_t K, int64_t steps) {
 }
 
 // `copied`: h and w go through the workspace (float32, or rows that TMA cannot read in place).
-Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied) {
+Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied) {
   Layout l = {};
   l.planes = dtype == QK_F32 ? 3 : 1;
   l.kp = round_up(K, 8);
@@ -363,6 +363,21 @@ Layout layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied)
   }
   l.total = at;
   return l;
+}
+
+// The same, kept per thread for the last sizes of each kind.
+const Layout& layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool copied) {
+  struct Cached {
+    int64_t M = -1, V = -1, K = -1;
+    Layout l;
+  };
+  thread_local Cached cache[2][2][2];
+  Cached& c = cache[bwd][dtype == QK_BF16][copied];
+  if (c.M != M || c.V != V || c.K != K) {
+    c.l = plan_layout(bwd, M, V, K, dtype, copied);
+    c.M = M, c.V = V, c.K = K;
+  }
+  return c.l;
 }
 
 qk_status check_linear(int dtype, int64_t M, int64_t V, int64_t K) {
@@ -509,7 +524,7 @@ qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int
 template <typename T>
 qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean) {
   const bool copied = !in_place(c.h, c.w, c.K, dtype);
-  const Layout l = layout(false, c.M, c.V, c.K, dtype, copied);
+  const Layout& l = layout(false, c.M, c.V, c.K, dtype, copied);
   Operand h, w;
   qk_status st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
   ProductArgs p = {};
@@ -546,7 +561,7 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean
 template <typename T>
 qk_status backward(const Call& c, int dtype, const float* lse, const float* dloss, void* dh, void* dw) {
   const bool copied = !in_place(c.h, c.w, c.K, dtype);
-  const Layout l = layout(true, c.M, c.V, c.K, dtype, copied);
+  const Layout& l = layout(true, c.M, c.V, c.K, dtype, copied);
   XentRow* row = reinterpret_cast<XentRow*>(c.ws + l.row);
   float* scale = reinterpret_cast<float*>(c.ws + l.scale);
   float* sum = reinterpret_cast<float*>(c.ws + l.sum);

@@ -73,7 +73,7 @@ struct ProductArgs {
   // epilogues; v0: vocabulary index of column 0
   int64_t v0;
   const int64_t* targets;    // lse
-  float2* part;              // lse: [half column tile, or pair and warp][part_ld] (maximum, sum)
+  float2* part;              // lse: [half column tile, or CTA][part_ld] (maximum, sum)
   int64_t part_ld;
   int64_t part0;             // lse over columns: first pair's place in the list
   float* at_target;          // lse: logit of the target
@@ -84,7 +84,7 @@ struct ProductArgs {
   const float* sum;          // finish: fp32 [rows][sum_ld]
   int64_t sum_ld;
   int32_t vec;               // store: rows start on 16 bytes
-  const float* scale;        // accum, store: factor (device)
+  const float* scale;        // accum, store, finish: factor (device)
 };
 
 // Splits a float into three bf16 parts; what is not finite stays in the first.
@@ -254,91 +254,91 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // + 256 x 216 = 63488 of them go to the warps that feed and to those that keep sums.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 0 && lane == 0) {
-    // ---- producer: this CTA's half of each step's operands ----
-    constexpr int half_n = TN / 2;
-    constexpr uint32_t bytes = 2u * uint32_t(kStageBytes);
-    int64_t q = 0;  // steps issued
-    int st = 0;
-    uint32_t turn = 0;
-    for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
-      const TileAt at = tile_at(p, t);
-      const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * (at.n < p.n_full ? half_n : p.last_n / 2);
-      const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
-      int pair = s0 / p.steps, in_pair = s0 % p.steps;
-      for (int s = s0; s < s1; ++s, ++q) {
-        if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
-        const int k = in_pair * kStepK;
-        // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0): the small products first
-        const int pa = pairs == 1 ? 0 : pair < 3 ? 2 - pair : pair == 3 ? 1 : 0;
-        const int pb = pairs == 1 ? 0 : pair < 3 ? pair : pair == 4 ? 1 : 0;
-        const uint32_t bar = map_to_rank(full0 + 8 * st, 0);
-        if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, bytes);
-        const uint32_t da = ring + uint32_t(st) * kStageBytes, db = da + kABytes;
-        if constexpr (A_MN) {
-          tma_load_3d(da, &map_a, a0, k, pa, bar);
-          tma_load_3d(da + kABytes / 2, &map_a, a0 + 64, k, pa, bar);
-        } else {
-          tma_load_3d(da, &map_a, k, a0, pa, bar);
-        }
-        if constexpr (B_MN) {
-          for (int i = 0; i < half_n / 64; ++i)
-            tma_load_3d(db + uint32_t(i) * (64 * kStepK * 2), &map_b, b0 + 64 * i, k, pb, bar);
-        } else {
-          tma_load_3d(db, &map_b, k, b0, pb, bar);
-        }
-        if (++st == kStages) st = 0, turn ^= 1u;
-        if (++in_pair == p.steps) in_pair = 0, ++pair;
-      }
-    }
-    // A failed launch leaves once the loads in flight have landed: the leader's
-    // barriers count those of both CTAs.
-    if (failed && rank == 0)
-      for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
-        mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---- products of both CTAs ----
-    constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
-    constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
-    const int tail_parts = (p.depth - (p.steps - 1) * kStepK + 15) / 16;
-    int st = 0;
-    uint32_t turn = 0, it = 0;  // it: chains begun
-    for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
-      const TileAt at = tile_at(p, t);
-      const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
-      const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
-      const int parts = parts_of(at.n);
-      const uint32_t stride = uint32_t(kSet / parts);
-      int in_pair = s0 % p.steps;
-      for (int c0 = s0; c0 < s1 && !failed; c0 += p.chunk, ++it) {
-        const uint32_t acc = it & 1u;
-        if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
-        tcgen05_fence_after();
-        const uint32_t d = tmem + acc * kSet;
-        const int c1 = min(s1, c0 + p.chunk);
-        for (int s = c0; s < c1; ++s) {
-          if (!wait(full0 + 8 * st, turn)) break;
-          tcgen05_fence_after();
-          const uint32_t sa = ring + uint32_t(st) * kStageBytes;
-          const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
-          const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
-          if (tail) in_pair = 0;
-          if (parts == 1 && tail && tail_parts < kStepK / 16) {
-            for (int k = 0; k < tail_parts; ++k)
-              mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+    if (warp == 0 && lane == 0) {
+      // ---- producer: this CTA's half of each step's operands ----
+      constexpr int half_n = TN / 2;
+      constexpr uint32_t bytes = 2u * uint32_t(kStageBytes);
+      int64_t q = 0;  // steps issued
+      int st = 0;
+      uint32_t turn = 0;
+      for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
+        const TileAt at = tile_at(p, t);
+        const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * (at.n < p.n_full ? half_n : p.last_n / 2);
+        const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+        int pair = s0 / p.steps, in_pair = s0 % p.steps;
+        for (int s = s0; s < s1; ++s, ++q) {
+          if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
+          const int k = in_pair * kStepK;
+          // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0): the small products first
+          const int pa = pairs == 1 ? 0 : pair < 3 ? 2 - pair : pair == 3 ? 1 : 0;
+          const int pb = pairs == 1 ? 0 : pair < 3 ? pair : pair == 4 ? 1 : 0;
+          const uint32_t bar = map_to_rank(full0 + 8 * st, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, bytes);
+          const uint32_t da = ring + uint32_t(st) * kStageBytes, db = da + kABytes;
+          if constexpr (A_MN) {
+            tma_load_3d(da, &map_a, a0, k, pa, bar);
+            tma_load_3d(da + kABytes / 2, &map_a, a0 + 64, k, pa, bar);
           } else {
-#pragma unroll
-            for (int k = 0; k < kStepK / 16; ++k)
-              mma_bf16_pair(d + uint32_t(k & (parts - 1)) * stride, da + uint64_t(k) * kAStep,
-                            db + uint64_t(k) * kBStep, idesc, s > c0 || k >= parts);
+            tma_load_3d(da, &map_a, k, a0, pa, bar);
           }
-          mma_commit_pair(empty0 + 8 * st);
+          if constexpr (B_MN) {
+            for (int i = 0; i < half_n / 64; ++i)
+              tma_load_3d(db + uint32_t(i) * (64 * kStepK * 2), &map_b, b0 + 64 * i, k, pb, bar);
+          } else {
+            tma_load_3d(db, &map_b, k, b0, pb, bar);
+          }
           if (++st == kStages) st = 0, turn ^= 1u;
+          if (++in_pair == p.steps) in_pair = 0, ++pair;
         }
-        if (!failed) mma_commit_pair(done0 + 8 * acc);
+      }
+      // A failed launch leaves once the loads in flight have landed: the leader's
+      // barriers count those of both CTAs.
+      if (failed && rank == 0)
+        for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
+          mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---- products of both CTAs ----
+      constexpr uint32_t kLbo = 64 * kStepK * 2;                       // MN-major: the next 64 rows
+      constexpr uint32_t kAStep = (A_MN ? 16 * 128 : 32) >> 4, kBStep = (B_MN ? 16 * 128 : 32) >> 4;  // 16 k
+      const int tail_parts = (p.depth - (p.steps - 1) * kStepK + 15) / 16;
+      int st = 0;
+      uint32_t turn = 0, it = 0;  // it: chains begun
+      for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
+        const TileAt at = tile_at(p, t);
+        const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+        const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
+        const int parts = parts_of(at.n);
+        const uint32_t stride = uint32_t(kSet / parts);
+        int in_pair = s0 % p.steps;
+        for (int c0 = s0; c0 < s1 && !failed; c0 += p.chunk, ++it) {
+          const uint32_t acc = it & 1u;
+          if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
+          tcgen05_fence_after();
+          const uint32_t d = tmem + acc * kSet;
+          const int c1 = min(s1, c0 + p.chunk);
+          for (int s = c0; s < c1; ++s) {
+            if (!wait(full0 + 8 * st, turn)) break;
+            tcgen05_fence_after();
+            const uint32_t sa = ring + uint32_t(st) * kStageBytes;
+            const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
+            const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
+            if (tail) in_pair = 0;
+            if (parts == 1 && tail && tail_parts < kStepK / 16) {
+              for (int k = 0; k < tail_parts; ++k)
+                mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
+            } else {
+#pragma unroll
+              for (int k = 0; k < kStepK / 16; ++k)
+                mma_bf16_pair(d + uint32_t(k & (parts - 1)) * stride, da + uint64_t(k) * kAStep,
+                              db + uint64_t(k) * kBStep, idesc, s > c0 || k >= parts);
+            }
+            mma_commit_pair(empty0 + 8 * st);
+            if (++st == kStages) st = 0, turn ^= 1u;
+          }
+          if (!failed) mma_commit_pair(done0 + 8 * acc);
+        }
       }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- epilogue: half a row of the tile a thread ----
@@ -383,7 +383,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       float v[kCols];
       for (int c0 = s0; c0 < s1; c0 += p.chunk, ++it) {
         const uint32_t acc = it & 1u;
-        if (!wait(done0 + 8 * acc, (it >> 1) & 1u)) break;
+        const bool summed = wait(done0 + 8 * acc, (it >> 1) & 1u);
+        if (!__all_sync(0xffffffffu, summed)) {  // a warp gives up as one: its lanes meet again below
+          failed = true;
+          break;
+        }
         tcgen05_fence_after();
         const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + acc * kSet + uint32_t(half * kCols);
         __syncwarp();  // the loads are the warp's
