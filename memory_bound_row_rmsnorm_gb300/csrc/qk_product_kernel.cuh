@@ -97,7 +97,7 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16* b) {
 }
 
 // 32 rows of 128 bytes from "a row a lane" (u[0..7], 16 bytes each) to memory:
-// put(row, unit, x) gets each 16 bytes once, eight lanes on the 128 bytes of one
+// put(k, row, unit, x) gets each 16 bytes once (k: 0..7, row = 4 k + lane / 8), eight lanes on the 128 bytes of one
 // row, so that stores are whole lines.  A lane storing its own row's vectors
 // touches 32 lines an instruction: dh at 8192 x 32000 x 4096 ran at 1150 TFLOP/s
 // that way.  Units are XORed with the row: no bank is hit twice.
@@ -117,7 +117,7 @@ __device__ __forceinline__ void rows_out(uint32_t buf, int lane, const uint4* u,
                  : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                  : "r"(buf + row * 128 + ((unit ^ (row & 7)) * 16))
                  : "memory");
-    put(row, unit, x);
+    put(k, row, unit, x);
   }
   __syncwarp();
 }
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 for (int e = 0; e < 8; ++e) v[c + 8 * k + e] -= f[e];
               }
             }
-            rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+            rows_out(buf, lane, u, [&](int, int r, int unit, const uint4& x) {
               const int col = c + unit * 8;
               if (r < rows_left && col < width)
                 *reinterpret_cast<uint4*>(out + pl * p.plane_stride + r * p.ld + col) = x;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           uint4 u[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) u[k] = Vec16<float>::pack(v + c + 4 * k);
-          rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+          rows_out(buf, lane, u, [&](int, int r, int unit, const uint4& x) {
             const int col = c + unit * 4;
             if (r >= rows_left || col >= width) return;  // ld is a multiple of 4
             float* o = out + r * p.ld + col;
@@ -564,13 +564,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           uint4 u[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) u[k] = Vec16<float>::pack(v + c + 4 * k);
-          rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+          // The sums so far, all eight loads before the first store: one after the
+          // other they cost a trip to memory each.
+          float4 y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = k * 4 + (lane >> 3), col = c + (lane & 7) * 4;
+            if (r < rows_left && col < width) y[k] = *reinterpret_cast<const float4*>(sum + r * p.sum_ld + col);
+          }
+          rows_out(buf, lane, u, [&](int k, int r, int unit, const uint4& x) {
             const int col = c + unit * 4;
             if (r >= rows_left || col >= width) return;  // sum_ld is a multiple of 4
-            const float4 y = *reinterpret_cast<const float4*>(sum + r * p.sum_ld + col);
             float f[4];
             Vec16<float>::unpack(x, f);
-            f[0] += y.x, f[1] += y.y, f[2] += y.z, f[3] += y.w;
+            f[0] += y[k].x, f[1] += y[k].y, f[2] += y[k].z, f[3] += y[k].w;
             T* o = out + r * p.ld + col;
             if (p.vec) {
               if constexpr (sizeof(T) == 2) {
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) u[k] = Vec16<T>::pack(v + c + E * k);
           if (p.vec) {
-            rows_out(buf, lane, u, [&](int r, int unit, const uint4& x) {
+            rows_out(buf, lane, u, [&](int, int r, int unit, const uint4& x) {
               const int col = c + unit * E;
               if (r < rows_left && col < width) *reinterpret_cast<uint4*>(out + r * p.ld + col) = x;
             });
