@@ -19,6 +19,8 @@
 #include <cstdint>
 
 #include "../../include/qk.h"
+#include "qk_bwd_kernels.cuh"  // dw_reduce_kernel
+#include "qk_few_tokens.cuh"
 #include "qk_host.h"
 #include "qk_kernels.cuh"  // xent_mean_kernel
 #include "qk_product_kernel.cuh"
@@ -35,6 +37,7 @@ constexpr int kPairs = 76;  // CTA pairs of a GB300
 // cores work through 240 empty ones at 16 tokens, 34 us at 32000 x 4096 where
 // reading w takes 39 us at the copy's rate; the columns cost them nothing.
 constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewSmem = 200 << 10;  // h of the fp32 kernels for few tokens, in shared memory
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
@@ -44,36 +47,39 @@ int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 // ---------------------------------------------------------------------------
 
 // Rows of T into rows of bf16 planes whose row length is a multiple of 8 (what
-// TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.  A
-// thread takes 8 columns of a row; what lies behind the last column is written
-// but read by nobody.
+// TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.  A warp
+// takes a row, a lane two neighbouring columns at a time, so that every load and
+// store of a warp is whole lines.  What lies behind the last column is read by nobody.
 template <typename T>
 __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, int32_t cols, __nv_bfloat16* out,
                                                      int32_t ld, int64_t plane_stride) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const uint32_t per_row = uint32_t(ld) / 8;
-  for (int64_t i0 = blockIdx.x; i0 * 256 < rows * per_row; i0 += gridDim.x) {
-    const int64_t unit = i0 * 256 + threadIdx.x, i = unit / per_row;
-    if (i >= rows) return;
-    const int32_t j = int32_t(unit - i * per_row) * 8;
-    const T* src = in + i * cols + j;
-    float f[8];
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += int64_t(gridDim.x) * 8) {
+    const T* src = in + i * cols;
+    __nv_bfloat16* dst = out + i * ld;
+    constexpr int kUnroll = 4;
+    for (int j0 = 2 * lane; j0 < cols; j0 += 64 * kUnroll) {
+      T x[kUnroll][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = j + e < cols ? Vec16<T>::load1(src + e) : 0.f;
-    uint4* dst = reinterpret_cast<uint4*>(out + i * ld + j);
-    if constexpr (sizeof(T) == 2) {
-      *dst = Vec16<__nv_bfloat16>::pack(f);
-    } else {
-      __nv_bfloat16 b[8][3];
+      for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) split3(f[e], b[e]);
+        for (int e = 0; e < 2; ++e) x[u][e] = j0 + 64 * u + e < cols ? src[j0 + 64 * u + e] : T(0.f);
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        float x[8];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int j = j0 + 64 * u;
+        if (j >= cols) break;  // ld is even: the pair stays inside the row
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<__nv_bfloat162*>(dst + j) = __nv_bfloat162{x[u][0], x[u][1]};
+        } else {
+          __nv_bfloat16 a[3], b[3];
+          split3(x[u][0], a);
+          split3(x[u][1], b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __bfloat162float(b[e][pl]);
-        dst[pl * (plane_stride / 8)] = Vec16<__nv_bfloat16>::pack(x);
+          for (int pl = 0; pl < 3; ++pl)
+            *reinterpret_cast<__nv_bfloat162*>(dst + pl * plane_stride + j) = __nv_bfloat162{a[pl], b[pl]};
+        }
       }
     }
   }
@@ -278,6 +284,12 @@ struct Layout {
   // byte offsets
   int64_t h, w, part, at_target, row, scale, g, sum, ht, total;
   bool turned;         // dw's product reads h as [K][M]
+  int few;             // tokens of the fp32 kernels for few tokens (0: the products)
+  int few_grid;        // CTAs of the logits, each with a pair a token
+  int few_chunk;       // k of h in their shared memory
+  int few_kv;          // backward: columns of a thread
+  int columns, splits_y;  // backward: threads of a CTA along k, splits of the vocabulary by CTAs
+  int64_t per_split;
 };
 
 // Launches are waves of kPairs tiles; a wave takes as long as its tiles have
@@ -322,16 +334,45 @@ Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool co
   Layout l = {};
   l.planes = dtype == QK_F32 ? 3 : 1;
   l.kp = round_up(K, 8);
-  int64_t most = round_up(V, 256);
-  if (copied) most = std::min<int64_t>(most, kStageCopyBytes / (l.kp * 2 * l.planes));
-  if (bwd) most = std::min<int64_t>(most, kPieceBytes / (M * 2 * l.planes));
-  l.piece = bwd ? choose_piece(M, V, K, most) : std::min<int64_t>(V, std::max<int64_t>(kTileN, most / kTileN * kTileN));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
     at += round_up(bytes, 256);
     return o;
   };
+  // Few float32 tokens: the fp32 kernels (qk_few_tokens.cuh), while g stays within a piece.
+  const int mt = M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
+  if (dtype == QK_F32 && M <= 32 && V * mt * 4 <= kPieceBytes) {
+    l.few = mt;
+    l.few_chunk = int(std::min<int64_t>(round_up(K, 128), kFewSmem / (mt * 4) / 128 * 128));
+    l.few_grid = int(std::min<int64_t>(ceil_div(V, 16 * (64 / mt > 8 ? 8 : 64 / mt)), 2 * kPairs));
+    l.piece = V;
+    // columns of a thread in the backward: 64 sums and 64 values of h in registers
+    l.few_kv = K % 4 != 0 ? 1 : mt <= 8 ? 4 : mt == 16 ? 2 : 1;
+    const int64_t threads = ceil_div(K, l.few_kv);
+    l.columns = threads <= 64 ? 64 : threads <= 128 ? 128 : 256;
+    if (!bwd) {
+      l.part = take(int64_t(l.few_grid) * M * 8);
+      l.at_target = take(M * 4);
+    } else {
+      // two CTAs an SM, twice over, each with at least 64 rows of the vocabulary
+      const int64_t across = ceil_div(threads, l.columns);
+      const int64_t y = std::max<int64_t>(1, std::min<int64_t>(8 * kPairs / across, ceil_div(V, 64)));
+      l.per_split = round_up(ceil_div(V, y), 64);
+      l.splits_y = int(ceil_div(V, l.per_split));
+      l.splits = l.splits_y * (kFewThreads / l.columns);
+      l.row = take(M * int64_t(sizeof(XentRow)));
+      l.scale = take(4);
+      l.g = take(V * mt * 4);
+      l.sum = take(int64_t(l.splits) * M * K * 4);
+    }
+    l.total = at;
+    return l;
+  }
+  int64_t most = round_up(V, 256);
+  if (copied) most = std::min<int64_t>(most, kStageCopyBytes / (l.kp * 2 * l.planes));
+  if (bwd) most = std::min<int64_t>(most, kPieceBytes / (M * 2 * l.planes));
+  l.piece = bwd ? choose_piece(M, V, K, most) : std::min<int64_t>(V, std::max<int64_t>(kTileN, most / kTileN * kTileN));
   if (copied) {
     l.h = take(l.planes * M * l.kp * 2);
     l.w = take(l.planes * l.piece * l.kp * 2);
@@ -517,14 +558,83 @@ qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int
   *o = {src, c.K, rows, c.K, 1, 0};
   if (!copied) return QK_OK;
   *o = {at, c.K, rows, l.kp, l.planes, rows * l.kp};
-  return launch_pdl(planes_kernel<T>, dim3(blocks(c, rows * l.kp / 8)), 256, 0, c.stream, src, rows, int32_t(c.K),
+  return launch_pdl(planes_kernel<T>, dim3(unsigned(std::min<int64_t>(ceil_div(rows, 8), 16 * c.dev.sms))), 256, 0, c.stream, src, rows, int32_t(c.K),
                     reinterpret_cast<__nv_bfloat16*>(at), int32_t(l.kp), rows * l.kp);
+}
+
+// Launches of the fp32 kernels for few tokens.
+template <int MT, int KV, bool GRAD>
+qk_status launch_few_logits(const Call& c, const Layout& l, const FewArgs& a) {
+  const auto kernel = few_logits_kernel<float, MT, KV, GRAD>;
+  static std::atomic<uint64_t> prepared{0};  // one bit a device
+  const uint64_t bit = uint64_t(1) << (c.dev.index & 63);
+  if (!(prepared.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kFewSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      return QK_ERR_LAUNCH;
+    }
+    prepared.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl(kernel, dim3(unsigned(l.few_grid)), kFewLogitThreads, size_t(MT) * size_t(a.chunk) * 4, c.stream, a);
+}
+template <bool GRAD>
+qk_status few_logits(const Call& c, const Layout& l, const FewArgs& a) {
+  const bool vec = c.K % 4 == 0 && aligned16(c.w);
+  switch (l.few) {
+    case 4: return vec ? launch_few_logits<4, 4, GRAD>(c, l, a) : launch_few_logits<4, 1, GRAD>(c, l, a);
+    case 8: return vec ? launch_few_logits<8, 4, GRAD>(c, l, a) : launch_few_logits<8, 1, GRAD>(c, l, a);
+    case 16: return vec ? launch_few_logits<16, 4, GRAD>(c, l, a) : launch_few_logits<16, 1, GRAD>(c, l, a);
+    default: return vec ? launch_few_logits<32, 4, GRAD>(c, l, a) : launch_few_logits<32, 1, GRAD>(c, l, a);
+  }
+}
+qk_status few_forward(const Call& c, const Layout& l, float* loss, float* lse, float* mean) {
+  FewArgs f = {};
+  f.h = c.h, f.w = c.w, f.V = c.V, f.M = int32_t(c.M), f.K = int32_t(c.K), f.chunk = l.few_chunk;
+  f.targets = c.targets;
+  f.part = reinterpret_cast<float2*>(c.ws + l.part);
+  f.at_target = reinterpret_cast<float*>(c.ws + l.at_target);
+  const qk_status st = few_logits<false>(c, l, f);
+  if (st != QK_OK) return st;
+  const LossArgs a = {f.part, c.M, l.few_grid, f.at_target, c.targets, c.M, c.V, c.has_ignore, c.z, c.ignore, loss,
+                      lse, mean};
+  return launch_pdl(join_few_kernel, dim3(1), 1024, 0, c.stream, a);
+}
+qk_status few_backward(const Call& c, const Layout& l, void* dh, void* dw) {
+  FewArgs a = {};
+  a.h = c.h, a.w = c.w, a.V = c.V, a.M = int32_t(c.M), a.K = int32_t(c.K), a.chunk = l.few_chunk;
+  a.row = reinterpret_cast<const XentRow*>(c.ws + l.row);
+  a.scale = reinterpret_cast<const float*>(c.ws + l.scale);
+  a.g = reinterpret_cast<float*>(c.ws + l.g);
+  a.sum = dh != nullptr ? reinterpret_cast<float*>(c.ws + l.sum) : nullptr;
+  a.dw = dw;
+  a.ld = c.K;
+  a.columns = l.columns;
+  a.per_split = l.per_split;
+  qk_status st = few_logits<true>(c, l, a);
+  if (st != QK_OK || (dh == nullptr && dw == nullptr)) return st;
+  // The vectors' alignment is known only here; without it a thread takes one
+  // column after the other of the same number of threads' worth, in more CTAs.
+  const bool vec = l.few_kv > 1 && aligned16(c.w) && aligned16(dw);
+  const int kv = vec ? l.few_kv : 1;
+  const dim3 grid(unsigned(ceil_div(ceil_div(c.K, kv), l.columns)), unsigned(l.splits_y));
+  const auto go = [&](auto kernel) { return launch_pdl(kernel, grid, kFewThreads, 0, c.stream, a); };
+  switch (l.few) {
+    case 4: st = vec ? go(few_grad_kernel<float, 4, 4>) : go(few_grad_kernel<float, 4, 1>); break;
+    case 8: st = vec ? go(few_grad_kernel<float, 8, 4>) : go(few_grad_kernel<float, 8, 1>); break;
+    case 16: st = vec ? go(few_grad_kernel<float, 16, 2>) : go(few_grad_kernel<float, 16, 1>); break;
+    default: st = go(few_grad_kernel<float, 32, 1>);
+  }
+  if (st != QK_OK || dh == nullptr) return st;
+  // Hundreds of splits of few sums: a warp for each 32 of them and every 32nd split.
+  return launch_pdl(dw_reduce_kernel<0>, dim3(unsigned(ceil_div(c.M * c.K, 32))), kDwReduceThreads, 0, c.stream, a.sum,
+                    static_cast<float*>(dh), l.splits, c.M * c.K);
 }
 
 template <typename T>
 qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean) {
   const bool copied = !in_place(c.h, c.w, c.K, dtype);
   const Layout& l = layout(false, c.M, c.V, c.K, dtype, copied);
+  if (l.few != 0) return few_forward(c, l, loss, lse, mean);
   Operand h, w;
   qk_status st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
   ProductArgs p = {};
@@ -569,6 +679,7 @@ qk_status backward(const Call& c, int dtype, const float* lse, const float* dlos
   Operand h, w, ht = {};
   qk_status st = launch_pdl(rows_kernel, dim3(1), 1024, 0, c.stream, c.targets, lse, dloss, c.M, c.V, c.has_ignore,
                             c.ignore, c.z, row, scale);
+  if (l.few != 0) return st == QK_OK ? few_backward(c, l, dh, dw) : st;
   if (st == QK_OK) st = operand(c, l, copied, static_cast<const T*>(c.h), c.M, c.ws + l.h, &h);
   if (st == QK_OK && dw != nullptr && l.turned) {
     const int64_t ld = round_up(c.M, 8);
