@@ -48,6 +48,13 @@ __device__ __forceinline__ float qmax_of(int qtype) { return qtype == 0 ? 448.f 
 __device__ __forceinline__ float scale_of(float amax, bool bad, int qtype) {
   return bad ? __int_as_float(0x7fc00000) : fmaxf(amax, kSmallestGroupMax) / qmax_of(qtype);
 }
+// y / s with inv = 1 / s rounded: the product's residual corrects it (Markstein's
+// division step), so that what is rounded to 8 bits is the rounded quotient, not
+// one that the reciprocal's rounding moved across a tie.  A NaN s stays NaN.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+  const float q = y * inv;
+  return fmaf(fmaf(-q, s, y), inv, q);
+}
 // One value in 8 bits, to nearest even.  |v| exceeds qmax by rounding at most, which saturates.
 __device__ __forceinline__ uint32_t quantise(float v, int qtype) {
   if (qtype == 0) return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
           const float s = scale_of(m, bad > 0.f, a.qtype);
           if (tid == 0) sc[0] = s;
           const float inv = 1.f / s;
-          for (int64_t j = tid; j < N; j += TH) q[j] = uint8_t(quantise(normed(j) * inv, a.qtype));
+          for (int64_t j = tid; j < N; j += TH) q[j] = uint8_t(quantise(quotient(normed(j), s, inv), a.qtype));
         } else {
           __syncthreads();  // a warp reads what others kept of h
           for (int64_t g = warp; g < a.groups; g += TH / 32) {
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int64_t j = g * a.group + lane + 32 * k;
-              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(v[k] * inv, a.qtype));
+              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(quotient(v[k], s, inv), a.qtype));
             }
           }
         }

@@ -66,10 +66,10 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
   float* red = reinterpret_cast<float*>(smem + 512);             // [2][16] warp sums
   uint32_t* redm = reinterpret_cast<uint32_t*>(smem + 640);      // [2][16] warp maxima
   unsigned char* ring = smem + kSmemHeader;
-  // 8-bit output by elements: maxima of 32 columns, and a group's 1 / scale
+  // 8-bit output by elements: maxima of 32 columns, a group's scale and 1 / scale
   constexpr bool kBlocks = OP == kNormQuant && !VEC;
   __shared__ uint32_t blk[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
-  __shared__ float invs[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
+  __shared__ float scales[kBlocks ? 2 : 1][kBlocks ? 256 : 1], invs[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = tid / TPR, l = tid % TPR;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         } else {
           // A warp's 32 elements of one k lie in one group, and a group is 1, 2 or
           // 4 such blocks: block maxima, then a thread a group turns them into its
-          // scale, whose reciprocal the row's threads read.
+          // scale and its reciprocal, which the row's threads read.
           const int per_row = (NU + 31) / 32, groups = int(a.groups);
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
             for (int b = first; b < min(per_row, first + blocks); ++b) m = max(m, blk[bit][g * per_row + b]);
             const float s = scale_of(__uint_as_float(m), m >= 0x7f800000u, a.qtype);
             if (row_ok) a.scale[row * a.groups + c] = s;
+            scales[bit][g * groups + c] = s;
             invs[bit][g * groups + c] = 1.f / s;
           }
           __syncthreads();
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
           const int u = l + k * TPR;
           if (u >= NU) continue;
           if (!VEC && a.group != 0) {
+            s = scales[bit][g * int(a.groups) + (u >> shift)];
             inv = invs[bit][g * int(a.groups) + (u >> shift)];
           } else if (a.group != 0) {
             s = scale_of(__uint_as_float(um[k]), um[k] >= 0x7f800000u, a.qtype);
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
           }
           float* f = yv + k * E;
 #pragma unroll
-          for (int e = 0; e < E; ++e) f[e] *= inv;
+          for (int e = 0; e < E; ++e) f[e] = quotient(f[e], s, inv);
           U::store8(qrow, u, f, a.qtype);
         }
       }
@@ -384,7 +386,7 @@ struct NormTable {
       QK_NORM_SHAPE(OP, T, 512, 512, 4, true)
 
 // Static shared memory of the kernels (the block maxima and scales of the 8-bit output), kept free beside the ring.
-constexpr int kNormStaticSmem = 4096 + 16;
+constexpr int kNormStaticSmem = 6144 + 16;
 
 // Defined by the instantiation translation units: (operator, type) x (vectors, elements).
 NormTable norm_shapes_add_f32(bool vec);

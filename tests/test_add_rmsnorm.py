@@ -249,6 +249,26 @@ def test_quant_of_a_row_that_covers_every_code(cuda, dtype):
         check_quant(q, scale, y_ref, 0, qtype, qtype)
 
 
+@gpu
+@pytest.mark.parametrize("N", [4096, 1000, 1023])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("qtype", ["e4m3", "int8"])
+def test_quant_is_the_rounded_quotient(cuda, qtype, group, N):
+    """q against the division of the float32 y that the plain norm gives (the
+    same sums in the same order), rounded by torch: equal but where y itself
+    differs, which the equal rstd excludes."""
+    x, r, w = rows(300, N, "f32", 1).to(DEV), rows(300, N, "f32", 2, 3.0).to(DEV), syn.uniform_weight(N, "f32", 3, DEV)
+    y, _, rstd = qb.add_rmsnorm_fwd(x, r, w, eps=EPS)
+    _, qd, _ = QT[qtype]
+    q, scale, _, rstd2 = qb.rmsnorm_quant_fwd(x, w, residual=r, eps=EPS, group=group, qdtype=qd)
+    same = rstd == rstd2
+    assert same.any()
+    wide = torch.repeat_interleave(scale, group or N, 1)[:, :N]
+    want = y / wide
+    want = want.round() if qtype == "int8" else want.to(qd).float()
+    assert torch.equal(q.float()[same], want[same])
+
+
 def backward64(h, w, rstd, dy, dh):
     h, w, r, dy = to_f64(h), to_f64(w), to_f64(rstd)[:, None], to_f64(dy)
     up = 0.0 if dh is None else to_f64(dh)
