@@ -350,6 +350,34 @@ def test_backward_against_differences(cuda):
 
 
 @gpu
+def test_rows_beyond_32_bit_offsets(cuda):
+    """2.2e9 elements: sampled rows, the last among them, of every output."""
+    M, N = 540000, 4096
+    x, r = (torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for i in range(0, M, 54000):
+        x[i:i + 54000] = syn.normal_rows(54000, N, "bf16", i, DEV)
+        r[i:i + 54000] = syn.normal_rows(54000, N, "bf16", i + 1, DEV, sigma=3.0)
+    w = syn.uniform_weight(N, "bf16", 3, DEV)
+    at = torch.tensor([0, 1, 262143, 524287, 524288, 524289, M - 2, M - 1], device=DEV)
+    h_ref, y_ref, rstd_ref = forward64(x[at].cpu(), r[at].cpu(), w.cpu())
+    q, scale, none, _ = qb.rmsnorm_quant_fwd(x, w, residual=r, eps=EPS, group=128, want_h=False)
+    check_quant(q[at], scale[at].cpu(), y_ref, 128, "e4m3", "quant")
+    y, h, rstd = qb.add_rmsnorm_fwd(x, r, w, eps=EPS, out_h=r)
+    assert torch.equal(h[at].cpu(), h_ref)
+    check_scalars(to_f64(rstd[at]), rstd_ref, "rstd")
+    check_rows(to_f64(y[at]), y_ref, "bf16", False, "y")
+    dx, dw = qb.add_rmsnorm_bwd(h, w, rstd, x, y)
+    dx_ref, sx, _, _ = backward64(h_ref, w.cpu(), rstd[at].cpu(), x[at].cpu(), y[at].cpu())
+    check_scaled(to_f64(dx[at]), dx_ref, sx, "bf16", "dx")
+    ref, mag = torch.zeros(N, dtype=torch.float64, device=DEV), torch.zeros(N, dtype=torch.float64, device=DEV)
+    for i in range(0, M, 54000):
+        term = x[i:i + 54000].double() * h[i:i + 54000].double() * rstd[i:i + 54000, None].double()
+        ref += term.sum(0)
+        mag += term.abs().sum(0)
+    check_scaled(to_f64(dw), to_f64(ref), to_f64(mag), "f32", "dw")
+
+
+@gpu
 def test_zero_rows(cuda):
     w = torch.ones(64, device=DEV)
     e = torch.empty(0, 64, device=DEV)

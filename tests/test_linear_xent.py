@@ -151,11 +151,44 @@ def test_both_passes(cuda, dtype, M, V, K):
 @pytest.mark.parametrize("dtype,M,V,K", [("bf16", 1000, 2048, 1024), ("bf16", 4100, 40000, 64), ("f32", 2050, 20000, 40),
                                          ("bf16", 40, 33000, 512), ("f32", 24, 9000, 520), ("bf16", 2048, 300, 2056),
                                          ("bf16", 70000, 600, 32), ("bf16", 9000, 33000, 16), ("f32", 24, 50000, 520),
-                                         ("bf16", 16, 20000, 2049), ("f32", 65, 30000, 513), ("bf16", 64, 19457, 1032)])
+                                         ("bf16", 16, 20000, 2049), ("f32", 65, 30000, 513), ("bf16", 64, 19457, 1032),
+                                         ("bf16", 20000, 8000, 64), ("bf16", 20000, 7901, 67), ("f32", 20000, 3001, 64),
+                                         ("f32", 16, 3000, 4000), ("f32", 32, 2000, 2001)])
 def test_larger(cuda, dtype, M, V, K):
     """Several pieces of the vocabulary, long sums, many tokens on few columns and the reverse."""
     c = make(M, V, K, dtype, 77)
     check(c, run(c, 1e-4), 1e-4, what=f"{M}x{V}x{K} {dtype}")
+
+
+@gpu
+def test_weights_beyond_32_bit_offsets(cuda):
+    """A vocabulary of 2.2e9 weights: the last rows, the targets' rows and dh
+    against float64 over pieces of it."""
+    M, V, K = 5, 530000, 4096
+    w = torch.empty(V, K, dtype=torch.bfloat16, device=DEV)
+    for v in range(0, V, 53000):
+        w[v:v + 53000] = syn.normal_rows(53000, K, "bf16", 100 + v, DEV, sigma=2.0 / K ** 0.5)
+    c = {"h": syn.normal_rows(M, K, "bf16", 1, DEV), "w": w, "t": torch.tensor([V - 1, 0, 524288, 524287, IGNORE], device=DEV),
+         "dloss": torch.linspace(0.5, 1.5, M, device=DEV)}
+    out = run(c)
+    logits = torch.cat([c["h"].double() @ w[v:v + 53000].double().T for v in range(0, V, 53000)], 1)
+    e = 1e-5 * torch.stack([(c["h"].double().abs() @ w[v:v + 53000].double().abs().T).amax(1)
+                            for v in range(0, V, 53000)]).amax(0)
+    lse = torch.logsumexp(logits, 1)
+    near(out["lse"], lse, e + 1e-5 * lse.abs(), "lse")
+    d = torch.where(c["t"] == IGNORE, 0.0, c["dloss"].double())
+    one = torch.zeros_like(logits)
+    one[torch.arange(4), c["t"][:4]] = 1.0
+    p = torch.exp(logits - lse[:, None])
+    g, size = d[:, None] * (p - one), d[:, None] * (p + one)
+    rel = 2 * (1e-5 + 2 * e) + 2 ** -8  # as reference() has it
+    ref = sum(g[:, v:v + 53000] @ w[v:v + 53000].double() for v in range(0, V, 53000))
+    mag = sum(size[:, v:v + 53000] @ w[v:v + 53000].double().abs() for v in range(0, V, 53000))
+    near(out["dh"], ref, rel[:, None] * mag + 2 ** -8 * ref.abs(), "dh")
+    rows = torch.tensor([0, 1, 524286, 524287, 524288, V - 2, V - 1], device=DEV)
+    ref = g[:, rows].T @ c["h"].double()
+    near(out["dw"][rows], ref, rel.max() * (size[:, rows].T @ c["h"].double().abs()) + 2 ** -8 * ref.abs(), "dw")
+    assert torch.isfinite(out["dw"].view(-1)[::4097]).all()
 
 
 @gpu
