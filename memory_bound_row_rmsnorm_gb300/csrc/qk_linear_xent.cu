@@ -251,9 +251,14 @@ __global__ void __launch_bounds__(256) finish_kernel(const float* sum, int32_t l
     const int32_t j = int32_t(unit - i * per_row) * 4;
     const float4* s = reinterpret_cast<const float4*>(sum + i * ld + j);
     float4 v = s[0];
-    for (int k = 1; k < splits; ++k) {
-      const float4 x = s[k * (split_stride / 4)];
-      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    for (int k0 = 1; k0 < splits; k0 += 8) {  // eight loads in flight
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < splits) x[k] = s[(k0 + k) * (split_stride / 4)];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < splits) v = make_float4(v.x + x[k].x, v.y + x[k].y, v.z + x[k].z, v.w + x[k].w);
     }
     const float f[4] = {v.x, v.y, v.z, v.w};
     T* o = out + i * cols + j;
