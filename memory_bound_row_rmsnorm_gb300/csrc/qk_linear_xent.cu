@@ -30,9 +30,9 @@ namespace {
 
 constexpr int64_t kMaxDim = INT32_MAX - 15;  // TMA coordinates, and rows padded to 8, are 32-bit
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece
-constexpr int64_t kStageCopyBytes = int64_t(64) << 20;  // copied or split weights of one piece
+constexpr int64_t kStageCopyBytes = int64_t(256) << 20;  // copied or split weights of one piece: enough for a wave of tiles
 constexpr int kPairs = 76;  // CTA pairs of a GB300
-// Up to this many tokens the forward puts the vocabulary on the tile's rows and
+// Up to this many bf16 tokens the forward puts the vocabulary on the tile's rows and
 // the tokens on its 16 to 64 columns.  With tokens on the 256 rows the tensor
 // cores work through 240 empty ones at 16 tokens, 34 us at 32000 x 4096 where
 // reading w takes 39 us at the copy's rate; the columns cost them nothing.
@@ -48,37 +48,64 @@ int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
 // Rows of T into rows of bf16 planes whose row length is a multiple of 8 (what
 // TMA wants): float32 in three planes, bf16 (an unaligned tensor) copied.  A warp
-// takes a row, a lane two neighbouring columns at a time, so that every load and
-// store of a warp is whole lines.  What lies behind the last column is read by nobody.
-template <typename T>
+// takes a row; a lane takes 8 neighbouring columns at a time where the rows are
+// float32 vectors (VEC), else 2, so that a warp's loads and stores are whole
+// lines.  What lies behind the last column is read by nobody.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) planes_kernel(const T* in, int64_t rows, int32_t cols, __nv_bfloat16* out,
                                                      int32_t ld, int64_t plane_stride) {
+  static_assert(!VEC || sizeof(T) == 4, "16-byte loads of four floats");
   grid_dependency_wait();
   allow_dependent_launch();
+  constexpr int kCols = VEC ? 8 : 2, kUnroll = VEC ? 2 : 4;
   const int lane = threadIdx.x & 31;
   for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += int64_t(gridDim.x) * 8) {
     const T* src = in + i * cols;
     __nv_bfloat16* dst = out + i * ld;
-    constexpr int kUnroll = 4;
-    for (int j0 = 2 * lane; j0 < cols; j0 += 64 * kUnroll) {
-      T x[kUnroll][2];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) x[u][e] = j0 + 64 * u + e < cols ? src[j0 + 64 * u + e] : T(0.f);
+    for (int64_t j0 = kCols * lane; j0 < cols; j0 += 32 * kCols * kUnroll) {
+      T x[kUnroll][kCols];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int j = j0 + 64 * u;
-        if (j >= cols) break;  // ld is even: the pair stays inside the row
+        const int64_t j = j0 + 32 * kCols * u;
+        if constexpr (VEC) {  // cols is a multiple of 4
+#pragma unroll
+          for (int e = 0; e < kCols; e += 4) {
+            const float4 v = j + e < cols ? *reinterpret_cast<const float4*>(src + j + e) : float4{};
+            x[u][e] = v.x, x[u][e + 1] = v.y, x[u][e + 2] = v.z, x[u][e + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) x[u][e] = j + e < cols ? src[j + e] : T(0.f);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t j = j0 + 32 * kCols * u;
+        if (j >= cols) break;  // ld is a multiple of 8: the columns stay inside the row
         if constexpr (sizeof(T) == 2) {
           *reinterpret_cast<__nv_bfloat162*>(dst + j) = __nv_bfloat162{x[u][0], x[u][1]};
         } else {
-          __nv_bfloat16 a[3], b[3];
-          split3(x[u][0], a);
-          split3(x[u][1], b);
+          uint32_t o[3][kCols / 2];
 #pragma unroll
-          for (int pl = 0; pl < 3; ++pl)
-            *reinterpret_cast<__nv_bfloat162*>(dst + pl * plane_stride + j) = __nv_bfloat162{a[pl], b[pl]};
+          for (int e = 0; e < kCols; e += 2) {
+            __nv_bfloat16 a[3], b[3];
+            split3(x[u][e], a);
+            split3(x[u][e + 1], b);
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+              const __nv_bfloat162 v{a[pl], b[pl]};
+              o[pl][e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) {
+            __nv_bfloat16* to = dst + pl * plane_stride + j;
+            if constexpr (VEC) {
+              *reinterpret_cast<uint4*>(to) = make_uint4(o[pl][0], o[pl][1], o[pl][2], o[pl][3]);
+            } else {
+              *reinterpret_cast<uint32_t*>(to) = o[pl][0];
+            }
+          }
         }
       }
     }
@@ -323,12 +350,12 @@ int64_t choose_piece(int64_t M, int64_t V, int64_t K, int64_t most) {
 // k splits of dh's product over a piece: with few tiles (few rows, or a narrow
 // model) they give every pair work, with many they even out the last wave; each
 // costs a pass of fp32 sums through memory (written, and read once more).
-int choose_splits(int64_t M, int64_t K, int64_t steps) {
+int choose_splits(int64_t M, int64_t K, int64_t steps, int products) {
   const int64_t tiles = ceil_div(M, kTileM) * ceil_div(K, kTileN);
   int best = 1;
   double best_us = 1e30;
-  for (int s = 1; s <= kPairs && int64_t(s) * 16 <= std::max<int64_t>(steps, 16); ++s) {
-    const double us = double(waves(tiles * s)) * double(ceil_div(steps, s)) * 0.27 + (s > 1 ? s : 0) * (double(M) * double(K) * 8 / 6.0e6);
+  for (int s = 1; s <= kPairs && int64_t(s) * 16 <= std::max<int64_t>(steps * products, 16); ++s) {
+    const double us = double(waves(tiles * s)) * double(ceil_div(steps, s) * products) * 0.27 + (s > 1 ? s : 0) * (double(M) * double(K) * 8 / 6.0e6);
     if (us < 0.97 * best_us) best = s, best_us = us;
   }
   return best;
@@ -383,8 +410,9 @@ Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool co
     l.w = take(l.planes * l.piece * l.kp * 2);
   }
   if (!bwd) {
-    const int64_t pairs = M > kFewTokens ? 2 * ceil_div(V, kTileN)
-                                         : 2 * std::min<int64_t>(ceil_div(V, kTileM), kPairs * ceil_div(V, l.piece));
+    const int64_t pairs = M > kFewTokens || l.planes == 3
+                              ? 2 * ceil_div(V, kTileN)
+                              : 2 * std::min<int64_t>(ceil_div(V, kTileM), kPairs * ceil_div(V, l.piece));
     l.part = take(pairs * M * 8);
     l.at_target = take(M * 4);
   } else {
@@ -401,8 +429,8 @@ Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool co
     l.scale = take(4);
     l.ld_g = round_up(l.piece, 8);
     l.g = take(l.planes * M * l.ld_g * 2);
-    const int64_t steps = ceil_div(l.piece, kStepK) * (l.planes == 3 ? 6 : 1);
-    const int splits = choose_splits(M, K, steps);
+    const int64_t steps = ceil_div(l.piece, kStepK);
+    const int splits = choose_splits(M, K, steps, l.planes == 3 ? 6 : 1);
     l.split_steps = int(ceil_div(steps, splits));
     l.splits = int(ceil_div(steps, l.split_steps));
     l.sum = take(int64_t(l.splits) * M * l.kp * 4);
@@ -488,15 +516,15 @@ bool make_map(CUtensorMap* map, const Operand& o, int box_rows) {
 }
 
 // C [rows, cols] = A B^T over `depth`; the epilogue's fields of p are set by the caller.
-template <int EPI, bool A_MN, bool B_MN, typename T, int TN = kTileN>
-qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const Operand& b, int64_t rows,
+template <int EPI, bool A_MN, bool B_MN, typename T, int PLANES, int TN>
+qk_status launch_planes(const Call& c, ProductArgs p, const Operand& a, const Operand& b, int64_t rows,
                          int64_t cols, int64_t depth, int splits, int split_steps) {
-  const auto kernel = product_kernel<EPI, A_MN, B_MN, T, TN>;
+  const auto kernel = product_kernel<EPI, A_MN, B_MN, T, TN, PLANES>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
   const uint64_t bit = uint64_t(1) << (c.dev.index & 63);
   if (!(prepared.load(std::memory_order_acquire) & bit)) {
     cudaFuncAttributes fa;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem(TN)) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem(TN, PLANES)) != cudaSuccess ||
         cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
       cudaGetLastError();
       return QK_ERR_LAUNCH;
@@ -508,8 +536,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   }
   p.rows = int32_t(rows);
   p.cols = int32_t(cols);
-  p.planes = int32_t(a.planes);
-  p.chunk = a.planes == 3 ? 8 : 16;
+  p.chunk = PLANES == 3 ? 2 : 16;
   p.depth = int32_t(depth);
   p.steps = int32_t(ceil_div(depth, kStepK));
   p.m_tiles = int32_t(ceil_div(rows, kTileM));
@@ -519,10 +546,8 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   const int64_t rest = cols - int64_t(p.n_tiles - 1) * TN, unit = B_MN ? 128 : 32;
   p.last_n = TN < 256 ? TN : int32_t(std::min<int64_t>(TN, round_up(rest, unit)));
   p.n_full = p.last_n == TN ? p.n_tiles : p.n_tiles - 1;
-  const int64_t total = int64_t(p.steps) * (p.planes == 3 ? 6 : 1);
-  if (total > INT32_MAX) return QK_ERR_UNSUPPORTED;
-  p.split_steps = splits == 1 ? int32_t(total) : split_steps;
-  p.splits = int32_t(ceil_div(total, p.split_steps));
+  p.split_steps = splits == 1 ? p.steps : split_steps;
+  p.splits = int32_t(ceil_div(p.steps, p.split_steps));
   p.timeout_ns = kWaitTimeoutNs;
   p.status = c.dev.status;
   CUtensorMap ma, mb;
@@ -533,7 +558,7 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(tiles, std::min(kPairs, c.dev.sms / 2))), 1, 1);
   cfg.blockDim = dim3(kProductThreads, 1, 1);
-  cfg.dynamicSmemBytes = product_smem(TN);
+  cfg.dynamicSmemBytes = product_smem(TN, PLANES);
   cfg.stream = static_cast<cudaStream_t>(c.stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -550,6 +575,19 @@ qk_status launch_product(const Call& c, ProductArgs p, const Operand& a, const O
   return QK_OK;
 }
 
+// bf16 operands, or float32 ones in three planes.
+template <int EPI, bool A_MN, bool B_MN, typename T, int TN = kTileN>
+qk_status launch_product(const Call& c, const ProductArgs& p, const Operand& a, const Operand& b, int64_t rows,
+                         int64_t cols, int64_t depth, int splits, int split_steps) {
+  if constexpr (TN == kTileN && (sizeof(T) == 4 || EPI == kEpiLse)) {
+    if (a.planes == 3)
+      return launch_planes<EPI, A_MN, B_MN, T, 3, TN>(c, p, a, b, rows, cols, depth, splits, split_steps);
+  }
+  if constexpr (sizeof(T) == 2 || EPI == kEpiAccum)
+    return launch_planes<EPI, A_MN, B_MN, T, 1, TN>(c, p, a, b, rows, cols, depth, splits, split_steps);
+  return QK_ERR_UNSUPPORTED;  // not reached: float outputs have float operands
+}
+
 unsigned blocks(const Call& c, int64_t n) { return unsigned(std::min<int64_t>(ceil_div(n, 256), 32 * c.dev.sms)); }
 
 // Rows that TMA reads where they are: bf16, 16-byte aligned.
@@ -563,8 +601,15 @@ qk_status operand(const Call& c, const Layout& l, bool copied, const T* src, int
   *o = {src, c.K, rows, c.K, 1, 0};
   if (!copied) return QK_OK;
   *o = {at, c.K, rows, l.kp, l.planes, rows * l.kp};
-  return launch_pdl(planes_kernel<T>, dim3(unsigned(std::min<int64_t>(ceil_div(rows, 8), 16 * c.dev.sms))), 256, 0, c.stream, src, rows, int32_t(c.K),
-                    reinterpret_cast<__nv_bfloat16*>(at), int32_t(l.kp), rows * l.kp);
+  const dim3 grid(unsigned(std::min<int64_t>(ceil_div(rows, 8), 16 * c.dev.sms)));
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(at);
+  if constexpr (sizeof(T) == 4) {
+    if (c.K % 4 == 0 && aligned16(src))
+      return launch_pdl(planes_kernel<T, true>, grid, 256, 0, c.stream, src, rows, int32_t(c.K), out, int32_t(l.kp),
+                        rows * l.kp);
+  }
+  return launch_pdl(planes_kernel<T, false>, grid, 256, 0, c.stream, src, rows, int32_t(c.K), out, int32_t(l.kp),
+                    rows * l.kp);
 }
 
 // Launches of the fp32 kernels for few tokens.
@@ -648,12 +693,13 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean
   p.part_ld = c.M;
   p.at_target = reinterpret_cast<float*>(c.ws + l.at_target);
   int64_t pairs = 2 * ceil_div(c.V, kTileN);  // of a row, for the join
-  if (c.M <= kFewTokens) pairs = 0;
+  const bool by_columns = c.M <= kFewTokens && l.planes == 1;
+  if (by_columns) pairs = 0;
   for (p.v0 = 0; p.v0 < c.V && st == QK_OK; p.v0 += l.piece) {
     const int64_t width = std::min(l.piece, c.V - p.v0);
     st = operand(c, l, copied, static_cast<const T*>(c.w) + p.v0 * c.K, width, c.ws + l.w, &w);
     if (st != QK_OK) break;
-    if (c.M > kFewTokens) {
+    if (!by_columns) {
       st = launch_product<kEpiLse, false, false, __nv_bfloat16>(c, p, h, w, c.M, width, c.K, 1, 0);
       continue;
     }
@@ -666,7 +712,7 @@ qk_status forward(const Call& c, int dtype, float* loss, float* lse, float* mean
   if (st != QK_OK) return st;
   const LossArgs a = {p.part, p.part_ld, pairs, p.at_target, c.targets, c.M, c.V, c.has_ignore, c.z, c.ignore, loss, lse,
                       mean};
-  if (c.M <= kFewTokens) return launch_pdl(join_few_kernel, dim3(1), 1024, 0, c.stream, a);
+  if (by_columns) return launch_pdl(join_few_kernel, dim3(1), 1024, 0, c.stream, a);
   st = launch_pdl(join_kernel, dim3(unsigned(ceil_div(c.M, 32))), 1024, 0, c.stream, a);
   if (st != QK_OK || mean == nullptr) return st;
   return launch_pdl(xent_mean_kernel<0>, dim3(1), 1024, 0, c.stream, loss, c.targets, c.M, c.has_ignore, c.ignore,

@@ -15,8 +15,9 @@
 // sum over 8192 k measured 1e-5 off, where rounding to nearest gives 1e-6).  So
 // a chain ends after `chunk` steps of 64 k, and the chains of a tile are added in
 // registers, to nearest.  16 steps for bf16 (lse 3e-7 off at K = 4096), whose
-// outputs of consequence are bf16; 8 for float32, whose gradients measured
-// 1.3e-6 off with 16 and 7e-7 with 8, against 0.8 to 1.6e-6 of fp32 products.
+// outputs of consequence are bf16; 2 (48 products) for float32, whose gradients
+// are 4e-7 off, against 0.8 to 1.6e-6 of fp32 products (with 1 step 2e-7, for
+// 5 to 10 % more time).
 // Shorter chains cost time and power: with 8 steps the bf16 backward of 8192 x
 // 32000 x 4096 took 4.40 ms in a long run, with 16 4.31.
 //
@@ -25,8 +26,11 @@
 //
 // float32 operands come as three bf16 planes, x = x0 + x1 + x2 with 8 bits of
 // the significand each (what is left is below 2^-26 of x); the products x_a y_b
-// with a + b <= 2 are summed, the small ones first, as one long k axis.  What is
-// left out is below 2^-25 of a term.
+// with a + b <= 2 are summed, the small ones first.  What is left out is below
+// 2^-25 of a term.  A step loads its six operand tiles once for its six plane
+// pairs, half the bytes of two tiles for each: what steps of one pair wait for is
+// the way from L2 to the SMs (0.34 to 0.38 us for 64 KB a pair of CTAs, whatever
+// they multiply).  4096 x 16384 x 1024 backward: 1436 us, 1720 TFLOP/s of bf16 products.
 #pragma once
 
 #include "qk_internal.h"
@@ -48,10 +52,13 @@ enum Epilogue : int { kEpiLse = 0, kEpiGrad = 1, kEpiAccum = 2, kEpiStore = 3, k
 
 // Shared memory by the tile's columns TN: six stages of 32 KB, or ten of A's
 // 16 KB and B's TN / 2 rows when that is little, and the way out.
-__host__ __device__ constexpr int product_stages(int tn) { return tn == kTileN ? 6 : 10; }
-__host__ __device__ constexpr int product_stage_bytes(int tn) { return kABytes + tn / 2 * kStepK * 2; }
-__host__ __device__ constexpr int product_smem(int tn) {  // and room to start on 1024 bytes
-  return product_stages(tn) * product_stage_bytes(tn) + (tn == kTileN ? 8 * kOutBytes : 0) + 1024;
+// Three planes at once take two stages of 96 KB.
+__host__ __device__ constexpr int product_stages(int tn, int planes) { return planes == 3 ? 2 : tn == kTileN ? 6 : 10; }
+__host__ __device__ constexpr int product_stage_bytes(int tn, int planes) {
+  return planes * (kABytes + tn / 2 * kStepK * 2);
+}
+__host__ __device__ constexpr int product_smem(int tn, int planes) {  // and room to start on 1024 bytes
+  return product_stages(tn, planes) * product_stage_bytes(tn, planes) + (tn == kTileN ? 8 * kOutBytes : 0) + 1024;
 }
 
 struct XentRow {   // what the gradient needs of a row
@@ -61,9 +68,8 @@ struct XentRow {   // what the gradient needs of a row
 
 struct ProductArgs {
   int32_t rows, cols;        // of C
-  int32_t steps;             // steps of 64 k in one plane pair
-  int32_t depth;             // k in one plane pair
-  int32_t planes;            // 1 (bf16) or 3 (float32)
+  int32_t steps;             // steps of 64 k
+  int32_t depth;             // k
   int32_t m_tiles, n_tiles;
   int32_t n_full, last_n;    // column tiles of TN columns (the first ones); columns of a product in the last
   int32_t chunk;             // steps of one chain of products
@@ -180,11 +186,13 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs& p, uint32_t t) {
   return r;
 }
 
-template <int EPI, bool A_MN, bool B_MN, typename T, int TN>
+template <int EPI, bool A_MN, bool B_MN, typename T, int TN, int PLANES>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const ProductArgs p) {
-  constexpr int kStages = product_stages(TN), kStageBytes = product_stage_bytes(TN);
+  constexpr int kStages = product_stages(TN, PLANES), kStageBytes = product_stage_bytes(TN, PLANES);
+  constexpr int kBBytes = TN / 2 * kStepK * 2;  // one CTA's part of a step of B
+  static_assert(PLANES == 1 || TN == kTileN, "three planes at once: full tiles");
   // A product of few columns waits for the one before it on the same sums, some
   // 125 cycles where its own work is 16 to 64; so a step's products of 16 k go to
   // four sets of sums (two at 128 columns), which the epilogue adds.  Tiles of TN
@@ -207,8 +215,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t ring = (smem_addr(dynamic_smem) + 1023u) & ~1023u;  // the same in both CTAs
   const uint32_t tiles = uint32_t(p.m_tiles) * uint32_t(p.n_tiles) * uint32_t(p.splits);
   const uint32_t first_tile = cluster_id_x(), tile_step = num_clusters_x();
-  const int pairs = p.planes == 3 ? 6 : 1;
-  const int total_steps = pairs * p.steps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // Only g's product: a narrow tile of dw or dh waits for A's steps all the
     // same (2047 x 8191 x 513 fp32: 148 us without, 151 with), and the forward's
     // loop is 3 % slower with the choice in it.
-    if (TN < kTileN || EPI != kEpiGrad) return kParts;
+    if (TN < kTileN || EPI != kEpiGrad || PLANES == 3) return kParts;
     return n < p.n_full || p.last_n > 128 ? 1 : p.last_n > 64 ? 2 : 4;
   };
   bool failed = false;
@@ -264,31 +270,30 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
         const TileAt at = tile_at(p, t);
         const int a0 = at.m * kTileM + int(rank) * 128, b0 = at.n * TN + int(rank) * (at.n < p.n_full ? half_n : p.last_n / 2);
-        const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
-        int pair = s0 / p.steps, in_pair = s0 % p.steps;
+        const int s0 = at.split * p.split_steps, s1 = min(p.steps, s0 + p.split_steps);
         for (int s = s0; s < s1; ++s, ++q) {
           if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
-          const int k = in_pair * kStepK;
-          // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0): the small products first
-          const int pa = pairs == 1 ? 0 : pair < 3 ? 2 - pair : pair == 3 ? 1 : 0;
-          const int pb = pairs == 1 ? 0 : pair < 3 ? pair : pair == 4 ? 1 : 0;
+          const int k = s * kStepK;
           const uint32_t bar = map_to_rank(full0 + 8 * st, 0);
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, bytes);
-          const uint32_t da = ring + uint32_t(st) * kStageBytes, db = da + kABytes;
-          if constexpr (A_MN) {
-            tma_load_3d(da, &map_a, a0, k, pa, bar);
-            tma_load_3d(da + kABytes / 2, &map_a, a0 + 64, k, pa, bar);
-          } else {
-            tma_load_3d(da, &map_a, k, a0, pa, bar);
-          }
-          if constexpr (B_MN) {
-            for (int i = 0; i < half_n / 64; ++i)
-              tma_load_3d(db + uint32_t(i) * (64 * kStepK * 2), &map_b, b0 + 64 * i, k, pb, bar);
-          } else {
-            tma_load_3d(db, &map_b, k, b0, pb, bar);
+          const uint32_t sa = ring + uint32_t(st) * kStageBytes, sb = sa + PLANES * kABytes;
+#pragma unroll
+          for (int pl = 0; pl < PLANES; ++pl) {
+            const uint32_t da = sa + pl * kABytes, db = sb + pl * kBBytes;
+            if constexpr (A_MN) {
+              tma_load_3d(da, &map_a, a0, k, pl, bar);
+              tma_load_3d(da + kABytes / 2, &map_a, a0 + 64, k, pl, bar);
+            } else {
+              tma_load_3d(da, &map_a, k, a0, pl, bar);
+            }
+            if constexpr (B_MN) {
+              for (int i = 0; i < half_n / 64; ++i)
+                tma_load_3d(db + uint32_t(i) * (64 * kStepK * 2), &map_b, b0 + 64 * i, k, pl, bar);
+            } else {
+              tma_load_3d(db, &map_b, k, b0, pl, bar);
+            }
           }
           if (++st == kStages) st = 0, turn ^= 1u;
-          if (++in_pair == p.steps) in_pair = 0, ++pair;
         }
       }
       // A failed launch leaves once the loads in flight have landed: the leader's
@@ -305,11 +310,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       uint32_t turn = 0, it = 0;  // it: chains begun
       for (uint32_t t = first_tile; t < tiles && !failed; t += tile_step) {
         const TileAt at = tile_at(p, t);
-        const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+        const int s0 = at.split * p.split_steps, s1 = min(p.steps, s0 + p.split_steps);
         const uint32_t idesc = instruction_desc(A_MN, B_MN, at.n < p.n_full ? uint32_t(TN) : uint32_t(p.last_n));
         const int parts = parts_of(at.n);
         const uint32_t stride = uint32_t(kSet / parts);
-        int in_pair = s0 % p.steps;
         for (int c0 = s0; c0 < s1 && !failed; c0 += p.chunk, ++it) {
           const uint32_t acc = it & 1u;
           if (!wait(free0 + 8 * acc, ((it >> 1) & 1u) ^ 1u)) break;
@@ -320,10 +324,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (!wait(full0 + 8 * st, turn)) break;
             tcgen05_fence_after();
             const uint32_t sa = ring + uint32_t(st) * kStageBytes;
-            const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0), db = operand_desc(sa + kABytes, B_MN ? kLbo : 0);
-            const bool tail = ++in_pair == p.steps;  // a plane pair's last step may hold fewer k
-            if (tail) in_pair = 0;
-            if (parts == 1 && tail && tail_parts < kStepK / 16) {
+            const uint64_t da = operand_desc(sa, A_MN ? kLbo : 0);
+            const uint64_t db = operand_desc(sa + PLANES * kABytes, B_MN ? kLbo : 0);
+            const bool tail = s == p.steps - 1;  // the last step may hold fewer k
+            if constexpr (PLANES == 3) {  // the six plane pairs of these k, the small ones first
+              const int count = tail ? tail_parts : kStepK / 16;
+              bool add = s > c0;
+#pragma unroll
+              for (int pair = 0; pair < 6; ++pair) {
+                const int pa = pair < 3 ? 2 - pair : pair == 3 ? 1 : 0, pb = pair < 3 ? pair : pair == 4 ? 1 : 0;
+                for (int k = 0; k < count; ++k) {
+                  mma_bf16_pair(d, da + uint64_t(pa * (kABytes >> 4) + k * kAStep),
+                                db + uint64_t(pb * (kBBytes >> 4) + k * kBStep), idesc, add);
+                  add = true;
+                }
+              }
+            } else if (parts == 1 && tail && tail_parts < kStepK / 16) {
               for (int k = 0; k < tail_parts; ++k)
                 mma_bf16_pair(d, da + uint64_t(k) * kAStep, db + uint64_t(k) * kBStep, idesc, s > c0 || k > 0);
             } else {
@@ -363,7 +379,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t it = 0;
     for (uint32_t t = first_tile; t < tiles && !failed && half * kCols < TN; t += tile_step) {
       const TileAt at = tile_at(p, t);
-      const int s0 = at.split * p.split_steps, s1 = min(total_steps, s0 + p.split_steps);
+      const int s0 = at.split * p.split_steps, s1 = min(p.steps, s0 + p.split_steps);
       const int64_t i = int64_t(at.m) * kTileM + rank * 128 + quarter * 32 + lane;
       const int64_t j0 = int64_t(at.n) * TN + half * kCols;
       const bool live = i < p.rows;
