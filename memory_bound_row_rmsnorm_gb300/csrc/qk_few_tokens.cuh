@@ -4,10 +4,10 @@
 // What bounds it is reading w once (and writing dw): the bf16 planes that the
 // products of qk_product_kernel.cuh want move 12 bytes more for each 4-byte
 // weight and pass, while at 16 tokens a weight costs 16 multiplications, which
-// the SMs keep up with at about the memory's rate.  80000 x 464: forward of 4
-// tokens 185 us by planes, 33 so; of 32 tokens 191 and 106; backward of 4 tokens
-// 463 and 147, of 32 434 and 418.  (bf16 rows that have to be copied are faster
-// by the products from 4 tokens on: one copy, and a quarter of the bytes.)
+// the SMs keep up with at about the memory's rate.  80000 x 464, by planes and so:
+// forward of 4 to 32 tokens 148 us, and 35 (4 tokens), 66 (16) or 106 (32);
+// backward 287 us, and 102, 190 or 310.  (bf16 rows that have to be copied are
+// faster by the products from 4 tokens on: one copy, and a quarter of the bytes.)
 #pragma once
 
 #include "qk_product_kernel.cuh"  // XentRow

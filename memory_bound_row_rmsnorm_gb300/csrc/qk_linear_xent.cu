@@ -373,8 +373,12 @@ Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool co
     return o;
   };
   // Few float32 tokens: the fp32 kernels (qk_few_tokens.cuh), while g stays within a piece.
+  // The backward of 17 to 32 tokens multiplies more than it moves: by the fp32
+  // kernels 87 us at 8000 x 1024, 149 at 16000 x 1024, 540 at 30000 x 2048 and
+  // 342 at 8000 x 4096; by the products 100, 139, 453 and 289.
   const int mt = M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
-  if (dtype == QK_F32 && M <= 32 && V * mt * 4 <= kPieceBytes) {
+  const int64_t most_few = bwd && V > (int64_t(1) << 24) / K ? 16 : 32;
+  if (dtype == QK_F32 && M <= most_few && V * mt * 4 <= kPieceBytes) {
     l.few = mt;
     l.few_chunk = int(std::min<int64_t>(round_up(K, 128), kFewSmem / (mt * 4) / 128 * 128));
     l.few_grid = int(std::min<int64_t>(ceil_div(V, 16 * (64 / mt > 8 ? 8 : 64 / mt)), 2 * kPairs));
