@@ -161,6 +161,27 @@ def test_larger(cuda, dtype, M, V, K):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,M,V,K", [("f32", 40, 90000, 513), ("f32", 700, 50000, 1040), ("bf16", 16, 70000, 2049),
+                                         ("bf16", 200, 140000, 1025)])
+def test_weights_copied_in_pieces(cuda, dtype, M, V, K):
+    """More weights than the workspace holds at a time as bf16 planes or aligned
+    rows, of vectors and of single elements."""
+    c = make(M, V, K, dtype, 78)
+    planes = 3 if dtype == "f32" else 1
+    assert planes * V * ((K + 7) // 8 * 8) * 2 > 2 ** 28
+    for off in (0, 1):
+        check(c, run(c, 1e-4, off=off), 1e-4, what=f"{M}x{V}x{K} {dtype} offset {off}")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_vocabulary_of_millions(cuda, dtype):
+    """Few float32 tokens whose gradient of the logits is more than one piece."""
+    c = make(20, 2200000, 8, dtype, 79)
+    check(c, run(c), what=f"20x2200000x8 {dtype}")
+
+
+@gpu
 def test_weights_beyond_32_bit_offsets(cuda):
     """A vocabulary of 2.2e9 weights: the last rows, the targets' rows and dh
     against float64 over pieces of it."""
