@@ -349,7 +349,9 @@ typedef enum { QK_E4M3 = 0, QK_INT8 = 1 } qk_qtype;
  * whole row), with qmax = 448 (QK_E4M3) or 127 (QK_INT8):
  *   scale[i,c] = max(max_{j in group c} |y[i,j]|, 2^-100) / qmax
  *   q[i,j]     = y[i,j] / scale[i,c], rounded to nearest even
- * so that q * scale stands for y.  A group of zeros has a positive scale.  A
+ * so that q * scale stands for y.  With bfloat16 rows the quotient is of the
+ * exact products h w, in which rstd cancels: what lies on a tie goes to even,
+ * whatever the order in which the row was summed.  A group of zeros has a positive scale.  A
  * group with an infinite or NaN y gets scale = NaN, and so does everything
  * that its q stand for.
  *

@@ -44,10 +44,6 @@ struct NormArgs {
 };
 
 __device__ __forceinline__ float qmax_of(int qtype) { return qtype == 0 ? 448.f : 127.f; }
-// The scale of a group from its largest |y|; `bad` when a y of the group is not finite.
-__device__ __forceinline__ float scale_of(float amax, bool bad, int qtype) {
-  return bad ? __int_as_float(0x7fc00000) : fmaxf(amax, kSmallestGroupMax) / qmax_of(qtype);
-}
 // y / s with inv = 1 / s rounded: the product's residual corrects it (Markstein's
 // division step), so that what is rounded to 8 bits is the rounded quotient, not
 // one that the reciprocal's rounding moved across a tie.  A NaN s stays NaN.
@@ -55,6 +51,62 @@ __device__ __forceinline__ float quotient(float y, float s, float inv) {
   const float q = y * inv;
   return fmaf(fmaf(-q, s, y), inv, q);
 }
+// The scale of a group from its largest |y|; `bad` when a y of the group is not
+// finite.  By quotient(), which is the rounded division for all of these (every
+// significand was tried), in a third of a division's instructions.
+__device__ __forceinline__ float scale_of(float amax, bool bad, int qtype) {
+  const float s = quotient(fmaxf(amax, kSmallestGroupMax), qmax_of(qtype), qtype == 0 ? 1.f / 448.f : 1.f / 127.f);
+  return bad ? __int_as_float(0x7fc00000) : s;
+}
+
+// An element of a row on its way to 8 bits, and the scale of a group of them.
+// Each stands as (h mul) w, of which scale() gets the group's largest; what is
+// rounded is quotient((h mul) w, den, 1 / den).
+//
+// float32: that is y, and den is the scale.
+// bf16: a product h w has 16 bits of significand, and of y = h rstd w only rstd
+// has more, which the quotient does not depend on.  So rstd is left out but for
+// its power of two: mul = 2^e qmax / 2^k (448 = 7 / 8 2^9, 127 = 127 / 128 2^7)
+// makes y' = (h mul) w exact in 23 bits, and y / scale = y' / (max |h 2^e w| / 2^k)
+// is one division of exact numbers.  A quotient that lies on a tie is one
+// then, and goes to even.  From a rounded y it goes to either side with the last
+// bit of rstd, which the order of a row's sum decides: at 16384 x 4096 one
+// value in 10000 lies on a tie, and their error was 8.7e-4 of q's norm.
+template <typename T>
+struct EightBits {
+  float mul, rest = 1.f, low = 0.f;  // y = (h mul) w 2^k / qmax * rest; low: kSmallestGroupMax / rest
+  __device__ __forceinline__ EightBits(float rs, int qtype) : mul(rs) {
+    if constexpr (sizeof(T) == 2) {  // rs is 0, infinite, NaN or a normal number: 1 / sqrt of a float32
+      const uint32_t b = __float_as_uint(rs);
+      mul = __uint_as_float(b & 0x7f800000u) * (qtype == 0 ? 0.875f : 0.9921875f);
+      rest = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
+      low = kSmallestGroupMax / rest;
+    }
+  }
+  __device__ __forceinline__ float scale(float m, int qtype, float* den) const {
+    if constexpr (sizeof(T) == 4) {
+      return *den = scale_of(m, !(m < __int_as_float(0x7f800000)), qtype);
+    } else {
+      // m 2^k / qmax = m + m / 7 or m + m / 127, a number of 16 bits: the
+      // constant's rounding is 2^-27 or less of the sum and does not show.
+      const float top = fmaf(m, qtype == 0 ? 1.f / 7.f : 1.f / 127.f, m);
+      const float amax = top * rest;
+      const bool bad = !(amax < __int_as_float(0x7f800000));
+      const float s = scale_of(amax, bad, qtype);
+      *den = bad ? s : fmaxf(top, low) * (qtype == 0 ? 0x1p-9f : 0x1p-7f);
+      return s;
+    }
+  }
+  // 1 / den.  For bf16 den is below 2^122, far from where the approximation
+  // ends, and a step of Newton's is enough: quotient() finds a tie from any
+  // reciprocal within a bit or two.
+  __device__ __forceinline__ static float inverse(float den) {
+    if constexpr (sizeof(T) == 4) return 1.f / den;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(den));
+    return fmaf(fmaf(-den, r, 1.f), r, r);
+  }
+};
 // One value in 8 bits, to nearest even.  |v| exceeds qmax by rounding at most, which saturates.
 __device__ __forceinline__ uint32_t quantise(float v, int qtype) {
   if (qtype == 0) return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
@@ -150,26 +202,30 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
       const float rs = 1.f / sqrtf(fmaf(cta_sum<TH>(ss, red[0]), a.inv_n, a.eps));
       if (tid == 0 && a.rstd != nullptr) a.rstd[row] = rs;
       // From here on h (when kept) is what is read: x or r may be gone.
-      auto normed = [&](int64_t j) { return (h != nullptr ? V::load1(h + j) : value(j)) * rs * V::load1(w + j); };
+      auto scaled = [&](int64_t j, float f) { return (h != nullptr ? V::load1(h + j) : value(j)) * f * V::load1(w + j); };
       if constexpr (OP == kAddNorm) {
         T* y = static_cast<T*>(a.y) + row * N;
-        for (int64_t j = tid; j < N; j += TH) V::store1(y + j, normed(j));
+        for (int64_t j = tid; j < N; j += TH) V::store1(y + j, scaled(j, rs));
       } else {
         uint8_t* q = static_cast<uint8_t*>(a.y) + row * N;
         float* sc = a.scale + row * a.groups;
+        const EightBits<T> eight(rs, a.qtype);
+        constexpr float kNan = __builtin_nanf("");
         if (a.group == 0) {
           float m = 0.f, bad = 0.f;
           for (int64_t j = tid; j < N; j += TH) {
-            const float v = fabsf(normed(j));
+            const float v = fabsf(scaled(j, eight.mul));
             m = fmaxf(m, v);
             if (!(v < __int_as_float(0x7f800000))) bad = 1.f;
           }
           m = cta_max<TH>(m, red[1]);
           bad = cta_max<TH>(bad, red[2]);
-          const float s = scale_of(m, bad > 0.f, a.qtype);
+          float den;
+          const float s = eight.scale(bad > 0.f ? kNan : m, a.qtype, &den);
           if (tid == 0) sc[0] = s;
-          const float inv = 1.f / s;
-          for (int64_t j = tid; j < N; j += TH) q[j] = uint8_t(quantise(quotient(normed(j), s, inv), a.qtype));
+          const float inv = eight.inverse(den);
+          for (int64_t j = tid; j < N; j += TH)
+            q[j] = uint8_t(quantise(quotient(scaled(j, eight.mul), den, inv), a.qtype));
         } else {
           __syncthreads();  // a warp reads what others kept of h
           for (int64_t g = warp; g < a.groups; g += TH / 32) {
@@ -178,18 +234,19 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // a group has at most 128 columns
               const int64_t j = g * a.group + lane + 32 * k;
-              v[k] = 32 * k < a.group && j < N ? normed(j) : 0.f;
+              v[k] = 32 * k < a.group && j < N ? scaled(j, eight.mul) : 0.f;
               m = fmaxf(m, fabsf(v[k]));
               bad |= !(fabsf(v[k]) < __int_as_float(0x7f800000));
             }
             m = group_max<32>(m);
-            const float s = scale_of(m, __any_sync(0xffffffffu, bad), a.qtype);
+            float den;
+            const float s = eight.scale(__any_sync(0xffffffffu, bad) ? kNan : m, a.qtype, &den);
             if (lane == 0) sc[g] = s;
-            const float inv = 1.f / s;
+            const float inv = eight.inverse(den);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int64_t j = g * a.group + lane + 32 * k;
-              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(quotient(v[k], s, inv), a.qtype));
+              if (32 * k < a.group && j < N) q[j] = uint8_t(quantise(quotient(v[k], den, inv), a.qtype));
             }
           }
         }

@@ -66,10 +66,10 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
   float* red = reinterpret_cast<float*>(smem + 512);             // [2][16] warp sums
   uint32_t* redm = reinterpret_cast<uint32_t*>(smem + 640);      // [2][16] warp maxima
   unsigned char* ring = smem + kSmemHeader;
-  // 8-bit output by elements: maxima of 32 columns, a group's scale and 1 / scale
+  // 8-bit output by elements: maxima of 32 columns, a group's divisor and its reciprocal
   constexpr bool kBlocks = OP == kNormQuant && !VEC;
   __shared__ uint32_t blk[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
-  __shared__ float scales[kBlocks ? 2 : 1][kBlocks ? 256 : 1], invs[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
+  __shared__ float dens[kBlocks ? 2 : 1][kBlocks ? 256 : 1], invs[kBlocks ? 2 : 1][kBlocks ? 256 : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = tid / TPR, l = tid % TPR;
@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
           U::store(a.y, base + u, U::pack(f));
         }
       } else {
-        // Largest |y| of each unit, as bits: ordered like the numbers, infinity and NaN on top.
+        // Largest |y| (times what EightBits has beside it) of each unit, as bits:
+        // ordered like the numbers, infinity and NaN on top.
+        const EightBits<T> eight(rs, a.qtype);
         float yv[VPT * E];
         uint32_t um[VPT], rowm = 0;
 #pragma unroll
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
           um[k] = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            f[e] = (f[e] * rs) * fw[e];
+            f[e] = (f[e] * eight.mul) * fw[e];
             um[k] = max(um[k], __float_as_uint(fabsf(f[e])));
           }
           rowm = max(rowm, um[k]);
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         } else {
           // A warp's 32 elements of one k lie in one group, and a group is 1, 2 or
           // 4 such blocks: block maxima, then a thread a group turns them into its
-          // scale and its reciprocal, which the row's threads read.
+          // scale, its divisor and the reciprocal, which the row's threads read.
           const int per_row = (NU + 31) / 32, groups = int(a.groups);
 #pragma unroll
           for (int k = 0; k < VPT; ++k) {
@@ -280,21 +282,22 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
             const int blocks = a.group / 32, first = c * blocks;
             uint32_t m = 0;
             for (int b = first; b < min(per_row, first + blocks); ++b) m = max(m, blk[bit][g * per_row + b]);
-            const float s = scale_of(__uint_as_float(m), m >= 0x7f800000u, a.qtype);
+            float den;
+            const float s = eight.scale(__uint_as_float(m), a.qtype, &den);
             if (row_ok) a.scale[row * a.groups + c] = s;
-            scales[bit][g * groups + c] = s;
-            invs[bit][g * groups + c] = 1.f / s;
+            dens[bit][g * groups + c] = den;
+            invs[bit][g * groups + c] = eight.inverse(den);
           }
           __syncthreads();
         }
         if (!row_ok) continue;
         uint8_t* qrow = static_cast<uint8_t*>(a.y) + row * N;
         float* srow = a.scale + row * a.groups;
-        float s = 0.f, inv = 0.f;
+        float den = 0.f, inv = 0.f;
         const int shift = 31 - __clz(a.group);  // groups are powers of two
         if (a.group == 0) {
-          s = scale_of(__uint_as_float(rowm), rowm >= 0x7f800000u, a.qtype);
-          inv = 1.f / s;
+          const float s = eight.scale(__uint_as_float(rowm), a.qtype, &den);
+          inv = eight.inverse(den);
           if (l == 0) srow[0] = s;
         }
 #pragma unroll
@@ -302,16 +305,16 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
           const int u = l + k * TPR;
           if (u >= NU) continue;
           if (!VEC && a.group != 0) {
-            s = scales[bit][g * int(a.groups) + (u >> shift)];
+            den = dens[bit][g * int(a.groups) + (u >> shift)];
             inv = invs[bit][g * int(a.groups) + (u >> shift)];
           } else if (a.group != 0) {
-            s = scale_of(__uint_as_float(um[k]), um[k] >= 0x7f800000u, a.qtype);
-            inv = 1.f / s;
+            const float s = eight.scale(__uint_as_float(um[k]), a.qtype, &den);
+            inv = eight.inverse(den);
             if (((u * E) & (a.group - 1)) == 0) srow[(u * E) >> shift] = s;
           }
           float* f = yv + k * E;
 #pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = quotient(f[e], s, inv);
+          for (int e = 0; e < E; ++e) f[e] = quotient(f[e], den, inv);
           U::store8(qrow, u, f, a.qtype);
         }
       }

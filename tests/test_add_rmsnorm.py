@@ -269,6 +269,96 @@ def test_quant_is_the_rounded_quotient(cuda, qtype, group, N):
     assert torch.equal(q.float()[same], want[same])
 
 
+def eight_bits_of_the_ratio(h, w, group, qtype):
+    """q of bf16 rows by the definition alone: h w qmax / max |h w|, in which
+    the row's rstd cancels.  In float64 the products are exact, the quotient is
+    rounded once, and what lies on a tie is one: such a quotient has few bits.
+    (One that is off a tie is so by 2^-24 of itself at least, since h w has 16
+    bits, so float32's rounding on the way to e4m3 makes none.)"""
+    p = to_f64(h) * to_f64(w)[None, :]
+    M, N = p.shape
+    g = group or N
+    pieces = -(-N // g)
+    pad = np.zeros((M, pieces * g))
+    pad[:, :N] = np.abs(p)
+    top = np.repeat(pad.reshape(M, pieces, g).max(2), g, 1)[:, :N]
+    v = np.divide(p * QT[qtype][2], top, out=np.zeros_like(p), where=top > 0)
+    ties = v * 2 - np.floor(v * 2) == 0 if qtype == "int8" else np.zeros_like(v, dtype=bool)
+    if qtype == "e4m3":
+        step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -40))), -6) - 3)
+        u = np.abs(v) / step
+        return torch.from_numpy(v).float().to(torch.float8_e4m3fn), int((u - np.floor(u) == 0.5).sum())
+    return torch.from_numpy(np.rint(v)).to(torch.int8), int((ties & (v != np.floor(v))).sum())
+
+
+@gpu
+@pytest.mark.parametrize("M,N,off", [(64, 4096, 0), (200, 264, 0), (64, 1003, 0), (40, 2048, 1), (8, 8192, 0), (3, 9001, 0),
+                                     (2, 32768, 0), (2, 40000, 0)])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("qtype", ["e4m3", "int8"])
+def test_quant_ties_go_to_even(cuda, qtype, group, M, N, off):
+    """bf16 rows: every value is the rounded quotient, those on a tie the even
+    one, though the order of a row's sum moves rstd by a bit."""
+    code, td = DT["bf16"]
+    qc, qd, _ = QT[qtype]
+    gen = torch.Generator().manual_seed(N + group)
+    ties = 0
+    for few_bits in (False, True):  # integers up to 96 meet many ties, normal values few
+        x = rows(M, N, "bf16", N, 3.0)
+        w = syn.uniform_weight(N, "bf16", N + 2, "cpu")
+        if few_bits:
+            x = torch.randint(-96, 97, (M, N), generator=gen).to(td)
+            w = torch.ones(N, dtype=td)
+        for c in (1.0, 2.0 ** 20, 1.5 * 2.0 ** -9):  # rows of other sizes: another rstd, the same q
+            h = x * torch.tensor(c, dtype=td) if not few_bits else (x.float() * c).to(td)
+            want, n = eight_bits_of_the_ratio(h, w, group, qtype)
+            ties += n
+            q, cq = guarded((M, N), torch.int8, off)
+            scale, cs = guarded((M, -(-N // group) if group else 1), torch.float32)
+            qb.qk_rmsnorm_quant_fwd(shifted(h, off), None, shifted(w, off), q, scale, None, None, M, N, 1e-12, group, code,
+                                    qc)
+            torch.cuda.synchronize()
+            cq("q"), cs("scale")
+            assert torch.equal(q.view(qd).float().cpu(), want.float()), (few_bits, c)
+    assert ties > 20
+
+
+@gpu
+@pytest.mark.parametrize("N,off", [(256, 0), (264, 1), (9001, 0)])
+@pytest.mark.parametrize("qtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quant_at_the_ends_of_the_range(cuda, dtype, qtype, N, off):
+    """Groups whose largest y lies about 2^-100, where the scale stops; a y
+    beyond float32, and one just below its end."""
+    code, td = DT[dtype]
+    qc, qd, _ = QT[qtype]
+    for group in (0, 32):
+        groups = -(-N // group) if group else 1
+        x = rows(12, N, dtype, 1) * (2.0 ** torch.arange(-116, -104, dtype=torch.float64)[:, None]).to(td)
+        w = syn.uniform_weight(N, dtype, 2, "cpu")
+        q, cq = guarded((12, N), torch.int8, off)
+        scale, cs = guarded((12, groups), torch.float32)
+        qb.qk_rmsnorm_quant_fwd(shifted(x, off), None, shifted(w, off), q, scale, None, None, 12, N, EPS, group, code, qc)
+        torch.cuda.synchronize()
+        cq("q"), cs("scale")
+        _, y, _ = forward64(x, None, w)
+        assert (np.abs(y).max(1) < 2.0 ** -100).any() and (np.abs(y).max(1) > 2.0 ** -100).any()
+        check_quant(q.view(qd), scale, y, group, qtype, "tiny")
+        x = torch.ones(3, N, dtype=td)
+        x[0, 1] = 0.75
+        x[1, 1] = 4.0
+        w = torch.ones(N, dtype=td)
+        w[1] = 2.0 ** 127 * 1.5  # y: below float32's end, beyond it, and by a quarter below the end again
+        x[2, 1] = 1.0
+        q, scale, _, rstd = qb.rmsnorm_quant_fwd(shifted(x, off), shifted(w, off), eps=EPS, group=group, qdtype=qd)
+        y = to_f64(x) * to_f64(rstd)[:, None] * to_f64(w)
+        over = np.abs(y).max(1) > 3.4028235e38
+        assert list(over) == [False, True, False]
+        assert np.array_equal(np.isnan(to_f64(scale)[:, 0]), over)
+        assert torch.isfinite(scale[:, 1:]).all()
+        check_quant(q[~torch.from_numpy(over)], scale[~torch.from_numpy(over)], y[~over], group, qtype, "large")
+
+
 def backward64(h, w, rstd, dy, dh):
     h, w, r, dy = to_f64(h), to_f64(w), to_f64(rstd)[:, None], to_f64(dy)
     up = 0.0 if dh is None else to_f64(dh)
