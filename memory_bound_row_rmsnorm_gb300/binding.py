@@ -9,7 +9,8 @@ The ``softmax_fwd`` / ``rmsnorm_fwd`` / ``layernorm_fwd`` / ``xent_fwd`` helpers
 and return CUDA tensors (they allocate the outputs with PyTorch and then call
 the C entry points), and so do ``add_rmsnorm_fwd`` / ``add_rmsnorm_bwd`` /
 ``rmsnorm_quant_fwd`` / ``linear_xent_fwd`` / ``linear_xent_bwd``, which allocate
-their workspaces too.
+their workspaces too.  A helper runs on torch's current stream, or on the
+``stream`` it is given, which has to have waited for the inputs.
 """
 from __future__ import annotations
 
@@ -323,6 +324,34 @@ def qk_test_wait_timeout(timeout_ns: int, stream=None) -> None:
 
 
 # --- tensor helpers ----------------------------------------------------------
+def _on(stream, helper, *args):
+    """helper(*args) on `stream` (a torch.cuda.Stream or a cudaStream_t).  Torch
+    hands freed memory out again at once, in the order of the stream that it
+    belongs to.  So `stream` is torch's current one meanwhile, and what the
+    helper allocates is that stream's: memory of the caller's stream may have
+    work on that stream before it, for which `stream` does not wait.  The tensors
+    that cross from one stream to the other are known to the allocator as used on
+    both, so that their memory is not handed out while either still reads them.
+    The inputs have to be ready: `stream` waits for nothing here."""
+    import torch
+    if not args[0].is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # 0 and 1 name the legacy default stream, which torch's default stream is
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = helper(*args)
+    if stream.cuda_stream != caller.cuda_stream:
+        for t in args:
+            if hasattr(t, "record_stream"):
+                t.record_stream(stream)
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+    return out
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -343,22 +372,26 @@ def _rows(x):
 
 def softmax_fwd(x, out=None, stream=None):
     """Row-wise softmax over the last dimension of a CUDA tensor."""
+    if stream is not None:
+        return _on(stream, softmax_fwd, x, out)
     import torch
     M, N = _rows(x)
     y = torch.empty_like(x) if out is None else out
-    qk_softmax_fwd(x, y, M, N, _dtype_code(x), stream)
+    qk_softmax_fwd(x, y, M, N, _dtype_code(x))
     return y
 
 
 def rmsnorm_fwd(x, w, eps: float = 1e-6, out=None, want_rstd: bool = True, stream=None):
     """RMSNorm over the last dimension; returns (y, rstd) (rstd is None if not wanted)."""
+    if stream is not None:
+        return _on(stream, rmsnorm_fwd, x, w, eps, out, want_rstd)
     import torch
     M, N = _rows(x)
     if w.dtype != x.dtype or w.numel() != N or not w.is_contiguous():
         raise ValueError("w must be a contiguous [N] tensor of x's dtype")
     y = torch.empty_like(x) if out is None else out
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
-    qk_rmsnorm_fwd(x, w, y, rstd, M, N, eps, _dtype_code(x), stream)
+    qk_rmsnorm_fwd(x, w, y, rstd, M, N, eps, _dtype_code(x))
     return y, rstd
 
 
@@ -366,6 +399,8 @@ def layernorm_fwd(x, w, b=None, eps: float = 1e-5, out=None, want_stats: bool = 
                   stream=None):
     """LayerNorm over the last dimension; returns (y, mean, rstd) (the two
     statistics are None if not wanted).  b may be None (no bias)."""
+    if stream is not None:
+        return _on(stream, layernorm_fwd, x, w, b, eps, out, want_stats)
     import torch
     M, N = _rows(x)
     for name, t in (("w", w), ("b", b)):
@@ -376,7 +411,7 @@ def layernorm_fwd(x, w, b=None, eps: float = 1e-5, out=None, want_stats: bool = 
     if want_stats:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    qk_layernorm_fwd(x, w, b, y, mean, rstd, M, N, eps, _dtype_code(x), stream)
+    qk_layernorm_fwd(x, w, b, y, mean, rstd, M, N, eps, _dtype_code(x))
     return y, mean, rstd
 
 
@@ -384,6 +419,8 @@ def xent_fwd(logits, targets, want_lse: bool = True, ignore_index=None, z_loss: 
              want_mean: bool = False, stream=None):
     """Per-row cross-entropy; returns (loss, lse) (lse is None if not wanted),
     or (loss, lse, mean) with want_mean."""
+    if stream is not None:
+        return _on(stream, xent_fwd, logits, targets, want_lse, ignore_index, z_loss, want_mean)
     import torch
     M, N = _rows(logits)
     if targets.dtype != torch.int64 or targets.numel() != M or not targets.is_contiguous():
@@ -391,26 +428,29 @@ def xent_fwd(logits, targets, want_lse: bool = True, ignore_index=None, z_loss: 
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
     lse = torch.empty_like(loss) if want_lse else None
     if ignore_index is None and not z_loss and not want_mean:
-        qk_xent_fwd(logits, targets, loss, lse, M, N, _dtype_code(logits), stream)
+        qk_xent_fwd(logits, targets, loss, lse, M, N, _dtype_code(logits))
         return loss, lse
     mean = torch.empty((), dtype=torch.float32, device=logits.device) if want_mean else None
-    qk_xent_fwd_ex(logits, targets, loss, lse, mean, M, N, _dtype_code(logits), ignore_index, z_loss,
-                   stream)
+    qk_xent_fwd_ex(logits, targets, loss, lse, mean, M, N, _dtype_code(logits), ignore_index, z_loss)
     return (loss, lse, mean) if want_mean else (loss, lse)
 
 
 def softmax_bwd(y, dy, out=None, stream=None):
     """Softmax backward over the last dimension: y * (dy - sum(dy * y))."""
+    if stream is not None:
+        return _on(stream, softmax_bwd, y, dy, out)
     import torch
     M, N = _rows(y)
     dx = torch.empty_like(y) if out is None else out
-    qk_softmax_bwd(y, dy, dx, M, N, _dtype_code(y), stream)
+    qk_softmax_bwd(y, dy, dx, M, N, _dtype_code(y))
     return dx
 
 
 def rmsnorm_bwd(x, w, rstd, dy, stream=None):
     """RMSNorm backward; returns (dx, dw) with dw in float32.  Allocates the
     workspace with PyTorch (the library itself allocates nothing)."""
+    if stream is not None:
+        return _on(stream, rmsnorm_bwd, x, w, rstd, dy)
     import torch
     M, N = _rows(x)
     code = _dtype_code(x)
@@ -418,17 +458,18 @@ def rmsnorm_bwd(x, w, rstd, dy, stream=None):
     ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=x.device)
     dx = torch.empty_like(x)
     dw = torch.empty(N, dtype=torch.float32, device=x.device)
-    qk_rmsnorm_bwd(x, w, rstd, dy, dx, dw, ws, ws_bytes, M, N, code, stream)
+    qk_rmsnorm_bwd(x, w, rstd, dy, dx, dw, ws, ws_bytes, M, N, code)
     return dx, dw
 
 
 def xent_bwd(logits, targets, lse, dloss=None, ignore_index=None, z_loss: float = 0.0, stream=None):
     """Cross-entropy backward: dloss * ((1 + 2 z lse) softmax(logits) - onehot(targets))."""
+    if stream is not None:
+        return _on(stream, xent_bwd, logits, targets, lse, dloss, ignore_index, z_loss)
     import torch
     M, N = _rows(logits)
     dx = torch.empty_like(logits)
-    qk_xent_bwd_ex(logits, targets, lse, dloss, dx, M, N, _dtype_code(logits), ignore_index, z_loss,
-                   stream)
+    qk_xent_bwd_ex(logits, targets, lse, dloss, dx, M, N, _dtype_code(logits), ignore_index, z_loss)
     return dx
 
 
@@ -471,23 +512,9 @@ def _same(name, t, shape, dtype, dev):
     return t
 
 
-def _stream_on(stream, dev):
-    """The stream handle of a call on device dev (None: torch's current stream)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev) or None
-    return _stream(stream)
-
-
-def _used_on(stream, *tensors):
-    """Tells torch's allocator that a call on `stream` uses tensors that were
-    allocated on the current one, so that their memory is not handed out again
-    before the kernels are done."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _current_stream(dev):
+    """The handle of torch's current stream on device dev."""
+    return torch._C._cuda_getCurrentRawStream(dev) or None
 
 
 @functools.lru_cache(maxsize=512)
@@ -501,6 +528,8 @@ def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, wan
     """h = x + residual and its RMSNorm over the last dimension; returns
     (y, h, rstd) (rstd is None if not wanted).  out and out_h may be x or
     residual (out_h=residual keeps the residual stream in place)."""
+    if stream is not None:
+        return _on(stream, add_rmsnorm_fwd, x, residual, w, eps, out, out_h, want_rstd)
     M, N, code, dev = _matrix(x)
     shape, dtype = x.shape, x.dtype
     _same("residual", residual, shape, dtype, dev)
@@ -510,9 +539,7 @@ def add_rmsnorm_fwd(x, residual, w, eps: float = 1e-6, out=None, out_h=None, wan
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
     _check(load_library().qk_add_rmsnorm_fwd(
         x.data_ptr(), residual.data_ptr(), w.data_ptr(), y.data_ptr(), h.data_ptr(),
-        rstd.data_ptr() if want_rstd else None, M, N, eps, code, _stream_on(stream, dev)), "qk_add_rmsnorm_fwd")
-    if stream is not None:
-        _used_on(stream, y, h, rstd)
+        rstd.data_ptr() if want_rstd else None, M, N, eps, code, _current_stream(dev)), "qk_add_rmsnorm_fwd")
     return y, h, rstd
 
 
@@ -520,6 +547,8 @@ def add_rmsnorm_bwd(h, w, rstd, dy, dh=None, out=None, stream=None):
     """Backward of add_rmsnorm_fwd; returns (dx, dw): dx is the gradient of x
     and of residual alike, dw is float32.  dh is the gradient that reaches h by
     the residual stream (None: none).  out may be h, dy or dh."""
+    if stream is not None:
+        return _on(stream, add_rmsnorm_bwd, h, w, rstd, dy, dh, out)
     M, N, code, dev = _matrix(h)
     shape, dtype = h.shape, h.dtype
     _same("w", w, (N,), dtype, dev)
@@ -533,10 +562,8 @@ def add_rmsnorm_bwd(h, w, rstd, dy, dh=None, out=None, stream=None):
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
     _check(load_library().qk_add_rmsnorm_bwd(
         h.data_ptr(), w.data_ptr(), rstd.data_ptr(), dy.data_ptr(), None if dh is None else dh.data_ptr(),
-        dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, M, N, code, _stream_on(stream, dev)),
+        dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, M, N, code, _current_stream(dev)),
         "qk_add_rmsnorm_bwd")
-    if stream is not None:
-        _used_on(stream, dx, dw, ws)
     return dx, dw
 
 
@@ -547,6 +574,8 @@ def rmsnorm_quant_fwd(x, w, residual=None, eps: float = 1e-6, group: int = 0, qd
     (torch.float8_e4m3fn by default, or torch.int8) that stands for
     q * scale; scale has one float32 a row (group 0) or one for each group of
     32, 64 or 128 columns.  h is None without a residual or if not wanted."""
+    if stream is not None:
+        return _on(stream, rmsnorm_quant_fwd, x, w, residual, eps, group, qdtype, out_h, want_h, want_rstd)
     M, N, code, dev = _matrix(x)
     shape, dtype, device = x.shape, x.dtype, x.device
     if qdtype is None or qdtype is torch.float8_e4m3fn:
@@ -573,9 +602,7 @@ def rmsnorm_quant_fwd(x, w, residual=None, eps: float = 1e-6, group: int = 0, qd
     _check(load_library().qk_rmsnorm_quant_fwd(
         x.data_ptr(), None if residual is None else residual.data_ptr(), w.data_ptr(), q.data_ptr(),
         scale.data_ptr(), None if h is None else h.data_ptr(), rstd.data_ptr() if want_rstd else None, M, N, eps,
-        group, code, qcode, _stream_on(stream, dev)), "qk_rmsnorm_quant_fwd")
-    if stream is not None:
-        _used_on(stream, q, scale, h, rstd)
+        group, code, qcode, _current_stream(dev)), "qk_rmsnorm_quant_fwd")
     return q, scale, h, rstd
 
 
@@ -594,6 +621,8 @@ def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_l
     """Per-row cross-entropy of the logits h @ w.T, which are never stored;
     returns (loss, lse) (lse is None if not wanted), or (loss, lse, mean) with
     want_mean.  Options as in xent_fwd."""
+    if stream is not None:
+        return _on(stream, linear_xent_fwd, h, w, targets, want_lse, ignore_index, z_loss, want_mean)
     M, V, K, code, dev = _linear_xent_sizes(h, w, targets)
     loss = torch.empty(h.shape[:-1], dtype=torch.float32, device=h.device)
     lse = torch.empty_like(loss) if want_lse else None
@@ -603,9 +632,7 @@ def linear_xent_fwd(h, w, targets, want_lse: bool = True, ignore_index=None, z_l
     _check(load_library().qk_linear_xent_fwd(
         h.data_ptr(), w.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr() if want_lse else None,
         mean.data_ptr() if want_mean else None, ws.data_ptr(), nbytes, M, V, K, code, _options(ignore_index, z_loss),
-        _stream_on(stream, dev)), "qk_linear_xent_fwd")
-    if stream is not None:
-        _used_on(stream, loss, lse, mean, ws)
+        _current_stream(dev)), "qk_linear_xent_fwd")
     return (loss, lse, mean) if want_mean else (loss, lse)
 
 
@@ -613,6 +640,8 @@ def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: f
                     want_dh: bool = True, want_dw: bool = True, stream=None):
     """Backward of linear_xent_fwd; returns (dh, dw) (None if not wanted).
     dloss is the float32 gradient of each row's loss (None: 1)."""
+    if stream is not None:
+        return _on(stream, linear_xent_bwd, h, w, targets, lse, dloss, ignore_index, z_loss, want_dh, want_dw)
     M, V, K, code, dev = _linear_xent_sizes(h, w, targets)
     _same("lse", lse, h.shape[:-1], torch.float32, dev)
     if dloss is not None:
@@ -624,7 +653,5 @@ def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: f
     _check(load_library().qk_linear_xent_bwd(
         h.data_ptr(), w.data_ptr(), targets.data_ptr(), lse.data_ptr(), None if dloss is None else dloss.data_ptr(),
         dh.data_ptr() if want_dh else None, dw.data_ptr() if want_dw else None, ws.data_ptr(), nbytes, M, V, K, code,
-        _options(ignore_index, z_loss), _stream_on(stream, dev)), "qk_linear_xent_bwd")
-    if stream is not None:
-        _used_on(stream, dh, dw, ws)
+        _options(ignore_index, z_loss), _current_stream(dev)), "qk_linear_xent_bwd")
     return dh, dw
