@@ -415,6 +415,34 @@ def test_backward_long_rows_and_many_rows(cuda, dtype, M, N):
 
 
 @gpu
+@pytest.mark.parametrize("N,off", [(64, 0), (1003, 0), (4096, 0), (2048, 1), (9001, 0)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_of_rows_of_any_size(cuda, dtype, N, off):
+    """Rows around 1e-17 to 1e16 with eps = 0: rstd^3 is beyond float32 at either
+    end, the gradient is not.  dh is of the size of the rest of dx, 1 / the row."""
+    code, td = DT[dtype]
+    size = torch.tensor([1e-17, 1e-14, 1e-13, 1e-12, 1e-7, 1.0, 1e7, 1e12, 1e14, 1e15, 1e16], dtype=torch.float64)
+    M = len(size)
+    h = (rows(M, N, dtype, N, 3.0).double() * size[:, None]).to(td)
+    w, dy = syn.uniform_weight(N, dtype, N + 1, "cpu"), rows(M, N, dtype, N + 2)
+    dh = (rows(M, N, dtype, N + 3).double() / size[:, None]).to(td)
+    _, _, rstd = qb.add_rmsnorm_fwd(h.to(DEV), torch.zeros_like(h).to(DEV), w.to(DEV), eps=0.0)
+    check_scalars(to_f64(rstd), 1.0 / np.sqrt((to_f64(h) ** 2).mean(1)), "rstd")
+    dx_ref, sx, dw_ref, sw = backward64(h, w, rstd.cpu(), dy, dh)
+    dx, cx = guarded((M, N), td, off)
+    dw, cw = guarded((N,), torch.float32)
+    n = qb.qk_add_rmsnorm_bwd_workspace_size(M, N, code)
+    ws, cs = guarded((n,), torch.uint8)
+    qb.qk_add_rmsnorm_bwd(shifted(h, off), shifted(w, off), rstd, shifted(dy, off), shifted(dh, off), dx, dw, ws, n, M, N,
+                          code)
+    torch.cuda.synchronize()
+    cx("dx"), cw("dw"), cs("workspace")
+    for i in range(M):  # each row by itself: their sizes are up to 33 decades apart
+        check_scaled(to_f64(dx[i]), dx_ref[i], sx[i], dtype, f"dx of a row of {size[i]:g}")
+    check_scaled(to_f64(dw), dw_ref, sw, "f32", "dw")
+
+
+@gpu
 def test_backward_against_differences(cuda):
     """The kernel's gradient against central differences of the 64-bit forward:
     sum(y * dy) + sum(h * dh) moved along random directions (their own error is
