@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kFewLogitThreads, 1) few_logits_kernel(const F
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.K, KC = a.chunk;
-  auto stage = [&](int k0) {  // h's columns [k0, k0 + KC)
+  auto stage = [&](int64_t k0) {  // h's columns [k0, k0 + KC)
     for (int m = warp; m < MT; m += NW)
       for (int j = lane; j < KC; j += 32)
         hs[m * KC + j] = m < a.M && k0 + j < K ? Vec16<T>::load1(static_cast<const T*>(a.h) + int64_t(m) * K + k0 + j) : 0.f;
@@ -104,14 +104,14 @@ __global__ void __launch_bounds__(kFewLogitThreads, 1) few_logits_kernel(const F
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
     constexpr int kUnroll = KV == 4 ? 1 : 4;  // loads of w in flight: R kUnroll
-    for (int kc = 0; kc < K; kc += KC) {
+    for (int64_t kc = 0; kc < K; kc += KC, w += KC) {  // k counts from kc: a sum of ints near 2^31 would not fit
       if (KC < K) {
         __syncthreads();
         stage(kc);
         __syncthreads();
       }
-      const int end = min(K, kc + KC);
-      for (int k0 = kc + lane * KV; k0 < end; k0 += 32 * KV * kUnroll) {
+      const int end = int(min(int64_t(KC), K - kc));
+      for (int k0 = lane * KV; k0 < end; k0 += 32 * KV * kUnroll) {
         float wv[kUnroll][R][KV];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(kFewLogitThreads, 1) few_logits_kernel(const F
           for (int m = 0; m < MT; ++m) {
             float hv[KV];
             if constexpr (KV == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(hs + m * KC + (k - kc));
+              const float4 x = *reinterpret_cast<const float4*>(hs + m * KC + k);
               hv[0] = x.x, hv[1] = x.y, hv[2] = x.z, hv[3] = x.w;
             } else {
-              hv[0] = hs[m * KC + (k - kc)];
+              hv[0] = hs[m * KC + k];
             }
 #pragma unroll
             for (int r = 0; r < R; ++r)

@@ -213,6 +213,14 @@ def test_weights_beyond_32_bit_offsets(cuda):
 
 
 @gpu
+@pytest.mark.parametrize("M,V,K", [(3, 21, 2 ** 18 + 4), (3, 21, 2 ** 18 + 5), (1, 2, 2 ** 19), (20, 9, 60001)])
+def test_rows_of_many_chunks(cuda, M, V, K):
+    """Few float32 tokens whose h is walked in tens of pieces of shared memory."""
+    c = make(M, V, K, "f32", 80, ignored=0)
+    check(c, run(c), what=f"{M}x{V}x{K} f32")
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_targets(cuda, dtype):
     """Out of range, the extremes, the first and last column, the same column
