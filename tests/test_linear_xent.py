@@ -220,6 +220,88 @@ def test_rows_of_many_chunks(cuda, M, V, K):
     check(c, run(c), what=f"{M}x{V}x{K} f32")
 
 
+# --- float32 by three bf16 planes: what each pair of planes gives ---
+# An output's error in norm, relative to the output, is below 1e-6:
+#   * what the six plane pairs leave out, and float32's rounding of g, lse, loss
+#     and the outputs: below 3e-7 (the first test below forms just that; the most
+#     is the target's logit as lse - loss: two roundings of numbers from 8 to 16,
+#     2^-20 / sqrt(12) each, to logits of size 2 are 2e-7, for 40 rows 3e-7);
+#   * the tensor core cuts an addition's tail off, 2^-25.5 of the sum each.  Of a
+#     chain's 48 additions 28 are made at the sum's full size (20 of the first 24
+#     hold the small pairs, 2^-8 of it or less): 28 2^-25.5 = 5.9e-7.
+# A pair that is missing in one of the three products shows as 1.2e-6 or more.
+PLANE_PAIRS = [(0, 0), (0, 1), (1, 0), (1, 1), (0, 2), (2, 0)]
+BOUND = 1e-6
+
+
+def by_planes(a, b, pairs):
+    """a b^T in float64 over the given pairs of bf16 planes."""
+    def planes(x):
+        out, rest = [], x.double()
+        for _ in range(3):
+            out.append(rest.float().bfloat16().double())
+            rest = rest - out[-1]
+        return out
+    pa, pb = planes(a), planes(b)
+    return sum(pa[i] @ pb[j].T for i, j in pairs)
+
+
+def exact_step(c):
+    """The targets' logits, lse, dh and dw in float64 (no row ignored, z = 0)."""
+    h, w, t, d = c["h"].double(), c["w"].double(), c["t"], c["dloss"].double()
+    logits = h @ w.T
+    lse = torch.logsumexp(logits, 1)
+    at = logits.gather(1, t[:, None])[:, 0]
+    g = torch.exp(logits - lse[:, None])
+    g[torch.arange(len(t), device=t.device), t] -= 1
+    g *= d[:, None]
+    return at, lse, g @ w, g.T @ h
+
+
+def norm_errors(loss, lse, dh, dw, want):
+    got = (lse.double() - loss.double(), lse.double(), dh.double(), dw.double())
+    return {k: ((a - b).norm() / b.norm()).item() for k, a, b in zip(("target logits", "lse", "dh", "dw"), got, want)}
+
+
+@pytest.mark.parametrize("M,V,K", [(48, 70, 64), (40, 300, 96), (130, 515, 513), (40, 5003, 72)])
+def test_the_bound_sees_each_plane_pair(M, V, K):
+    gen = torch.Generator().manual_seed(M + V)
+    c = {"h": syn.normal_rows(M, K, "f32", 1, "cpu"), "w": syn.normal_rows(V, K, "f32", 2, "cpu", sigma=2 / K ** 0.5),
+         "t": torch.randint(0, V, (M,), generator=gen), "dloss": syn.uniform_weight(M, "f32", 3, "cpu", lo=0.25, hi=2.0)}
+    want = exact_step(c)
+
+    def errors(logits=PLANE_PAIRS, dh=PLANE_PAIRS, dw=PLANE_PAIRS):
+        x = by_planes(c["h"], c["w"], logits)
+        lse = torch.logsumexp(x, 1)
+        scale = c["dloss"].max()
+        g = torch.exp(x - lse[:, None])
+        g[torch.arange(M), c["t"]] -= 1
+        g = (g * (c["dloss"] / scale).double()[:, None]).float()
+        loss = (lse - x.gather(1, c["t"][:, None])[:, 0]).float()
+        return norm_errors(loss, lse.float(), (by_planes(g, c["w"].T, dh) * scale).float(),
+                           (by_planes(g.T, c["h"].T, dw) * scale).float(), want)
+
+    assert max(errors().values()) < 3e-7
+    for pair in PLANE_PAIRS:
+        less = [p for p in PLANE_PAIRS if p != pair]
+        assert errors(logits=less)["target logits"] > 1.2 * BOUND, pair
+        assert errors(dh=less)["dh"] > 1.2 * BOUND, pair
+        assert errors(dw=less)["dw"] > 1.2 * BOUND, pair
+
+
+@gpu
+@pytest.mark.parametrize("M,V,K,off", [(48, 70, 64, 0), (64, 64, 64, 1), (40, 300, 96, 0), (130, 515, 513, 0),
+                                       (257, 700, 192, 0), (40, 5003, 72, 1), (2050, 3000, 65, 0), (300, 1031, 2056, 0),
+                                       (40, 90000, 513, 0), (3000, 40000, 130, 0)])
+def test_float32_products_use_all_planes(cuda, M, V, K, off):
+    """More than 32 tokens: narrow and full column tiles, aligned and unaligned
+    rows, one chain and many, one piece of the vocabulary and several."""
+    c = make(M, V, K, "f32", 90 + M, ignored=0)
+    out = run(c, off=off)
+    errors = norm_errors(out["loss"], out["lse"], out["dh"], out["dw"], exact_step(c))
+    assert max(errors.values()) < BOUND, errors
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_targets(cuda, dtype):
