@@ -459,6 +459,36 @@ def test_the_end_of_a_model(cuda, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_gradient_that_leaves_the_end_of_a_model(cuda, dtype, residual):
+    """dx of the same path in norm, the norm's part alone and beside a residual
+    gradient of its size.  Three stages each round what they pass on (dy, g and
+    the output: half steps of 2^-8 for bf16, independent), so the whole is off by
+    3 half steps in norm at most, float32 by its sums' 3e-5 as above."""
+    M, N, V = 150, 192, 1100
+    x, r = syn.normal_rows(M, N, dtype, 1, DEV), syn.normal_rows(M, N, dtype, 2, DEV, sigma=3.0)
+    g = syn.uniform_weight(N, dtype, 3, DEV)
+    c = make(M, V, N, dtype, 4)
+    y, h, rstd = qb.add_rmsnorm_fwd(x, r, g)
+    lse = qb.linear_xent_fwd(y, c["w"], c["t"], ignore_index=IGNORE)[1]
+    dy, dw = qb.linear_xent_bwd(y, c["w"], c["t"], lse, c["dloss"], ignore_index=IGNORE)
+    h64, g64, w64 = (t.double().requires_grad_() for t in (h, g, c["w"]))
+    y64 = h64 * (h64.square().mean(1, keepdim=True) + 1e-6).rsqrt() * g64
+    each = torch.nn.functional.cross_entropy(y64 @ w64.T, c["t"], ignore_index=IGNORE, reduction="none")
+    gh, gg, gw = torch.autograd.grad(each, (h64, g64, w64), c["dloss"].double())
+    up = None
+    if residual:
+        up = syn.normal_rows(M, N, dtype, 5, DEV, sigma=gh.std().item())
+    dx, dg = qb.add_rmsnorm_bwd(h, g, rstd, dy, up)
+    step = 3 * 2 ** -8 if dtype == "bf16" else 3e-5
+    want = gh if up is None else gh + up.double()
+    assert (want - (0 if up is None else up.double())).norm() > 0.5 * want.norm()  # the norm's part weighs
+    for got, ref in ((dx, want), (dg, gg), (dw, gw)):
+        assert (got.double() - ref).norm() <= step * ref.norm()
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_another_stream_and_a_captured_graph(cuda, dtype):
     c = make(200, 1500, 128, dtype, 21)
