@@ -385,6 +385,83 @@ def test_one_of_the_gradients(cuda, dtype):
     assert torch.equal(run(c, dh=False)["dw"], both["dw"])
 
 
+# Tokens of the float32 kernels for few tokens (4, 8, 16 and 32 in registers),
+# with rows of vectors and of elements; bf16 beside them.
+FEW = [(1, 64), (4, 65), (7, 136), (8, 30), (11, 64), (16, 65), (20, 136), (32, 65)]
+
+
+@gpu
+@pytest.mark.parametrize("M,K", FEW)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_of_the_gradients_of_few_tokens(cuda, dtype, M, K):
+    c = make(M, 700, K, dtype, 6)
+    for off in (0, 1):
+        both = run(c, 1e-3, off=off)
+        assert torch.equal(run(c, 1e-3, off=off, dw=False)["dh"], both["dh"])
+        assert torch.equal(run(c, 1e-3, off=off, dh=False)["dw"], both["dw"])
+        neither = run(c, 1e-3, off=off, dh=False, dw=False)
+        assert torch.equal(neither["loss"], both["loss"])
+
+
+@gpu
+@pytest.mark.parametrize("K", [48, 49])
+@pytest.mark.parametrize("M", [3, 8, 16, 17, 32])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_targets_of_few_tokens(cuda, dtype, M, K):
+    """Out of range at either end, ignored, the first and the last column; all ignored; a single column."""
+    V = 515
+    c = make(M, V, K, dtype, 5, ignored=0)
+    for edges in ([0, V - 1, V], [-1, IGNORE, 255], [-(2 ** 63), 2 ** 63 - 1, 1]):
+        c["t"][:3] = torch.tensor(edges)
+        out = run(c, 1e-3)
+        check(c, out, 1e-3, what=f"{edges}")
+        for i, t in enumerate(edges):
+            bad = t != IGNORE and not 0 <= t < V
+            assert bool(out["dh"][i].isnan().all()) == bad and bool(out["loss"][i].isnan()) == bad
+    check(c, run(c, ignore=None), ignore=None, what="no ignore index")
+    c["t"][:] = 3
+    check(c, run(c), what="one column")
+    check(c, run(c, ignore=3), ignore=3, what="every row ignored by a column")
+    c["t"][:] = IGNORE
+    out = run(c)
+    assert (out["loss"] == 0).all() and out["mean"].isnan().all()
+    assert (out["dh"] == 0).all() and (out["dw"] == 0).all()
+    c = make(M, 1, K, dtype, 5, ignored=0)
+    check(c, run(c), what="a vocabulary of one")
+
+
+@gpu
+@pytest.mark.parametrize("M,K", [(3, 72), (8, 73), (16, 72), (30, 73)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_values_that_are_not_finite(cuda, dtype, M, K):
+    """A NaN or infinity in a row of h or of w, and NaN in an ignored row's dloss and lse."""
+    V = 520
+    c = make(M, V, K, dtype, 4, ignored=0)
+    want = run(c)
+    keep = {k: v.clone() for k, v in c.items()}
+    c["h"][1, 3] = float("nan")
+    c["h"][2, K - 1] = float("inf")
+    out = run(c)
+    bad = torch.zeros(M, dtype=torch.bool)
+    bad[1:3] = True
+    for k in ("loss", "lse"):
+        assert not torch.isfinite(out[k][bad]).any() and torch.equal(out[k][~bad], want[k][~bad])
+    assert out["dh"][1].isnan().all() and torch.equal(out["dh"][~bad], want["dh"][~bad])
+    assert out["dw"].isnan().all() and out["mean"].isnan().all()
+    c["h"].copy_(keep["h"])
+    c["w"][V - 1, 0] = float("nan")  # every token's logit of that row
+    out = run(c)
+    assert out["lse"].isnan().all() and out["loss"].isnan().all() and out["dh"].isnan().all()
+    c["w"].copy_(keep["w"])
+    c["t"][0] = IGNORE
+    want = run(c)
+    c["dloss"][0] = float("nan")
+    lse = want["lse"].clone()
+    lse[0] = float("nan")
+    dh, dw = qb.linear_xent_bwd(c["h"], c["w"], c["t"], lse, c["dloss"], ignore_index=IGNORE)
+    assert torch.equal(dh, want["dh"]) and torch.equal(dw, want["dw"]) and (dh[0] == 0).all()
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_the_same_bits_every_time(cuda, dtype):
