@@ -496,6 +496,38 @@ def test_rows_beyond_32_bit_offsets(cuda):
 
 
 @gpu
+@pytest.mark.parametrize("N,off", [(64, 0), (100, 1), (1003, 0), (4096, 0), (9001, 0), (40000, 0)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_row_of_zeros_without_eps(cuda, dtype, N, off):
+    """eps = 0: rstd is infinite and the row NaN, as 1 / sqrt(0) and 0 / 0 are;
+    the other rows and the dw of a gradient without that row are as always."""
+    x, r = rows(5, N, dtype, 1), rows(5, N, dtype, 2)
+    x[2], r[2] = 0, 0
+    w = syn.uniform_weight(N, dtype, 3, "cpu")
+    xs, rs, ws = (shifted(t, off) for t in (x, r, w))
+    y, h, rstd = qb.add_rmsnorm_fwd(xs, rs, ws, eps=0.0)
+    with np.errstate(all="ignore"):
+        f = to_f64(h.cpu())
+        ref_rstd = 1.0 / np.sqrt((f * f).mean(1))
+        ref = f * ref_rstd[:, None] * to_f64(w)[None, :]
+    assert torch.equal(h.cpu(), (x.float() + r.float()).to(x.dtype)) and rstd[2].item() == float("inf")
+    keep = [0, 1, 3, 4]
+    check_scalars(to_f64(rstd)[keep], ref_rstd[keep], "rstd")
+    assert y[2].isnan().all()
+    check_rows(to_f64(y)[keep], ref[keep], dtype, False, "y")
+    for group in (0, 32):
+        for qdtype in (torch.float8_e4m3fn, torch.int8):
+            q, scale, _, _ = qb.rmsnorm_quant_fwd(xs, ws, residual=rs, eps=0.0, group=group, qdtype=qdtype)
+            assert scale[2].isnan().all() and torch.isfinite(scale[keep]).all()
+            check_quant(q[keep], scale[keep], ref[keep], group, "int8" if qdtype is torch.int8 else "e4m3", "quant")
+    dy, dh = rows(5, N, dtype, 4), rows(5, N, dtype, 5)
+    dx, dw = qb.add_rmsnorm_bwd(h, ws, rstd, shifted(dy, off), shifted(dh, off))
+    assert dx[2].isnan().all() and dw.isnan().all()
+    dx_ref, sx, _, _ = backward64(h.cpu()[keep], w, rstd.cpu()[keep], dy[keep], dh[keep])
+    check_scaled(to_f64(dx)[keep], dx_ref, sx, dtype, "dx")
+
+
+@gpu
 def test_zero_rows(cuda):
     w = torch.ones(64, device=DEV)
     e = torch.empty(0, 64, device=DEV)
