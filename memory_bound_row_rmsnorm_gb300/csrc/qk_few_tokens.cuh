@@ -68,9 +68,11 @@ __global__ void __launch_bounds__(kFewLogitThreads, 1) few_logits_kernel(const F
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.K, KC = a.chunk;
   auto stage = [&](int64_t k0) {  // h's columns [k0, k0 + KC)
-    for (int m = warp; m < MT; m += NW)
-      for (int j = lane; j < KC; j += 32)
-        hs[m * KC + j] = m < a.M && k0 + j < K ? Vec16<T>::load1(static_cast<const T*>(a.h) + int64_t(m) * K + k0 + j) : 0.f;
+    const int left = int(min(int64_t(KC), K - k0));
+    for (int m = warp; m < MT; m += NW) {
+      const T* src = static_cast<const T*>(a.h) + int64_t(m) * K + k0;
+      for (int j = lane; j < KC; j += 32) hs[m * KC + j] = m < a.M && j < left ? Vec16<T>::load1(src + j) : 0.f;
+    }
   };
   if (KC >= K) stage(0);
   __syncthreads();
