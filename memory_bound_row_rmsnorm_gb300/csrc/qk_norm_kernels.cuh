@@ -3,7 +3,7 @@
 //
 //   h = rnd(x + r),  rstd = (mean h^2 + eps)^-1/2,  y = h rstd w
 //   q = rne(y / scale), scale = max(max |y|, 2^-100) / qmax per row or group of columns
-//   dx = dh + rstd (dy w - u mean(dy w u)),  dw = sum over rows of dy u,  u = h rstd
+//   dx = dh + rstd dy w - h rstd^3 mean(dy w h),  dw = sum over rows of dy h rstd
 //
 // All three are bound by memory: a handful of operations for the 2 to 4
 // matrices that pass through.
@@ -179,14 +179,13 @@ __global__ void __launch_bounds__(kNormAnyThreads) norm_any_kernel(const NormArg
       const float rs = a.rstd[row];
       float dot = 0.f;
       for (int64_t j = tid; j < N; j += TH) dot = fmaf(V::load1(r + j) * V::load1(w + j), V::load1(x + j), dot);
-      const float c = (cta_sum<TH>(dot, red[0]) * a.inv_n) * rs;  // rstd^3 alone may leave float32's range
+      const float c = (cta_sum<TH>(dot, red[0]) * a.inv_n) * rs * rs * rs;  // in this order, as in the ring kernel
       const bool first = row == blockIdx.x;
       for (int64_t j = tid; j < N; j += TH) {
         const float hv = V::load1(x + j), dy = V::load1(r + j);
         const float up = dh != nullptr ? V::load1(dh + j) : 0.f;
-        const float u = hv * rs;
-        V::store1(dx + j, fmaf(fmaf(u, -c, dy * V::load1(w + j)), rs, up));
-        const float p = dy * u;  // this thread's columns are its own in every row
+        V::store1(dx + j, up + fmaf(hv, -c, (rs * dy) * V::load1(w + j)));
+        const float p = (dy * hv) * rs;  // this thread's columns are its own in every row
         part[j] = first ? p : part[j] + p;
       }
     } else {

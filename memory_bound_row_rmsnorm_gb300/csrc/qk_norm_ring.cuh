@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
 
     if constexpr (OP == kAddNormBwd) {
       if (!row_ok) continue;
-      const float c = (acc * a.inv_n) * rs;  // mean(dy w h rstd): rstd^3 alone may leave float32's range
+      const float c = (acc * a.inv_n) * rs * rs * rs;  // in this order: rstd^3 alone may leave float32's range
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int u = l + k * TPR;
@@ -208,9 +208,8 @@ __global__ void __launch_bounds__(THREADS) norm_ring_kernel(const NormArgs a) {
         U::unpack(wv[k], fw);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float u = fh[e] * rs;
-          o[e] = fmaf(fmaf(u, -c, fd[e] * fw[e]), rs, fu[e]);
-          dw[k * E + e] = fmaf(fd[e], u, dw[k * E + e]);
+          o[e] = fu[e] + fmaf(fh[e], -c, (rs * fd[e]) * fw[e]);
+          dw[k * E + e] += (fd[e] * fh[e]) * rs;
         }
         U::store(a.y, base + u, U::pack(o));
       }
