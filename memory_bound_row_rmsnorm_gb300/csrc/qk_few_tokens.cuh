@@ -1,13 +1,17 @@
 // qk_few_tokens.cuh -- the float32 linear cross-entropy of up to 32 tokens on the
 // fp32 units (sm_103a).
 //
-// What bounds it is reading w once (and writing dw): the bf16 planes that the
-// products of qk_product_kernel.cuh want move 12 bytes more for each 4-byte
-// weight and pass, while at 16 tokens a weight costs 16 multiplications, which
-// the SMs keep up with at about the memory's rate.  80000 x 464, by planes and so:
-// forward of 4 to 32 tokens 148 us, and 35 (4 tokens), 66 (16) or 106 (32);
-// backward 287 us, and 102, 190 or 310.  (bf16 rows that have to be copied are
-// faster by the products from 4 tokens on: one copy, and a quarter of the bytes.)
+// The bf16 planes that the products of qk_product_kernel.cuh want move 12 bytes
+// more for each 4-byte weight and pass; here w is read once (and dw written).
+// 80000 x 464, by planes and so: forward of 4 to 32 tokens 142 to 156 us, and 32
+// (4 tokens), 55 (16) or 104 (32), where w's bytes take 22; backward 272 to 279,
+// and 99, 181 or 309 (where they take 67, read twice and written).
+// What bounds it: w's bytes at 4 tokens.  At 16 and 32 tokens not yet the
+// multiplications, which run at 22 TFLOP/s, a quarter to a third of the fp32
+// units' rate: at 32 a 16-byte read of h from shared memory feeds only 8 of them
+// (R = 2 rows), at 16 no load of w is under way while one is multiplied.
+// (bf16 rows that have to be copied are faster by the products from 4 tokens on:
+// one copy, and a quarter of the bytes.)
 #pragma once
 
 #include "qk_product_kernel.cuh"  // XentRow

@@ -325,7 +325,7 @@ struct Layout {
 };
 
 // Launches are waves of kPairs tiles; a wave takes as long as its tiles have
-// steps of 64 k, about 0.27 us each at full rate.
+// steps of 64 k.
 int64_t waves(int64_t tiles) { return ceil_div(tiles, kPairs); }
 
 // Vocabulary rows of a piece, at most `most` (or 256) of them and whole tiles.
@@ -349,7 +349,12 @@ int64_t choose_piece(int64_t M, int64_t V, int64_t K, int64_t most) {
 
 // k splits of dh's product over a piece: with few tiles (few rows, or a narrow
 // model) they give every pair work, with many they even out the last wave; each
-// costs a pass of fp32 sums through memory (written, and read once more).
+// costs a pass of fp32 sums through memory (written, and read once more).  The
+// 0.27 us of a step only weigh it against those bytes: near what the tensor
+// cores' nominal rate takes.  At the rate of a measured burst it is 0.33, in a
+// long run under the power limit 0.37 (8192 x 32000 x 4096 forward: 53 waves of
+// 64 steps in 1271 us), and a float32 step's six products take some 1.8 (4096 x
+// 16384 x 1024 forward: 14 waves of 16 in 437 us, 40 of them for the planes).
 int choose_splits(int64_t M, int64_t K, int64_t steps, int products) {
   const int64_t tiles = ceil_div(M, kTileM) * ceil_div(K, kTileN);
   int best = 1;
@@ -374,8 +379,9 @@ Layout plan_layout(bool bwd, int64_t M, int64_t V, int64_t K, int dtype, bool co
   };
   // Few float32 tokens: the fp32 kernels (qk_few_tokens.cuh), while g stays within a piece.
   // The backward of 17 to 32 tokens multiplies more than it moves: by the fp32
-  // kernels 87 us at 8000 x 1024, 149 at 16000 x 1024, 540 at 30000 x 2048 and
-  // 342 at 8000 x 4096; by the products 100, 139, 453 and 289.
+  // kernels 83 us at 8000 x 1024, 147 at 16000 x 1024, 536 at 30000 x 2048 and
+  // 338 at 8000 x 4096; by the products 95, 134, 444 and 282.  (The forward: 30,
+  // 49, 226 and 124 us; by the products 47, 66, 276 and 179.)
   const int mt = M <= 4 ? 4 : M <= 8 ? 8 : M <= 16 ? 16 : 32;
   const int64_t most_few = bwd && V > (int64_t(1) << 24) / K ? 16 : 32;
   if (dtype == QK_F32 && M <= most_few && V * mt * 4 <= kPieceBytes) {

@@ -14,12 +14,14 @@
 // zero: a chain of n products of 16 k is short by about n 2^-25.5 of itself (a
 // sum over 8192 k measured 1e-5 off, where rounding to nearest gives 1e-6).  So
 // a chain ends after `chunk` steps of 64 k, and the chains of a tile are added in
-// registers, to nearest.  16 steps for bf16 (lse 3e-7 off at K = 4096), whose
+// registers, to nearest.  16 steps for bf16 (lse 2.6e-7 off at K = 4096), whose
 // outputs of consequence are bf16; 2 (48 products) for float32, whose gradients
 // are 4e-7 off, against 0.8 to 1.6e-6 of fp32 products (with 1 step 2e-7, for
 // 5 to 10 % more time).
-// Shorter chains cost time and power: with 8 steps the bf16 backward of 8192 x
-// 32000 x 4096 took 4.40 ms in a long run, with 16 4.31.
+// Shorter chains cost time and power.  8192 x 131072 x 4096 forward in a long
+// run: 16 steps 5.22 ms (lse 2.6e-7 off), 12 5.31 (1.9e-7), 8 5.41 (1.3e-7), 4
+// 5.77 (7e-8); float32 products with sums to nearest are 1e-7 off.  The bf16
+// backward of 8192 x 32000 x 4096: 4.06 ms with 16 steps, 4.21 with 8.
 //
 // An operand is stored with k innermost (K-major) or with its rows innermost
 // (MN-major): h, w and g serve as either, without a transposed copy.
@@ -30,7 +32,7 @@
 // 2^-25 of a term.  A step loads its six operand tiles once for its six plane
 // pairs, half the bytes of two tiles for each: what steps of one pair wait for is
 // the way from L2 to the SMs (0.34 to 0.38 us for 64 KB a pair of CTAs, whatever
-// they multiply).  4096 x 16384 x 1024 backward: 1436 us, 1720 TFLOP/s of bf16 products.
+// they multiply).  4096 x 16384 x 1024 backward: 1474 us, 1679 TFLOP/s of bf16 products.
 #pragma once
 
 #include "qk_internal.h"
