@@ -336,10 +336,14 @@ def _on(stream, helper, *args):
     import torch
     if not args[0].is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if not hasattr(stream, "cuda_stream"):
-        handle = int(stream)  # 0 and 1 name the legacy default stream, which torch's default stream is
-        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
-    caller = torch.cuda.current_stream()
+    dev = args[0].get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # 0 and 1 name the legacy default stream, which torch's default stream is
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle > 1 else torch.cuda.default_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the stream is of device {stream.device_index}")
+    caller = torch.cuda.current_stream(dev)
     with torch.cuda.stream(stream):
         out = helper(*args)
     if stream.cuda_stream != caller.cuda_stream:

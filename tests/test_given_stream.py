@@ -21,8 +21,8 @@ gpu = pytest.mark.gpu
 
 
 class FakeStream:
-    def __init__(self, handle):
-        self.cuda_stream = handle
+    def __init__(self, handle, device=0):
+        self.cuda_stream, self.device_index = handle, device
 
     def __eq__(self, other):
         return self.cuda_stream == other.cuda_stream
@@ -84,7 +84,7 @@ def watched(monkeypatch):
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch, "cuda", types.SimpleNamespace(
-        stream=stream, current_stream=lambda *a: now[0], default_stream=lambda *a: CALLER, is_available=lambda: True,
+        Stream=FakeStream, stream=stream, current_stream=lambda *a: now[0], default_stream=lambda *a: CALLER, is_available=lambda: True,
         is_initialized=lambda: True, ExternalStream=lambda handle, **kw: FakeStream(handle)))
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: now[0].cuda_stream, raising=False)
@@ -141,6 +141,23 @@ def test_the_current_stream_needs_no_record(watched, which):
         call(given)
         assert launched == [CALLER.cuda_stream], name
         assert all(t.stream == CALLER.cuda_stream and not t.uses for t in made + inputs), name
+
+
+@pytest.mark.parametrize("which", range(15))
+def test_a_stream_of_another_device_is_refused(watched, which):
+    """Torch would switch to that device, and the kernels run there on this one's memory."""
+    new, made, launched = watched
+    name, _, call = helper_calls(new)[which]
+    with pytest.raises(ValueError, match="device"):
+        call(FakeStream(0x7f0000002000, device=1))
+    assert not launched and not made, name
+
+
+def test_any_object_with_a_handle(watched):
+    """What names its handle cuda_stream is a stream, torch's class or not."""
+    new, made, launched = watched
+    qb.softmax_fwd(new(6, 64), stream=types.SimpleNamespace(cuda_stream=GIVEN.cuda_stream))
+    assert launched == [GIVEN.cuda_stream] and made[0].stream == GIVEN.cuda_stream
 
 
 def test_tensors_off_the_gpu_are_refused_on_a_given_stream():
