@@ -425,6 +425,118 @@ QK_API qk_status qk_linear_xent_bwd(const void* h, const void* w, const int64_t*
                                     int64_t K, qk_dtype dtype, const qk_xent_options* options,
                                     void* stream);
 
+/*
+ * A matrix in 8 bits with a scale for each 128 elements: the operands of
+ * qk_scaled_mm_fwd that no norm has made (weights, activations, gradients).
+ * (The article names no 8-bit types; q and scale are as in qk_rmsnorm_quant_fwd.)
+ * For each group, with qmax = 448 (QK_E4M3) or 127 (QK_INT8):
+ *   scale = max(max |x| of the group, 2^-100) / qmax,
+ *   q     = x / scale, rounded to nearest even (bfloat16: of the exact quotient
+ *           x qmax / max |x|, so that what lies on a tie goes to even).
+ * A group with an infinite or NaN x gets scale = NaN, and so does everything
+ * that its q stand for.
+ *
+ *   x        [M, N] dtype, read once.
+ *   q        [M, N] bytes, or NULL.  Groups are 128 columns of a row (block_rows
+ *            1) or blocks of 128 x 128 (block_rows 128); the last may be short.
+ *   scale    [M, ceil(N / 128)] or [ceil(M / 128), ceil(N / 128)] float32; NULL with q.
+ *   qt       [N, M] bytes, or NULL: x^T in 8 bits, its groups 128 rows of a
+ *            column of x (block_rows 1) or the same blocks.
+ *   scale_t  [N, ceil(M / 128)] or [ceil(N / 128), ceil(M / 128)] float32; NULL with qt.
+ *   At least one of q and qt.  No buffer overlaps another.  Any N >= 1.
+ */
+QK_API qk_status qk_quant_fwd(const void* x, void* q, float* scale, void* qt, float* scale_t, int64_t M,
+                              int64_t N, int64_t block_rows, qk_dtype dtype, qk_qtype qtype, void* stream);
+
+/*
+ * Matrix product of 8-bit values (e4m3) with a scale for each block of 128: what
+ * reads qk_rmsnorm_quant_fwd's output (group 128) and qk_quant_fwd's.
+ *   y[i,j] = sum_c a_scale[i,c] b_scale[j',c] sum_{k in block c of 128} a[i,k] b[j,k]
+ * with j' = j / 128 (b_block_rows 128: weights) or j (b_block_rows 1: both
+ * operands quantised along the summed axis, as for a weight's gradient).
+ * With `offsets` the rows of a are sorted by expert (qk_expert_sort): rows
+ * offsets[e] ... offsets[e+1] - 1 are multiplied with expert e's b.  (The
+ * article names no matrix products; this is the one behind a norm.)
+ *
+ *   a        [M, K] e4m3;  a_scale [M, ceil(K / 128)] float32.
+ *   b        [experts, N, K] e4m3;  b_scale [experts, N or ceil(N / 128), ceil(K / 128)] float32.
+ *   offsets  [experts + 1] int32 on the device, or NULL (experts is 1, all rows).
+ *            Offsets that fall, or lie outside [0, M], are read as their running
+ *            maximum within [0, M].  Rows before the first offset and behind the
+ *            last one are left as they were in y.
+ *   y        [M, N] out_dtype; overlaps no other buffer.
+ *   workspace  at least qk_scaled_mm_workspace_size() bytes, 256-byte aligned,
+ *              scratch; may be NULL when that is 0.  It is 0 when K is a multiple of
+ *              16; a and b must then be 16-byte aligned.  Otherwise a and b go
+ *              through it, in rows that start on 16 bytes.
+ *   M, N, K at most 2^31 - 16, experts at most 1024 (QK_ERR_UNSUPPORTED beyond).
+ *   A block's sum is float32, is multiplied with its scales and added to nearest
+ *   in float32.  Results do not change from run to run.  A NaN value or scale
+ *   reaches the outputs of its row (of its column) only.  Scales of 2^100 or more
+ *   may overflow where y itself would not.
+ *   The gradient for a is the product of y's gradient, quantised, with b turned
+ *   (qk_quant_fwd's qt with block_rows 128), with the same offsets.
+ */
+QK_API qk_status qk_scaled_mm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t experts, size_t* bytes);
+QK_API qk_status qk_scaled_mm_fwd(const void* a, const float* a_scale, const void* b, const float* b_scale,
+                                  const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes,
+                                  int64_t M, int64_t N, int64_t K, int64_t experts, int64_t b_block_rows,
+                                  qk_dtype out_dtype, void* stream);
+
+/*
+ * Tokens sorted by expert.  Each of T tokens has k choices; a choice outside
+ * [0, num_experts) has no row (a dropped or padded one).  The sort is stable.
+ *   offsets[e]  = number of choices of experts below e, e = 0 ... num_experts
+ *   slot[t, j]  = place of choice (t, j) among the sorted ones, -1 for none
+ *
+ *   experts  [T, k] int32 (id_bytes 4) or int64 (id_bytes 8).
+ *   offsets  [num_experts + 1] int32;  slot [T, k] int32.
+ *   workspace  at least qk_expert_sort_workspace_size() bytes, 16-byte aligned,
+ *              scratch; may be NULL when that is 0 (few choices).
+ *   T * k below 2^31 - 65536, num_experts at most 1024.  T may be 0.
+ */
+QK_API qk_status qk_expert_sort_workspace_size(int64_t T, int64_t k, int64_t num_experts, size_t* bytes);
+QK_API qk_status qk_expert_sort(const void* experts, int64_t id_bytes, int32_t* offsets, int32_t* slot,
+                                void* workspace, size_t workspace_bytes, int64_t T, int64_t k, int64_t num_experts,
+                                void* stream);
+
+/*
+ * rows[slot[t, j], :] = x[t, :] for each choice that has a slot in [0, P), and
+ * row_scale[slot[t, j], :] = scale[t, :] with it (8-bit rows).  Rows that no slot names are
+ * left as they were.  Slots that name a row twice leave one of the two, or of
+ * each a part.  The gradient for x is qk_expert_combine_fwd without weights.
+ *
+ *   x      [T, row_bytes] bytes of any type;  rows [P, row_bytes].
+ *   scale  [T, groups] float32 or NULL with groups 0;  row_scale [P, groups].
+ *   No buffer overlaps another.
+ */
+QK_API qk_status qk_expert_gather_fwd(const void* x, const float* scale, const int32_t* slot, void* rows,
+                                      float* row_scale, int64_t T, int64_t k, int64_t P, int64_t row_bytes,
+                                      int64_t groups, void* stream);
+
+/*
+ * Back to the tokens: y[t, :] = sum_j weights[t, j] rows[slot[t, j], :] over the
+ * choices that have a slot in [0, P), summed in float32 in their order (a token
+ * without any gets zeros).  weights NULL: all 1.
+ *
+ *   rows [P, N] dtype;  slot [T, k] int32;  weights [T, k] float32;  y [T, N] dtype.
+ *   y overlaps no other buffer.
+ */
+QK_API qk_status qk_expert_combine_fwd(const void* rows, const int32_t* slot, const float* weights, void* y,
+                                       int64_t T, int64_t k, int64_t P, int64_t N, qk_dtype dtype, void* stream);
+
+/*
+ * Its gradients: drows[slot[t, j], :] = weights[t, j] dy[t, :], and
+ * dweights[t, j] = sum_n dy[t, n] rows[slot[t, j], n] (0 for a choice without a slot).
+ * Rows that no slot names are left as they were; no two slots may name the same.
+ *
+ *   dy [T, N], rows and drows [P, N] dtype;  drows may be rows exactly.
+ *   dweights  [T, k] float32, or NULL when not wanted.
+ */
+QK_API qk_status qk_expert_combine_bwd(const void* dy, const void* rows, const int32_t* slot, const float* weights,
+                                       void* drows, float* dweights, int64_t T, int64_t k, int64_t P, int64_t N,
+                                       qk_dtype dtype, void* stream);
+
 /* Static English description of a status code; never NULL. */
 QK_API const char* qk_status_string(qk_status s);
 

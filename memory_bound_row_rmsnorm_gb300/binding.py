@@ -8,9 +8,11 @@ if the library is missing every call raises.
 The ``softmax_fwd`` / ``rmsnorm_fwd`` / ``layernorm_fwd`` / ``xent_fwd`` helpers take
 and return CUDA tensors (they allocate the outputs with PyTorch and then call
 the C entry points), and so do ``add_rmsnorm_fwd`` / ``add_rmsnorm_bwd`` /
-``rmsnorm_quant_fwd`` / ``linear_xent_fwd`` / ``linear_xent_bwd``, which allocate
-their workspaces too.  A helper runs on torch's current stream, or on the
-``stream`` it is given, which has to have waited for the inputs.
+``rmsnorm_quant_fwd`` / ``linear_xent_fwd`` / ``linear_xent_bwd`` / ``quant_fwd`` /
+``scaled_mm_fwd`` / ``expert_sort`` / ``expert_gather_fwd`` / ``expert_combine_fwd`` /
+``expert_combine_bwd``, which allocate their workspaces too.  A helper runs on
+torch's current stream, or on the ``stream`` it is given, which has to have
+waited for the inputs.
 """
 from __future__ import annotations
 
@@ -43,7 +45,9 @@ _EXPORTS = (
     "qk_xent_fwd_ex", "qk_xent_bwd_ex", "qk_layernorm_fwd", "qk_add_rmsnorm_fwd",
     "qk_add_rmsnorm_bwd", "qk_add_rmsnorm_bwd_workspace_size", "qk_rmsnorm_quant_fwd",
     "qk_linear_xent_fwd", "qk_linear_xent_fwd_workspace_size", "qk_linear_xent_bwd",
-    "qk_linear_xent_bwd_workspace_size",
+    "qk_linear_xent_bwd_workspace_size", "qk_quant_fwd", "qk_scaled_mm_fwd",
+    "qk_scaled_mm_workspace_size", "qk_expert_sort", "qk_expert_sort_workspace_size",
+    "qk_expert_gather_fwd", "qk_expert_combine_fwd", "qk_expert_combine_bwd",
 )
 
 
@@ -116,13 +120,25 @@ def load_library(path: str = LIBRARY):
         lib.qk_linear_xent_fwd.argtypes = [vp] * 7 + [ctypes.c_size_t, i64, i64, i64, i32, op, vp]
         lib.qk_linear_xent_bwd_workspace_size.argtypes = [i64, i64, i64, i32, sp]
         lib.qk_linear_xent_bwd.argtypes = [vp] * 8 + [ctypes.c_size_t, i64, i64, i64, i32, op, vp]
+        sz = ctypes.c_size_t
+        lib.qk_quant_fwd.argtypes = [vp] * 5 + [i64, i64, i64, i32, i32, vp]
+        lib.qk_scaled_mm_workspace_size.argtypes = [i64, i64, i64, i64, sp]
+        lib.qk_scaled_mm_fwd.argtypes = [vp] * 7 + [sz, i64, i64, i64, i64, i64, i32, vp]
+        lib.qk_expert_sort_workspace_size.argtypes = [i64, i64, i64, sp]
+        lib.qk_expert_sort.argtypes = [vp, i64, vp, vp, vp, sz, i64, i64, i64, vp]
+        lib.qk_expert_gather_fwd.argtypes = [vp] * 5 + [i64] * 5 + [vp]
+        lib.qk_expert_combine_fwd.argtypes = [vp] * 4 + [i64] * 4 + [i32, vp]
+        lib.qk_expert_combine_bwd.argtypes = [vp] * 6 + [i64] * 4 + [i32, vp]
         for name in ("qk_softmax_fwd", "qk_rmsnorm_fwd", "qk_xent_fwd", "qk_get_device_status",
                      "qk_get_plan", "qk_set_plan_override", "qk_test_wait_timeout",
                      "qk_softmax_bwd", "qk_rmsnorm_bwd_workspace_size", "qk_rmsnorm_bwd",
                      "qk_xent_bwd", "qk_rmsnorm_bwd_noalloc", "qk_xent_fwd_ex", "qk_xent_bwd_ex",
                      "qk_layernorm_fwd", "qk_add_rmsnorm_fwd", "qk_add_rmsnorm_bwd_workspace_size",
                      "qk_add_rmsnorm_bwd", "qk_rmsnorm_quant_fwd", "qk_linear_xent_fwd_workspace_size",
-                     "qk_linear_xent_fwd", "qk_linear_xent_bwd_workspace_size", "qk_linear_xent_bwd"):
+                     "qk_linear_xent_fwd", "qk_linear_xent_bwd_workspace_size", "qk_linear_xent_bwd",
+                     "qk_quant_fwd", "qk_scaled_mm_workspace_size", "qk_scaled_mm_fwd",
+                     "qk_expert_sort_workspace_size", "qk_expert_sort", "qk_expert_gather_fwd",
+                     "qk_expert_combine_fwd", "qk_expert_combine_bwd"):
             getattr(lib, name).restype = i32
         del fp
         _lib = lib
@@ -289,6 +305,57 @@ def qk_linear_xent_bwd(h, w, targets, lse, dloss, dh, dw, workspace, workspace_b
                                              _ptr(dh), _ptr(dw), _ptr(workspace), int(workspace_bytes), M,
                                              V, K, dtype, _options(ignore_index, z_loss), _stream(stream)),
            "qk_linear_xent_bwd")
+
+
+def qk_quant_fwd(x, q, scale, qt, scale_t, M: int, N: int, block_rows: int, dtype: int, qtype: int,
+                 stream=None) -> None:
+    _check(load_library().qk_quant_fwd(_ptr(x), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), M, N, block_rows,
+                                       dtype, qtype, _stream(stream)), "qk_quant_fwd")
+
+
+def qk_scaled_mm_workspace_size(M: int, N: int, K: int, experts: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().qk_scaled_mm_workspace_size(M, N, K, experts, ctypes.byref(n)),
+           "qk_scaled_mm_workspace_size")
+    return n.value
+
+
+def qk_scaled_mm_fwd(a, a_scale, b, b_scale, offsets, y, workspace, workspace_bytes: int, M: int, N: int, K: int,
+                     experts: int, b_block_rows: int, out_dtype: int, stream=None) -> None:
+    _check(load_library().qk_scaled_mm_fwd(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(offsets), _ptr(y),
+                                           _ptr(workspace), int(workspace_bytes), M, N, K, experts, b_block_rows,
+                                           out_dtype, _stream(stream)), "qk_scaled_mm_fwd")
+
+
+def qk_expert_sort_workspace_size(T: int, k: int, num_experts: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().qk_expert_sort_workspace_size(T, k, num_experts, ctypes.byref(n)),
+           "qk_expert_sort_workspace_size")
+    return n.value
+
+
+def qk_expert_sort(experts, id_bytes: int, offsets, slot, workspace, workspace_bytes: int, T: int, k: int,
+                   num_experts: int, stream=None) -> None:
+    _check(load_library().qk_expert_sort(_ptr(experts), id_bytes, _ptr(offsets), _ptr(slot), _ptr(workspace),
+                                         int(workspace_bytes), T, k, num_experts, _stream(stream)), "qk_expert_sort")
+
+
+def qk_expert_gather_fwd(x, scale, slot, rows, row_scale, T: int, k: int, P: int, row_bytes: int, groups: int,
+                         stream=None) -> None:
+    _check(load_library().qk_expert_gather_fwd(_ptr(x), _ptr(scale), _ptr(slot), _ptr(rows), _ptr(row_scale), T, k,
+                                               P, row_bytes, groups, _stream(stream)), "qk_expert_gather_fwd")
+
+
+def qk_expert_combine_fwd(rows, slot, weights, y, T: int, k: int, P: int, N: int, dtype: int, stream=None) -> None:
+    _check(load_library().qk_expert_combine_fwd(_ptr(rows), _ptr(slot), _ptr(weights), _ptr(y), T, k, P, N, dtype,
+                                                _stream(stream)), "qk_expert_combine_fwd")
+
+
+def qk_expert_combine_bwd(dy, rows, slot, weights, drows, dweights, T: int, k: int, P: int, N: int, dtype: int,
+                          stream=None) -> None:
+    _check(load_library().qk_expert_combine_bwd(_ptr(dy), _ptr(rows), _ptr(slot), _ptr(weights), _ptr(drows),
+                                                _ptr(dweights), T, k, P, N, dtype, _stream(stream)),
+           "qk_expert_combine_bwd")
 
 
 def qk_status_string(status: int) -> str:
@@ -659,3 +726,213 @@ def linear_xent_bwd(h, w, targets, lse, dloss=None, ignore_index=None, z_loss: f
         dh.data_ptr() if want_dh else None, dw.data_ptr() if want_dw else None, ws.data_ptr(), nbytes, M, V, K, code,
         _options(ignore_index, z_loss), _current_stream(dev)), "qk_linear_xent_bwd")
     return dh, dw
+
+
+def _device(x):
+    """The device index of a CUDA tensor on the current device, as _matrix finds it."""
+    global torch
+    if torch is None:
+        import torch as _torch
+        torch = _torch
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def quant_fwd(x, block_rows: int = 1, qdtype=None, want_q: bool = True, want_t: bool = False, stream=None):
+    """x [..., N] in 8 bits with a scale for each 128 columns of a row
+    (block_rows 1) or each block of 128 x 128 (block_rows 128, x of two
+    dimensions); returns (q, scale, qt, scale_t).  qt, with want_t, is x
+    transposed in 8 bits (x of two dimensions), its scales along x's columns.
+    What is not wanted is None.  qdtype as in rmsnorm_quant_fwd."""
+    if stream is not None:
+        return _on(stream, quant_fwd, x, block_rows, qdtype, want_q, want_t)
+    M, N, code, dev = _matrix(x)
+    if qdtype is None or qdtype is torch.float8_e4m3fn:
+        qdtype, qcode = torch.float8_e4m3fn, QK_E4M3
+    elif qdtype is torch.int8:
+        qcode = QK_INT8
+    else:
+        raise TypeError(f"unsupported qdtype {qdtype}: torch.float8_e4m3fn or torch.int8 expected")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if not want_q and not want_t:
+        raise ValueError("nothing is wanted")
+    if (want_t or block_rows == 128) and x.dim() != 2:
+        raise ValueError("blocks of rows and transposes need an x of two dimensions")
+    shape, device = x.shape, x.device
+    q = scale = qt = scale_t = None
+    f32 = torch.float32
+    if want_q:
+        q = torch.empty(shape, dtype=qdtype, device=device)
+        lead = shape[:-1] if block_rows == 1 else (_blocks(M),)
+        scale = torch.empty(lead + (_blocks(N),), dtype=f32, device=device)
+    if want_t:
+        qt = torch.empty((N, M), dtype=qdtype, device=device)
+        scale_t = torch.empty((N if block_rows == 1 else _blocks(N), _blocks(M)), dtype=f32, device=device)
+    _check(load_library().qk_quant_fwd(
+        x.data_ptr(), q.data_ptr() if want_q else None, scale.data_ptr() if want_q else None,
+        qt.data_ptr() if want_t else None, scale_t.data_ptr() if want_t else None, M, N, block_rows, code, qcode,
+        _current_stream(dev)), "qk_quant_fwd")
+    return q, scale, qt, scale_t
+
+
+def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None, stream=None):
+    """The product a @ b.T of 8-bit values (torch.float8_e4m3fn) with a scale for
+    each block of 128 of the last axis: a [..., K] with a_scale [..., blocks], b
+    [N, K] with b_scale [blocks of N, blocks] or [N, blocks].  With offsets
+    (int32, from expert_sort) a is [rows, K], b [experts, N, K], and rows
+    offsets[e] ... offsets[e + 1] - 1 are multiplied with b[e].T; rows behind
+    the last are left as they were in `out`, and not written in a new tensor.
+    The output is out_dtype, or out's (torch.bfloat16 or torch.float32; bfloat16
+    when neither is given)."""
+    if stream is not None:
+        return _on(stream, scaled_mm_fwd, a, a_scale, b, b_scale, offsets, out_dtype, out)
+    dev = _device(a)
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if a.dim() < 1 or b.dim() != (2 if offsets is None else 3):
+        raise ValueError("b must be [N, K], or [experts, N, K] with offsets")
+    shape = a.shape
+    K, N = shape[-1], b.shape[-2]
+    M = a.numel() // max(K, 1)
+    experts = 1 if offsets is None else b.shape[0]
+    _same("a", a, shape, e4m3, dev)
+    _same("b", b, b.shape[:-1] + (K,), e4m3, dev)
+    G = _blocks(K)
+    _same("a_scale", a_scale, shape[:-1] + (G,), f32, dev)
+    rows = b_scale.shape[-2] if b_scale.dim() > 1 else -1
+    if rows != N and rows != _blocks(N):
+        raise ValueError(f"b_scale must have {_blocks(N)} or {N} rows")
+    _same("b_scale", b_scale, b.shape[:-2] + (rows, G), f32, dev)
+    if offsets is not None:
+        if a.dim() != 2:
+            raise ValueError("a must be [rows, K] with offsets")
+        _same("offsets", offsets, (experts + 1,), torch.int32, dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype is torch.bfloat16:
+        code = QK_BF16
+    elif out_dtype is f32:
+        code = QK_F32
+    else:
+        raise TypeError(f"unsupported out_dtype {out_dtype}: float32 or bfloat16 expected")
+    y_shape = shape[:-1] + (N,)
+    y = torch.empty(y_shape, dtype=out_dtype, device=a.device) if out is None else _same("out", out, y_shape,
+                                                                                        out_dtype, dev)
+    nbytes = 0 if K % 16 == 0 else _workspace_bytes(qk_scaled_mm_workspace_size, dev, M, N, K, experts)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=a.device) if nbytes else None
+    _check(load_library().qk_scaled_mm_fwd(
+        a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), y.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, M, N,
+        K, experts, 1 if rows == N else 128, code, _current_stream(dev)), "qk_scaled_mm_fwd")
+    return y
+
+
+def expert_sort(experts, num_experts: int, stream=None):
+    """Sorts the choices experts [T, k] (int32 or int64; outside [0, num_experts):
+    none) by expert, in their order; returns (offsets, slot): int32 [num_experts + 1],
+    where each expert's rows begin, and int32 [T, k], each choice's row (-1: none)."""
+    if stream is not None:
+        return _on(stream, expert_sort, experts, num_experts)
+    dev = _device(experts)
+    if experts.dim() != 2 or not experts.is_contiguous() or experts.dtype not in (torch.int32, torch.int64):
+        raise ValueError("experts must be a contiguous int32 or int64 tensor [T, k]")
+    T, k = experts.shape
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=experts.device)
+    slot = torch.empty((T, k), dtype=torch.int32, device=experts.device)
+    nbytes = _workspace_bytes(qk_expert_sort_workspace_size, dev, T, k, num_experts)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=experts.device) if nbytes else None
+    _check(load_library().qk_expert_sort(
+        experts.data_ptr(), 4 if experts.dtype is torch.int32 else 8, offsets.data_ptr(), slot.data_ptr(),
+        ws.data_ptr() if nbytes else None, nbytes, T, k, num_experts, _current_stream(dev)), "qk_expert_sort")
+    return offsets, slot
+
+
+def _choices(slot, T, dev):
+    if slot.dim() != 2 or slot.shape[0] != T:
+        raise ValueError(f"slot must be [{T}, k]")
+    _same("slot", slot, slot.shape, torch.int32, dev)
+    return slot.shape[1]
+
+
+def expert_gather_fwd(x, slot, scale=None, out=None, out_scale=None, stream=None):
+    """Copies each token's row x[t] to row slot[t, j] for each of its choices;
+    returns the rows [T * k, N] (or out, [any number, N]).  With scale [T, groups]
+    (float32, 8-bit rows) the scales move too, and (rows, row scales) is returned.
+    Rows that no slot names are left as they were in `out`, and not written in a
+    new tensor.  The gradient for x is expert_combine_fwd(drows, slot)."""
+    if stream is not None:
+        return _on(stream, expert_gather_fwd, x, slot, scale, out, out_scale)
+    dev = _device(x)
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous tensor [T, N]")
+    T, N = x.shape
+    k = _choices(slot, T, dev)
+    rows = torch.empty((T * k, N), dtype=x.dtype, device=x.device) if out is None else out
+    P = rows.shape[0]
+    if out is not None:
+        _same("out", out, (P, N), x.dtype, dev)
+    groups, row_scale = 0, None
+    if scale is not None:
+        if scale.dim() != 2:
+            raise ValueError("scale must be [T, groups]")
+        groups = scale.shape[1]
+        _same("scale", scale, (T, groups), torch.float32, dev)
+        row_scale = (torch.empty((P, groups), dtype=torch.float32, device=x.device) if out_scale is None
+                     else _same("out_scale", out_scale, (P, groups), torch.float32, dev))
+    elif out_scale is not None:
+        raise ValueError("out_scale needs a scale")
+    _check(load_library().qk_expert_gather_fwd(
+        x.data_ptr(), None if scale is None else scale.data_ptr(), slot.data_ptr(), rows.data_ptr(),
+        None if scale is None else row_scale.data_ptr(), T, k, P, N * x.element_size(), groups, _current_stream(dev)),
+        "qk_expert_gather_fwd")
+    return rows if scale is None else (rows, row_scale)
+
+
+def expert_combine_fwd(rows, slot, weights=None, out=None, stream=None):
+    """Each token's sum over its choices of weights[t, j] * rows[slot[t, j]] (weights
+    float32 [T, k], None: 1); choices without a slot are left out."""
+    if stream is not None:
+        return _on(stream, expert_combine_fwd, rows, slot, weights, out)
+    P, N, code, dev = _matrix(rows)
+    if rows.dim() != 2:
+        raise ValueError("rows must be [rows, N]")
+    T = slot.shape[0] if slot.dim() > 0 else 0
+    k = _choices(slot, T, dev)
+    if weights is not None:
+        _same("weights", weights, (T, k), torch.float32, dev)
+    y = torch.empty((T, N), dtype=rows.dtype, device=rows.device) if out is None else _same("out", out, (T, N),
+                                                                                           rows.dtype, dev)
+    _check(load_library().qk_expert_combine_fwd(
+        rows.data_ptr(), slot.data_ptr(), None if weights is None else weights.data_ptr(), y.data_ptr(), T, k, P, N,
+        code, _current_stream(dev)), "qk_expert_combine_fwd")
+    return y
+
+
+def expert_combine_bwd(dy, rows, slot, weights, out=None, want_dweights: bool = True, stream=None):
+    """Backward of expert_combine_fwd; returns (drows, dweights) (dweights is None
+    if not wanted).  out may be rows; rows that no slot names are left as they
+    were in it, and not written in a new tensor."""
+    if stream is not None:
+        return _on(stream, expert_combine_bwd, dy, rows, slot, weights, out, want_dweights)
+    T, N, code, dev = _matrix(dy)
+    if dy.dim() != 2 or rows.dim() != 2:
+        raise ValueError("dy must be [T, N] and rows [rows, N]")
+    P = rows.shape[0]
+    _same("rows", rows, (P, N), dy.dtype, dev)
+    k = _choices(slot, T, dev)
+    _same("weights", weights, (T, k), torch.float32, dev)
+    drows = torch.empty_like(rows) if out is None else _same("out", out, (P, N), dy.dtype, dev)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dy.device) if want_dweights else None
+    _check(load_library().qk_expert_combine_bwd(
+        dy.data_ptr(), rows.data_ptr(), slot.data_ptr(), weights.data_ptr(), drows.data_ptr(),
+        dweights.data_ptr() if want_dweights else None, T, k, P, N, code, _current_stream(dev)),
+        "qk_expert_combine_bwd")
+    return drows, dweights

@@ -1,0 +1,484 @@
+// qk_experts.cu -- tokens sorted by expert, and back with weights.
+//
+//   sort     offsets[e] = number of choices of experts below e; slot[t, j] = place
+//            of choice (t, j) among the choices sorted by expert, in their order
+//   gather   rows[slot[t, j]] = x[t]
+//   combine  y[t] = sum_j weight[t, j] rows[slot[t, j]];
+//            drows[slot[t, j]] = weight[t, j] dy[t],  dweight[t, j] = dy[t] . rows[slot[t, j]]
+//
+// All bound by memory (the sort by latency): a token's row is read once and its
+// k rows are written, or the other way round.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "../../include/qk.h"
+#include "qk_device.cuh"
+#include "qk_host.h"
+
+namespace qk {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int64_t kMaxChoices = INT32_MAX - 65536;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int64_t kSortChunk = 4096;  // choices of a CTA, where they are few enough
+
+// ---------------------------------------------------------------------------
+// Sort
+// ---------------------------------------------------------------------------
+struct SortArgs {
+  const void* ids;
+  int32_t wide;       // ids are int64
+  int32_t experts;
+  int32_t blocks;
+  int64_t n, chunk;   // choices, and those of a CTA
+  int32_t* offsets;   // [experts + 1]
+  int32_t* slot;      // [n]
+  int32_t* counts;    // [blocks][experts], null where one CTA has all
+};
+
+__device__ __forceinline__ int32_t expert_at(const SortArgs& a, int64_t i) {
+  const int64_t v = a.wide ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+  return v >= 0 && v < a.experts ? int32_t(v) : -1;
+}
+
+// Choices of each expert among a CTA's.
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+  __shared__ int32_t hist[kMaxExperts];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t i0 = blockIdx.x * a.chunk, i1 = min(a.n, i0 + a.chunk);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
+    const int32_t e = expert_at(a, i);
+    if (e >= 0) atomicAdd(&hist[e], 1);  // whole numbers: any order gives the same
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.counts[int64_t(blockIdx.x) * a.experts + e] = hist[e];
+}
+
+// Places.  Each warp has a run of the CTA's choices: its counts by expert, summed
+// over the warps before it, are where its first choice of an expert goes.
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortArgs a) {
+  extern __shared__ int32_t next[];  // [warps][experts]
+  __shared__ int32_t sums[kSortWarps];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.experts;
+  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) next[i] = 0;
+  __syncthreads();
+  const int64_t c0 = blockIdx.x * a.chunk, c1 = min(a.n, c0 + a.chunk);
+  const int64_t run = ((a.chunk + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+  const int64_t i0 = min(c1, c0 + warp * run), i1 = min(c1, i0 + run);
+  int32_t* mine = next + warp * E;
+  for (int64_t i = i0 + lane; i < i1; i += 32) {
+    const int32_t e = expert_at(a, i);
+    if (e >= 0) atomicAdd(&mine[e], 1);
+  }
+  __syncthreads();
+  // Two experts a thread: all choices of each, those of the CTAs before this one, and
+  // the sum over the experts below.
+  int32_t total[2], before[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int e = int(threadIdx.x) * 2 + k;
+    total[k] = before[k] = 0;
+    if (e >= E) continue;
+    if (a.counts != nullptr) {
+      for (int b = 0; b < a.blocks; ++b) {
+        const int32_t c = a.counts[int64_t(b) * E + e];
+        total[k] += c;
+        if (b < int(blockIdx.x)) before[k] += c;
+      }
+    } else {
+      for (int w = 0; w < kSortWarps; ++w) total[k] += next[w * E + e];
+    }
+  }
+  int32_t sum = total[0] + total[1];
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  if (lane == 31) sums[warp] = sum;
+  __syncthreads();
+  int32_t base = sum - total[0] - total[1];
+  for (int w = 0; w < warp; ++w) base += sums[w];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int e = int(threadIdx.x) * 2 + k;
+    if (e < E) {
+      if (blockIdx.x == 0) {
+        a.offsets[e] = base;
+        if (e == E - 1) a.offsets[E] = base + total[k];
+      }
+      int32_t at = base + before[k];
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int32_t c = next[w * E + e];
+        next[w * E + e] = at;
+        at += c;
+      }
+    }
+    base += total[k];
+  }
+  __syncthreads();
+  for (int64_t i = i0; i < i1; i += 32) {  // in order, 32 at a time
+    const int32_t e = i + lane < i1 ? expert_at(a, i + lane) : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int32_t at = e >= 0 ? mine[e] + rank : -1;
+    __syncwarp();
+    if (e >= 0 && rank == 0) mine[e] += __popc(same);
+    __syncwarp();
+    if (i + lane < i1) a.slot[i + lane] = at;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gather: a warp copies a piece of a token's row to the places of its choices
+// ---------------------------------------------------------------------------
+struct GatherArgs {
+  const uint8_t* x;
+  const float* scale;
+  const int32_t* slot;
+  uint8_t* rows;
+  float* row_scale;
+  int64_t T, P, row_bytes, pieces;
+  int32_t k, groups;
+};
+
+template <typename W>
+__global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
+  constexpr int kUnroll = 4;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t words = a.row_bytes / int64_t(sizeof(W)), units = a.T * a.pieces;
+  for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
+    const int64_t t = u / a.pieces, piece = u - t * a.pieces;
+    const W* src = reinterpret_cast<const W*>(a.x + t * a.row_bytes);
+    const int64_t w0 = piece * (32 * kUnroll) + lane;
+    W v[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i)
+      if (w0 + 32 * i < words) v[i] = src[w0 + 32 * i];
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t at = a.slot[t * a.k + j];
+      if (at < 0 || at >= a.P) continue;
+      W* dst = reinterpret_cast<W*>(a.rows + int64_t(at) * a.row_bytes);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+        if (w0 + 32 * i < words) dst[w0 + 32 * i] = v[i];
+      if (piece == 0)
+        for (int g = lane; g < a.groups; g += 32)
+          a.row_scale[int64_t(at) * a.groups + g] = a.scale[t * a.groups + g];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine
+// ---------------------------------------------------------------------------
+struct CombineArgs {
+  const void* dy;        // [T, N] backward
+  const void* rows;      // [P, N]
+  const int32_t* slot;   // [T, k]
+  const float* weights;  // [T, k], null: 1 (forward)
+  void* out;             // [T, N] y, or [P, N] drows
+  float* dweights;       // [T, k] backward, may be null
+  int64_t T, P, N, pieces;
+  int32_t k;
+};
+
+// E values from p, of which `left` count.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_values(const T* p, int64_t left, float* f) {
+  using V = Vec16<T>;
+  if constexpr (VEC) {
+    V::unpack(*reinterpret_cast<const uint4*>(p), f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_values(T* p, int64_t left, const float* f) {
+  using V = Vec16<T>;
+  if constexpr (VEC) {
+    *reinterpret_cast<uint4*>(p) = V::pack(f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V::kElems; ++j)
+      if (j < left) V::store1(p + j, f[j]);
+  }
+}
+
+// A warp forms a piece of a token's row; the sum runs over the choices in order.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
+  constexpr int E = Vec16<T>::kElems;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t units = a.T * a.pieces;
+  for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
+    const int64_t t = u / a.pieces, c = ((u - t * a.pieces) * 32 + lane) * E;
+    if (c >= a.N) continue;
+    float sum[E] = {};
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t at = a.slot[t * a.k + j];
+      if (at < 0 || at >= a.P) continue;
+      const float w = a.weights != nullptr ? a.weights[t * a.k + j] : 1.f;
+      float f[E];
+      load_values<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at) * a.N + c, a.N - c, f);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+    }
+    store_values<T, VEC>(static_cast<T*>(a.out) + t * a.N + c, a.N - c, sum);
+  }
+}
+
+// A CTA takes a token: its choices one after the other, dy again from L1 or L2.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs a) {
+  constexpr int E = Vec16<T>::kElems;
+  __shared__ float red[8];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const T* dy = static_cast<const T*>(a.dy) + t * a.N;
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t at = a.slot[t * a.k + j];
+      const bool there = at >= 0 && at < a.P;
+      float dot = 0.f;
+      if (there) {
+        const float w = a.weights[t * a.k + j];
+        const T* row = static_cast<const T*>(a.rows) + int64_t(at) * a.N;
+        T* out = static_cast<T*>(a.out) + int64_t(at) * a.N;
+        for (int64_t c = threadIdx.x * E; c < a.N; c += 256 * E) {
+          float g[E], f[E];
+          load_values<T, VEC>(dy + c, a.N - c, g);
+          load_values<T, VEC>(row + c, a.N - c, f);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            dot = fmaf(g[i], f[i], dot);
+            g[i] *= w;
+          }
+          store_values<T, VEC>(out + c, a.N - c, g);
+        }
+      }
+      if (a.dweights == nullptr) continue;
+      dot = group_sum<32>(dot);
+      __syncthreads();
+      if (lane == 0) red[warp] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float s = 0.f;
+        for (int w = 0; w < 8; ++w) s += red[w];
+        a.dweights[t * a.k + j] = there ? s : 0.f;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+qk_status check_choices(int64_t T, int64_t k) {
+  if (T < 0 || k <= 0) return QK_ERR_INVALID_ARG;
+  if (T > kMaxChoices / k) return QK_ERR_UNSUPPORTED;
+  return QK_OK;
+}
+int64_t sort_blocks(int64_t n) { return std::min<int64_t>(152, ceil_div(n, kSortChunk)); }
+
+unsigned warps_grid(const CurrentDevice& d, int64_t units) {
+  return unsigned(std::max<int64_t>(1, std::min<int64_t>(ceil_div(units, 8), int64_t(d.sms) * 32)));
+}
+
+struct Buffer {
+  const void* p;
+  int64_t n;
+};
+template <int NO, int NI>
+bool any_overlap(const Buffer (&out)[NO], const Buffer (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Buffer& b : in)
+      if (overlap(out[i].p, out[i].n, b.p, b.n)) return true;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+template <typename T>
+qk_status launch_combine(const CurrentDevice& d, bool bwd, bool vec, CombineArgs a, void* stream) {
+  a.pieces = ceil_div(a.N, 32 * Vec16<T>::kElems);
+  if (bwd) {
+    const auto kernel = vec ? combine_bwd_kernel<T, true> : combine_bwd_kernel<T, false>;
+    return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(a.T, int64_t(d.sms) * 32))), 256, 0, stream, a);
+  }
+  const auto kernel = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
+  return launch_pdl(kernel, dim3(warps_grid(d, a.T * a.pieces)), 256, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace qk
+
+using namespace qk;
+
+extern "C" {
+
+qk_status qk_expert_sort_workspace_size(int64_t T, int64_t k, int64_t experts, size_t* bytes) {
+  if (bytes == nullptr) return QK_ERR_INVALID_ARG;
+  *bytes = 0;
+  const qk_status st = check_choices(T, k);
+  if (st != QK_OK) return st;
+  if (experts <= 0) return QK_ERR_INVALID_ARG;
+  if (experts > kMaxExperts) return QK_ERR_UNSUPPORTED;
+  const int64_t blocks = sort_blocks(T * k);
+  if (blocks > 1) *bytes = size_t(blocks * experts * 4);
+  return QK_OK;
+}
+
+qk_status qk_expert_sort(const void* experts, int64_t id_bytes, int32_t* offsets, int32_t* slot, void* workspace,
+                         size_t workspace_bytes, int64_t T, int64_t k, int64_t num_experts, void* stream) {
+  size_t need = 0;
+  qk_status st = qk_expert_sort_workspace_size(T, k, num_experts, &need);
+  if (st != QK_OK) return st;
+  if (id_bytes != 4 && id_bytes != 8) return QK_ERR_INVALID_ARG;
+  const int64_t n = T * k;
+  if (offsets == nullptr || (n > 0 && (experts == nullptr || slot == nullptr))) return QK_ERR_INVALID_ARG;
+  if (!aligned_to(experts, size_t(id_bytes)) || !aligned_to(offsets, 4) || !aligned_to(slot, 4)) return QK_ERR_MISALIGNED;
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return QK_ERR_INVALID_ARG;
+    if (!aligned_to(workspace, 16)) return QK_ERR_MISALIGNED;
+  }
+  const Buffer out[] = {{offsets, (num_experts + 1) * 4}, {slot, n * 4}, {workspace, int64_t(need)}},
+               in[] = {{experts, n * id_bytes}};
+  if (any_overlap(out, in)) return QK_ERR_INVALID_ARG;
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  SortArgs a = {};
+  a.ids = experts;
+  a.wide = id_bytes == 8;
+  a.experts = int32_t(num_experts);
+  a.n = n;
+  a.blocks = int32_t(std::max<int64_t>(1, sort_blocks(n)));
+  a.chunk = ceil_div(std::max<int64_t>(n, 1), a.blocks);
+  a.offsets = offsets;
+  a.slot = slot;
+  a.counts = a.blocks > 1 ? static_cast<int32_t*>(workspace) : nullptr;
+  if (a.blocks > 1) {
+    st = launch_pdl(sort_count_kernel, dim3(unsigned(a.blocks)), kSortThreads, 0, stream, a);
+    if (st != QK_OK) return st;
+  }
+  const size_t smem = size_t(kSortWarps) * num_experts * 4;
+  if (smem > (48 << 10) - 1024) {
+    static std::atomic<uint64_t> prepared{0};  // one bit a device
+    const uint64_t bit = uint64_t(1) << (d.index & 63);
+    if (!(prepared.load(std::memory_order_acquire) & bit)) {
+      if (cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSortWarps * kMaxExperts * 4) != cudaSuccess) {
+        cudaGetLastError();
+        return QK_ERR_LAUNCH;
+      }
+      prepared.fetch_or(bit, std::memory_order_acq_rel);
+    }
+  }
+  return launch_pdl(sort_place_kernel, dim3(unsigned(a.blocks)), kSortThreads, smem, stream, a);
+}
+
+qk_status qk_expert_gather_fwd(const void* x, const float* scale, const int32_t* slot, void* rows, float* row_scale,
+                               int64_t T, int64_t k, int64_t P, int64_t row_bytes, int64_t groups, void* stream) {
+  qk_status st = check_choices(T, k);
+  if (st != QK_OK) return st;
+  if (P < 0 || row_bytes <= 0 || groups < 0) return QK_ERR_INVALID_ARG;
+  if (P > INT32_MAX || groups > INT32_MAX) return QK_ERR_UNSUPPORTED;
+  if (std::max(T, P) > INT64_MAX / 16 / std::max(row_bytes, groups)) return QK_ERR_UNSUPPORTED;
+  if ((scale == nullptr) != (groups == 0) || (row_scale == nullptr) != (groups == 0)) return QK_ERR_INVALID_ARG;
+  if (T == 0 || P == 0) return QK_OK;
+  if (x == nullptr || slot == nullptr || rows == nullptr) return QK_ERR_INVALID_ARG;
+  if (!aligned_to(scale, 4) || !aligned_to(slot, 4) || !aligned_to(row_scale, 4)) return QK_ERR_MISALIGNED;
+  const Buffer out[] = {{rows, P * row_bytes}, {row_scale, P * groups * 4}},
+               in[] = {{x, T * row_bytes}, {scale, T * groups * 4}, {slot, T * k * 4}};
+  if (any_overlap(out, in)) return QK_ERR_INVALID_ARG;
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  GatherArgs a = {static_cast<const uint8_t*>(x), scale, slot, static_cast<uint8_t*>(rows), row_scale,
+                  T, P, row_bytes, 0, int32_t(k), int32_t(groups)};
+  // The widest word that rows consist of.
+  const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | uintptr_t(row_bytes);
+  auto launch = [&](auto kernel, int64_t word) {
+    a.pieces = ceil_div(row_bytes / word, 128);
+    return launch_pdl(kernel, dim3(warps_grid(d, T * a.pieces)), 256, 0, stream, a);
+  };
+  if (all % 16 == 0) return launch(gather_kernel<uint4>, 16);
+  if (all % 4 == 0) return launch(gather_kernel<uint32_t>, 4);
+  if (all % 2 == 0) return launch(gather_kernel<uint16_t>, 2);
+  return launch(gather_kernel<uint8_t>, 1);
+}
+
+qk_status qk_expert_combine_fwd(const void* rows, const int32_t* slot, const float* weights, void* y, int64_t T,
+                                int64_t k, int64_t P, int64_t N, qk_dtype dtype, void* stream) {
+  qk_status st = check_choices(T, k);
+  if (st != QK_OK) return st;
+  if (dtype != QK_F32 && dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (P < 0 || N <= 0) return QK_ERR_INVALID_ARG;
+  if (P > INT32_MAX || std::max(T, P) > INT64_MAX / 16 / N) return QK_ERR_UNSUPPORTED;
+  if (T == 0) return QK_OK;
+  if ((rows == nullptr && P > 0) || slot == nullptr || y == nullptr) return QK_ERR_INVALID_ARG;
+  const size_t es = size_t(elem_size(dtype));
+  if (!aligned_to(rows, es) || !aligned_to(y, es) || !aligned_to(slot, 4) || !aligned_to(weights, 4))
+    return QK_ERR_MISALIGNED;
+  const Buffer out[] = {{y, T * N * int64_t(es)}},
+               in[] = {{rows, P * N * int64_t(es)}, {slot, T * k * 4}, {weights, T * k * 4}};
+  if (any_overlap(out, in)) return QK_ERR_INVALID_ARG;
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  const CombineArgs a = {nullptr, rows, slot, weights, y, nullptr, T, P, N, 0, int32_t(k)};
+  const bool vec = N * int64_t(es) % 16 == 0 && aligned16(rows) && aligned16(y);
+  return dtype == QK_F32 ? launch_combine<float>(d, false, vec, a, stream)
+                         : launch_combine<__nv_bfloat16>(d, false, vec, a, stream);
+}
+
+qk_status qk_expert_combine_bwd(const void* dy, const void* rows, const int32_t* slot, const float* weights,
+                                void* drows, float* dweights, int64_t T, int64_t k, int64_t P, int64_t N,
+                                qk_dtype dtype, void* stream) {
+  qk_status st = check_choices(T, k);
+  if (st != QK_OK) return st;
+  if (dtype != QK_F32 && dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (P < 0 || N <= 0) return QK_ERR_INVALID_ARG;
+  if (P > INT32_MAX || std::max(T, P) > INT64_MAX / 16 / N) return QK_ERR_UNSUPPORTED;
+  if (T == 0) return QK_OK;
+  if (dy == nullptr || slot == nullptr || weights == nullptr || (P > 0 && (rows == nullptr || drows == nullptr)))
+    return QK_ERR_INVALID_ARG;
+  const size_t es = size_t(elem_size(dtype));
+  if (!aligned_to(dy, es) || !aligned_to(rows, es) || !aligned_to(drows, es) || !aligned_to(slot, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+    return QK_ERR_MISALIGNED;
+  const int64_t pb = P * N * int64_t(es);
+  const Buffer out[] = {{drows, pb}, {dweights, T * k * 4}},
+               in[] = {{dy, T * N * int64_t(es)}, {drows == rows ? nullptr : rows, pb}, {slot, T * k * 4},
+                       {weights, T * k * 4}};
+  if (any_overlap(out, in) || overlap(dweights, T * k * 4, rows, pb)) return QK_ERR_INVALID_ARG;
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  const CombineArgs a = {dy, rows, slot, weights, drows, dweights, T, P, N, 0, int32_t(k)};
+  const bool vec = N * int64_t(es) % 16 == 0 && aligned16(rows) && aligned16(drows) && aligned16(dy);
+  return dtype == QK_F32 ? launch_combine<float>(d, true, vec, a, stream)
+                         : launch_combine<__nv_bfloat16>(d, true, vec, a, stream);
+}
+
+}  // extern "C"

@@ -24,6 +24,7 @@
 #include "qk_host.h"
 #include "qk_kernels.cuh"  // xent_mean_kernel
 #include "qk_product_kernel.cuh"
+#include "qk_tensor_map.h"
 
 namespace qk {
 namespace {
@@ -488,25 +489,6 @@ struct Call {
 // ---------------------------------------------------------------------------
 // Tensor maps and launches
 // ---------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      p = nullptr;
-    }
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
 // A bf16 operand [planes][rows][ld] of which the first `inner` columns count.
 struct Operand {
   const void* base;
