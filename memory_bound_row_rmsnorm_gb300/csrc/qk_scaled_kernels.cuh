@@ -9,6 +9,7 @@
 #pragma once
 
 #include "qk_internal.h"
+#include "qk_rows_out.cuh"
 #include "qk_tensor.cuh"
 
 namespace qk {
@@ -29,7 +30,9 @@ struct ScaledArgs {
   int32_t experts;
   int32_t b_shift;          // 7: a scale a 128 rows of b, 0: a scale a row
   int32_t scale_vec;        // rows of scales are whole aligned float4
-  int32_t lane_tiles;       // tiles along the axis that stands on TMEM's lanes
+  int32_t n_tiles;          // tiles along N
+  int32_t n_full, last_n;   // pairs: tiles of 256 columns, and columns of a product in one behind them
+  int32_t y_vec;            // pairs: rows of y are whole 16-byte vectors
   int32_t split_steps;      // steps of one CTA of a cluster
   uint64_t timeout_ns;
   int* status;
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
   tcgen05_fence_after();
   const uint32_t tmem = tmem_at;
 
-  const int32_t tiles = table.tile0[p.experts] * p.lane_tiles;  // the host bounds it
+  const int32_t tiles = table.tile0[p.experts] * p.n_tiles;  // the host bounds it
   const int32_t first = int32_t(cluster_id_x()), step = int32_t(num_clusters_x());
   const int32_t s0 = int32_t(cluster_ctarank()) * p.split_steps, s1 = min(p.groups, s0 + p.split_steps);
   struct At {
@@ -155,8 +158,8 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
   };
   // Tile t, for t that rise: the expert is found by walking on from the last.
   auto tile = [&](int32_t t, int32_t& e) {
-    while (t >= table.tile0[e + 1] * p.lane_tiles) ++e;
-    const int32_t in = t - table.tile0[e] * p.lane_tiles, m_tiles = table.tile0[e + 1] - table.tile0[e];
+    while (t >= table.tile0[e + 1] * p.n_tiles) ++e;
+    const int32_t in = t - table.tile0[e] * p.n_tiles, m_tiles = table.tile0[e + 1] - table.tile0[e];
     At r;
     r.e = e;
     const int32_t n = in / m_tiles, m = in - n * m_tiles;
@@ -355,6 +358,309 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
   __syncthreads();
   tcgen05_fence_after();
   if (warp == 2) tmem_dealloc(tmem, kColumns);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of 256 rows of a x 256 rows of b, a pair of CTAs each: a on TMEM's lanes,
+// so a thread multiplies with one scale of a and, where b's scales are of blocks
+// (!COLS), one of b: a block's sums cost a fused multiply-add each.
+// ---------------------------------------------------------------------------
+constexpr int kPairStages = 5, kPairStageBytes = 2 * 128 * kScaledStepK;  // one CTA's 128 rows of a and of b
+constexpr int kPairScaleSlots = 2;
+constexpr int kSplitRegistersPair = 128 * 80 + 256 * 208;  // what the warps' shares add up to
+__host__ __device__ constexpr int pair_slot_bytes(bool cols) { return 128 * 16 + (cols ? 256 * 16 : 128); }
+__host__ __device__ constexpr int pair_smem(bool cols) {  // and room to start on 1024 bytes
+  return kPairStages * kPairStageBytes + 8 * kOutBytes + kPairScaleSlots * pair_slot_bytes(cols) + 1024;
+}
+
+template <bool COLS, typename T>
+__global__ void __launch_bounds__(kScaledThreads, 1)
+    scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const ScaledArgs p) {
+  constexpr int kStages = kPairStages, kStageBytes = kPairStageBytes, kSlots = kPairScaleSlots;
+  constexpr int kSlotBytes = pair_slot_bytes(COLS), kCols = 128;
+  constexpr uint32_t kColumns = 512;  // TMEM: two sets of sums
+  extern __shared__ unsigned char dynamic_smem[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kSlots];
+  __shared__ uint32_t tmem_at;
+  __shared__ ExpertTable table;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kStages, done0 = full0 + 16 * kStages,
+                 free0 = done0 + 16, sfull0 = free0 + 16, sempty0 = sfull0 + 8 * kSlots;
+  const uint32_t ring = (smem_addr(dynamic_smem) + 1023u) & ~1023u;  // the same in both CTAs
+  const uint32_t outs = ring + uint32_t(kStages * kStageBytes), slots = outs + 8 * kOutBytes;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);   // the leader's producer, and the bytes of both CTAs
+      mbar_init(empty0 + 8 * s, 1);  // a commit of the leader's products
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done0 + 8 * i, 1);   // a commit: the block is summed
+      mbar_init(free0 + 8 * i, 16);  // the epilogue warps of both CTAs have read it
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(sfull0 + 8 * i, 2);  // this CTA's own scales
+      mbar_init(sempty0 + 8 * i, 8);
+    }
+    fence_mbar_init();
+    prefetch_tensor_map(&map_a);
+    prefetch_tensor_map(&map_b);
+  }
+  __syncwarp();
+  if (warp == 2) {
+    tmem_alloc_pair(smem_addr(&tmem_at), kColumns);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (warp == 3) fill_table(table, p, 256, lane);
+  __syncwarp();
+  tcgen05_fence_before();
+  cluster_sync_all();
+  tcgen05_fence_after();
+  const uint32_t tmem = tmem_at;
+
+  const int32_t tiles = table.tile0[p.experts] * p.n_tiles;  // the host bounds it
+  const int32_t first = int32_t(cluster_id_x()), step = int32_t(num_clusters_x());
+  struct At {
+    int32_t e, n, row0, rows;  // expert, column tile, first row of a, rows of a
+  };
+  // Tile t, for t that rise.  Eight row tiles of an expert are walked together:
+  // the pairs that run at one time share their operands in L2.
+  auto tile = [&](int32_t t, int32_t& e) {
+    while (t >= table.tile0[e + 1] * p.n_tiles) ++e;
+    const uint32_t in = uint32_t(t - table.tile0[e] * p.n_tiles), m_tiles = uint32_t(table.tile0[e + 1] - table.tile0[e]);
+    const uint32_t band = 8u * uint32_t(p.n_tiles), group = in / band, rest = in - group * band;
+    const uint32_t wide = min(8u, m_tiles - group * 8u), n = rest / wide;
+    At r;
+    r.e = e;
+    r.n = int32_t(n);
+    r.row0 = table.row0[e] + int32_t(group * 8u + rest - n * wide) * 256;
+    r.rows = min(256, table.row0[e + 1] - r.row0);
+    return r;
+  };
+
+  bool failed = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (mbar_wait<false>(bar, parity, p.timeout_ns)) return true;
+    report_status(p.status, 5);
+    failed = true;
+    return false;
+  };
+
+  // Registers: the launch holds 384 x 168 = 64512 (the host checks it); 128 x 80
+  // + 256 x 208 = 63488 of them go to the warps that feed and to those that keep sums.
+  int32_t e = 0;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0 && lane == 0) {
+      // ---- producer: this CTA's half of each step's operands ----
+      int64_t q = 0;
+      int st = 0;
+      uint32_t turn = 0;
+      for (int32_t t = first; t < tiles && !failed; t += step) {
+        const At at = tile(t, e);
+        const int32_t a0 = at.row0 + int32_t(rank) * 128,
+                      b0 = at.n * 256 + int32_t(rank) * (at.n < p.n_full ? 128 : p.last_n / 2);
+        for (int32_t s = 0; s < p.groups; ++s, ++q) {
+          if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
+          const uint32_t bar = map_to_rank(full0 + 8 * st, 0), dst = ring + uint32_t(st) * kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, 2 * kStageBytes);
+          tma_load_3d(dst, &map_a, s * kScaledStepK, a0, 0, bar);
+          tma_load_3d(dst + kStageBytes / 2, &map_b, s * kScaledStepK, b0, at.e, bar);
+          if (++st == kStages) st = 0, turn ^= 1u;
+        }
+      }
+      if (failed && rank == 0)  // leave once the loads in flight have landed: the leader's barriers count both CTAs'
+        for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
+          mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---- products of both CTAs ----
+      int st = 0;
+      uint32_t turn = 0, it = 0;
+      for (int32_t t = first; t < tiles && !failed; t += step) {
+        const At at = tile(t, e);
+        const uint32_t idesc = instruction_desc_e4m3(256, at.n < p.n_full ? 256u : uint32_t(p.last_n));
+        for (int32_t s = 0; s < p.groups; ++s, ++it) {
+          const uint32_t buf = it & 1u;
+          if (!wait(free0 + 8 * buf, ((it >> 1) & 1u) ^ 1u)) break;
+          if (!wait(full0 + 8 * st, turn)) break;
+          tcgen05_fence_after();
+          const uint32_t sa = ring + uint32_t(st) * kStageBytes;
+          const uint64_t da = operand_desc(sa, 0), db = operand_desc(sa + kStageBytes / 2, 0);
+#pragma unroll
+          for (int k = 0; k < kScaledStepK / 32; ++k)
+            mma_e4m3_pair(tmem + buf * 256, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, k > 0);
+          mma_commit_pair(empty0 + 8 * st);
+          mma_commit_pair(done0 + 8 * buf);
+          if (++st == kStages) st = 0, turn ^= 1u;
+        }
+      }
+    } else if (warp >= 2) {
+      // ---- scales, four steps at a time: [128 rows of a][4], then [4][256 columns] or [2 blocks][4] ----
+      const int id = (warp - 2) * 32 + lane;
+      uint32_t it = 0;
+      for (int32_t t = first; t < tiles && !failed; t += step) {
+        const At at = tile(t, e);
+        const int32_t n0 = at.n * 256, row0 = int32_t(rank) * 128;
+        const float* as = p.a_scale + int64_t(at.row0) * p.groups;
+        const float* bs = p.b_scale + at.e * p.b_scale_stride;
+        for (int32_t s = 0; s < p.groups; s += kQuad, ++it) {
+          const uint32_t slot = it % kSlots;
+          const bool ok = wait(sempty0 + 8 * slot, ((it / kSlots) & 1u) ^ 1u);
+          if (!__all_sync(0xffffffffu, ok)) {
+            failed = true;
+            break;
+          }
+          const uint32_t dst = slots + slot * kSlotBytes, cols = dst + 128 * 16;
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 f[2], g[COLS ? 4 : 1];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = row0 + id + 64 * i;
+            f[i] = r < at.rows ? load_quad(as + int64_t(r) * p.groups, s, p.groups, p.scale_vec) : zero;
+          }
+          if constexpr (COLS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t n = n0 + id + 64 * i;
+              g[i] = n < p.N ? load_quad(bs + int64_t(n) * p.groups, s, p.groups, p.scale_vec) : zero;
+            }
+          } else {
+            g[0] = id < 2 && n0 + 128 * id < p.N
+                       ? load_quad(bs + int64_t(at.n * 2 + id) * p.groups, s, p.groups, p.scale_vec)
+                       : zero;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) st_shared_v4(dst + (id + 64 * i) * 16, f[i]);
+          if constexpr (COLS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t c = cols + (id + 64 * i) * 4;
+              st_shared(c, g[i].x);
+              st_shared(c + 1024, g[i].y);
+              st_shared(c + 2048, g[i].z);
+              st_shared(c + 3072, g[i].w);
+            }
+          } else if (id < 2) {
+            st_shared_v4(cols + id * 16, g[0]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull0 + 8 * slot);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- sums: half a row of the tile a thread ----
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t buf_out = outs + uint32_t(warp - 4) * kOutBytes;
+    uint32_t it = 0, sit = 0;
+    for (int32_t t = first; t < tiles && !failed; t += step) {
+      const At at = tile(t, e);
+      float2 v[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) v[j] = make_float2(0.f, 0.f);
+      for (int32_t s = 0; s < p.groups; s += kQuad, ++sit) {
+        const uint32_t slot = sit % kSlots, src_s = slots + slot * kSlotBytes, cols = src_s + 128 * 16;
+        bool ok = wait(sfull0 + 8 * slot, (sit / kSlots) & 1u);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        const float4 aq = ld_shared_v4(src_s + (quarter * 32 + lane) * 16);
+        const float4 bq = COLS ? make_float4(1.f, 1.f, 1.f, 1.f) : ld_shared_v4(cols + half * 16);
+        const float as[4] = {aq.x * bq.x, aq.y * bq.y, aq.z * bq.z, aq.w * bq.w};
+#pragma unroll
+        for (int qi = 0; qi < kQuad; ++qi) {
+          if (s + qi >= p.groups) break;
+          const uint32_t buf = it & 1u;
+          ok = wait(done0 + 8 * buf, (it >> 1) & 1u);
+          if (!__all_sync(0xffffffffu, ok)) {
+            failed = true;
+            break;
+          }
+          ++it;
+          tcgen05_fence_after();
+          const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + buf * 256 + uint32_t(half * kCols);
+          const float2 sc = make_float2(as[qi], as[qi]);
+          float x[2][32];  // a load is under way while the one before it is added
+          tmem_load_16(src, x[0]);
+          tmem_load_16(src + 16, x[0] + 16);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            float* now = x[(c / 32) & 1];
+            float* next = x[(c / 32 + 1) & 1];
+            tmem_load_wait(now);
+            tmem_load_wait(now + 16);
+            if (c + 32 < kCols) {
+              tmem_load_16(src + uint32_t(c + 32), next);
+              tmem_load_16(src + uint32_t(c + 48), next + 16);
+            } else {
+              tcgen05_fence_before();
+              __syncwarp();  // all lanes have read their sums
+              if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * buf, 0));
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              float2 lo = make_float2(now[j], now[j + 1]), hi = make_float2(now[j + 2], now[j + 3]);
+              if constexpr (COLS) {
+                const float4 bs = ld_shared_v4(cols + uint32_t(qi * 1024 + (half * kCols + c + j) * 4));
+                lo = mul2(lo, make_float2(bs.x, bs.y));
+                hi = mul2(hi, make_float2(bs.z, bs.w));
+              }
+              v[(c + j) / 2] = fma2(lo, sc, v[(c + j) / 2]);
+              v[(c + j) / 2 + 1] = fma2(hi, sc, v[(c + j) / 2 + 1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
+        if (failed) break;
+      }
+      if (failed) break;
+      const int32_t r0 = int32_t(rank) * 128 + quarter * 32, j0 = at.n * 256 + half * kCols;
+      const int rows_left = at.rows - r0, width = int(min(kCols, p.N - j0));  // this warp's part of y, may be <= 0
+      if (width <= 0 || rows_left <= 0) continue;
+      T* out = static_cast<T*>(p.y) + int64_t(at.row0 + r0) * p.N + j0;
+      constexpr int E = Vec16<T>::kElems;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 8 * E) {
+        if (c >= width) break;
+        uint4 u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float f[E];
+#pragma unroll
+          for (int j = 0; j < E; j += 2) f[j] = v[(c + E * k + j) / 2].x, f[j + 1] = v[(c + E * k + j) / 2].y;
+          u[k] = Vec16<T>::pack(f);
+        }
+        if (p.y_vec) {
+          rows_out(buf_out, lane, u, [&](int, int r, int unit, const uint4& x) {
+            const int col = c + unit * E;
+            if (r < rows_left && col < width) *reinterpret_cast<uint4*>(out + int64_t(r) * p.N + col) = x;
+          });
+        } else {  // rows that start off 16 bytes, or end inside a vector
+          elements_out<T>(buf_out, lane, u, [&](int r, int k, T x) {
+            if (r < rows_left && c + k < width) out[int64_t(r) * p.N + c + k] = x;
+          });
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (__syncthreads_or(failed)) {
+    // As above: what is under way lands before this CTA's memory goes to another.
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  tcgen05_fence_before();
+  cluster_sync_all();
+  tcgen05_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tmem, kColumns);
 }
 
 // Rows of `cols` bytes that start anywhere, to rows of `ld` bytes (a multiple of

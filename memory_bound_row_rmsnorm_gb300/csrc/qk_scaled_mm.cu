@@ -60,15 +60,20 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Once a device and kernel: its shared memory.
+// Once a device and kernel: its shared memory, and whether the launch holds the
+// registers that its warps share out (a build that held less would wait for the
+// rest forever).
 template <typename K>
-qk_status prepare(std::atomic<uint64_t>& prepared, const CurrentDevice& d, K kernel, int smem) {
+qk_status prepare(std::atomic<uint64_t>& prepared, const CurrentDevice& d, K kernel, int smem, int registers) {
   const uint64_t bit = uint64_t(1) << (d.index & 63);
   if (prepared.load(std::memory_order_acquire) & bit) return QK_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  cudaFuncAttributes fa;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
     cudaGetLastError();
     return QK_ERR_LAUNCH;
   }
+  if (fa.numRegs * kScaledThreads < registers) return QK_ERR_LAUNCH;
   prepared.fetch_or(bit, std::memory_order_acq_rel);
   return QK_OK;
 }
@@ -97,16 +102,42 @@ ScaledArgs arguments(const Call& c) {
   return p;
 }
 
+template <typename K>
+qk_status launch(const Call& c, K kernel, const CUtensorMap& ma, const CUtensorMap& mb, const ScaledArgs& p,
+                 int64_t grid, int cluster, int smem) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(kScaledThreads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = static_cast<cudaStream_t>(c.stream);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, p) != cudaSuccess) {
+    cudaGetLastError();
+    return QK_ERR_LAUNCH;
+  }
+  return QK_OK;
+}
+
+constexpr int64_t kMostTiles = int64_t(1) << 30;  // tile numbers are 32-bit
+
 template <int TN, typename T>
 qk_status launch_tiles(const Call& c) {
   const auto kernel = scaled_tile_kernel<TN, T>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
-  const qk_status st = prepare(prepared, c.dev, kernel, tile_smem(TN));
+  const qk_status st = prepare(prepared, c.dev, kernel, tile_smem(TN), 0);
   if (st != QK_OK) return st;
   ScaledArgs p = arguments(c);
-  p.lane_tiles = int32_t(ceil_div(c.N, 128));
-  const int64_t tiles = most_tiles(c, TN) * p.lane_tiles;
-  if (tiles > (1 << 30)) return QK_ERR_UNSUPPORTED;
+  p.n_tiles = int32_t(ceil_div(c.N, 128));
+  const int64_t tiles = most_tiles(c, TN) * p.n_tiles;
+  if (tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
   // Where the tiles leave SMs idle, a cluster shares a tile's k.
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= c.dev.sms && p.groups >= ranks * 2) ranks *= 2;
@@ -114,25 +145,28 @@ qk_status launch_tiles(const Call& c) {
   CUtensorMap ma, mb;
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, TN) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
     return QK_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(unsigned(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, c.dev.sms)), 1, 1);
-  cfg.blockDim = dim3(kScaledThreads, 1, 1);
-  cfg.dynamicSmemBytes = tile_smem(TN);
-  cfg.stream = static_cast<cudaStream_t>(c.stream);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(ranks);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ranks > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, p) != cudaSuccess) {
-    cudaGetLastError();
+  return launch(c, kernel, ma, mb, p, ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, c.dev.sms), ranks,
+                tile_smem(TN));
+}
+
+template <bool COLS, typename T>
+qk_status launch_pairs(const Call& c) {
+  const auto kernel = scaled_pair_kernel<COLS, T>;
+  static std::atomic<uint64_t> prepared{0};  // one bit a device
+  const qk_status st = prepare(prepared, c.dev, kernel, pair_smem(COLS), kSplitRegistersPair);
+  if (st != QK_OK) return st;
+  ScaledArgs p = arguments(c);
+  p.n_tiles = int32_t(ceil_div(c.N, 256));
+  // The last column tile as a product of the columns it has: halves of whole 8-row groups of b.
+  p.last_n = int32_t(std::min<int64_t>(256, round_up(c.N - int64_t(p.n_tiles - 1) * 256, 32)));
+  p.n_full = p.last_n == 256 ? p.n_tiles : p.n_tiles - 1;
+  p.y_vec = c.N * int64_t(sizeof(T)) % 16 == 0 && aligned16(c.y);
+  const int64_t tiles = most_tiles(c, 256) * p.n_tiles;
+  if (tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
     return QK_ERR_LAUNCH;
-  }
-  return QK_OK;
+  return launch(c, kernel, ma, mb, p, 2 * std::min<int64_t>(tiles, c.dev.sms / 2), 2, pair_smem(COLS));
 }
 
 // Rows of a and b as TMA reads them, by way of the workspace where K is not a multiple of 16.
@@ -161,7 +195,8 @@ qk_status product(const Call& c) {
   if (mean <= 16) return launch_tiles<16, T>(c);
   if (mean <= 32) return launch_tiles<32, T>(c);
   if (mean <= 64) return launch_tiles<64, T>(c);
-  return launch_tiles<128, T>(c);
+  if (mean <= 256) return launch_tiles<128, T>(c);
+  return c.b_rows == 1 ? launch_pairs<true, T>(c) : launch_pairs<false, T>(c);
 }
 
 }  // namespace
