@@ -365,45 +365,47 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
 // so a thread multiplies with one scale of a and, where b's scales are of blocks
 // (!COLS), one of b: a block's sums cost a fused multiply-add each.
 // ---------------------------------------------------------------------------
-constexpr int kPairStages = 5, kPairStageBytes = 2 * 128 * kScaledStepK;  // one CTA's 128 rows of a and of b
+constexpr int kPairStages = 4, kPairStageBytes = 2 * 128 * kScaledStepK;  // one CTA's 128 rows of a and of b
 constexpr int kPairScaleSlots = 2;
-constexpr int kSplitRegistersPair = 128 * 80 + 256 * 208;  // what the warps' shares add up to
+constexpr int kPairSums = 8, kPairThreads = 128 + 32 * kPairSums;  // warps that keep sums
+constexpr int kPairOut = 2;  // pieces of 32 rows x 128 bytes that a warp may have on their way out
+constexpr int kSplitRegistersPair = 128 * 80 + 32 * kPairSums * 208;  // what the warps' shares add up to
 __host__ __device__ constexpr int pair_slot_bytes(bool cols) { return 128 * 16 + (cols ? 256 * 16 : 128); }
 __host__ __device__ constexpr int pair_smem(bool cols) {  // and room to start on 1024 bytes
-  return kPairStages * kPairStageBytes + 8 * kOutBytes + kPairScaleSlots * pair_slot_bytes(cols) + 1024;
+  return kPairStages * kPairStageBytes + kPairSums * kPairOut * kOutBytes + kPairScaleSlots * pair_slot_bytes(cols) + 1024;
 }
 
 template <bool COLS, typename T>
-__global__ void __launch_bounds__(kScaledThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const ScaledArgs p) {
+                       const __grid_constant__ CUtensorMap map_y, const ScaledArgs p) {
   constexpr int kStages = kPairStages, kStageBytes = kPairStageBytes, kSlots = kPairScaleSlots;
   constexpr int kSlotBytes = pair_slot_bytes(COLS), kCols = 128;
   constexpr uint32_t kColumns = 512;  // TMEM: two sets of sums
   extern __shared__ unsigned char dynamic_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 + 2 * kSlots];
   __shared__ uint32_t tmem_at;
   __shared__ ExpertTable table;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kStages, done0 = full0 + 16 * kStages,
-                 free0 = done0 + 16, sfull0 = free0 + 16, sempty0 = sfull0 + 8 * kSlots;
+  const uint32_t full0 = smem_addr(bars), done0 = full0 + 8 * kStages, free0 = done0 + 8 * kStages,
+                 sfull0 = free0 + 16, sempty0 = sfull0 + 8 * kSlots;
   const uint32_t ring = (smem_addr(dynamic_smem) + 1023u) & ~1023u;  // the same in both CTAs
-  const uint32_t outs = ring + uint32_t(kStages * kStageBytes), slots = outs + 8 * kOutBytes;
+  const uint32_t outs = ring + uint32_t(kStages * kStageBytes), slots = outs + kPairSums * kPairOut * kOutBytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);   // the leader's producer, and the bytes of both CTAs
-      mbar_init(empty0 + 8 * s, 1);  // a commit of the leader's products
+      mbar_init(full0 + 8 * s, 1);  // the leader's producer, and the bytes of both CTAs
+      // A commit: the block is summed, and the stage may be filled again.  One for both: the
+      // thread that issues products is what a step of few waits for (460 -> 435 us at
+      // 16384 x 8192 x 4096 with a whole warp in its loop, and less with one commit).
+      mbar_init(done0 + 8 * s, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(done0 + 8 * i, 1);   // a commit: the block is summed
-      mbar_init(free0 + 8 * i, 16);  // the epilogue warps of both CTAs have read it
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(free0 + 8 * i, 2 * kPairSums);  // the epilogue warps of both CTAs have read the sums
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(sfull0 + 8 * i, 2);  // this CTA's own scales
-      mbar_init(sempty0 + 8 * i, 8);
+      mbar_init(sempty0 + 8 * i, kPairSums);
     }
     fence_mbar_init();
     prefetch_tensor_map(&map_a);
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
     return false;
   };
 
-  // Registers: the launch holds 384 x 168 = 64512 (the host checks it); 128 x 80
-  // + 256 x 208 = 63488 of them go to the warps that feed and to those that keep sums.
+  // Registers: the launch holds 384 x 168 = 64512 (the host checks it); 128 x 80 +
+  // 256 x 208 of them go to the warps that feed and to those that keep sums.
   int32_t e = 0;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
         const int32_t a0 = at.row0 + int32_t(rank) * 128,
                       b0 = at.n * 256 + int32_t(rank) * (at.n < p.n_full ? 128 : p.last_n / 2);
         for (int32_t s = 0; s < p.groups; ++s, ++q) {
-          if (!wait(empty0 + 8 * st, turn ^ 1u)) break;
+          if (!wait(done0 + 8 * st, turn ^ 1u)) break;
           const uint32_t bar = map_to_rank(full0 + 8 * st, 0), dst = ring + uint32_t(st) * kStageBytes;
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, 2 * kStageBytes);
           tma_load_3d(dst, &map_a, s * kScaledStepK, a0, 0, bar);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
       if (failed && rank == 0)  // leave once the loads in flight have landed: the leader's barriers count both CTAs'
         for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
           mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // ---- products of both CTAs ----
       int st = 0;
       uint32_t turn = 0, it = 0;
@@ -486,16 +488,21 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
         const uint32_t idesc = instruction_desc_e4m3(256, at.n < p.n_full ? 256u : uint32_t(p.last_n));
         for (int32_t s = 0; s < p.groups; ++s, ++it) {
           const uint32_t buf = it & 1u;
-          if (!wait(free0 + 8 * buf, ((it >> 1) & 1u) ^ 1u)) break;
-          if (!wait(full0 + 8 * st, turn)) break;
+          const bool ok = wait(free0 + 8 * buf, ((it >> 1) & 1u) ^ 1u) && wait(full0 + 8 * st, turn);
+          if (!__all_sync(0xffffffffu, ok)) {
+            failed = true;
+            break;
+          }
           tcgen05_fence_after();
-          const uint32_t sa = ring + uint32_t(st) * kStageBytes;
-          const uint64_t da = operand_desc(sa, 0), db = operand_desc(sa + kStageBytes / 2, 0);
+          if (elect_one()) {
+            const uint32_t sa = ring + uint32_t(st) * kStageBytes;
+            const uint64_t da = operand_desc(sa, 0), db = operand_desc(sa + kStageBytes / 2, 0);
 #pragma unroll
-          for (int k = 0; k < kScaledStepK / 32; ++k)
-            mma_e4m3_pair(tmem + buf * 256, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, k > 0);
-          mma_commit_pair(empty0 + 8 * st);
-          mma_commit_pair(done0 + 8 * buf);
+            for (int k = 0; k < kScaledStepK / 32; ++k)
+              mma_e4m3_pair(tmem + buf * 256, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, k > 0);
+            mma_commit_pair(done0 + 8 * st);
+          }
+          __syncwarp();
           if (++st == kStages) st = 0, turn ^= 1u;
         }
       }
@@ -557,13 +564,13 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- sums: half a row of the tile a thread ----
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t buf_out = outs + uint32_t(warp - 4) * kOutBytes;
-    uint32_t it = 0, sit = 0;
+    const uint32_t out_bufs = outs + uint32_t(warp - 4) * (kPairOut * kOutBytes);
+    uint32_t it = 0, sit = 0, piece = 0;
     for (int32_t t = first; t < tiles && !failed; t += step) {
       const At at = tile(t, e);
-      float2 v[kCols / 2];
+      float v[kCols];
 #pragma unroll
-      for (int j = 0; j < kCols / 2; ++j) v[j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < kCols; ++j) v[j] = 0.f;
       for (int32_t s = 0; s < p.groups; s += kQuad, ++sit) {
         const uint32_t slot = sit % kSlots, src_s = slots + slot * kSlotBytes, cols = src_s + 128 * 16;
         bool ok = wait(sfull0 + 8 * slot, (sit / kSlots) & 1u);
@@ -574,47 +581,59 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
         const float4 aq = ld_shared_v4(src_s + (quarter * 32 + lane) * 16);
         const float4 bq = COLS ? make_float4(1.f, 1.f, 1.f, 1.f) : ld_shared_v4(cols + half * 16);
         const float as[4] = {aq.x * bq.x, aq.y * bq.y, aq.z * bq.z, aq.w * bq.w};
-#pragma unroll
-        for (int qi = 0; qi < kQuad; ++qi) {
-          if (s + qi >= p.groups) break;
-          const uint32_t buf = it & 1u;
-          ok = wait(done0 + 8 * buf, (it >> 1) & 1u);
-          if (!__all_sync(0xffffffffu, ok)) {
+        // Loads wait for each other, so 64 columns are asked for at a time, the second
+        // 64 as the first are added: two trips to TMEM a block.  (16384 x 8192 x 4096: four
+        // trips of 32 columns with the next always under way 480 us; 16 warps with four trips
+        // of 16 each 500.  Single additions: packed pairs of them take 5 us more.)
+        float x[64];
+        uint32_t src = 0;
+        auto summed = [&] {  // waits for the next block's sums
+          const bool there = wait(done0 + 8 * (it % kStages), (it / kStages) & 1u);
+          if (!__all_sync(0xffffffffu, there)) {
             failed = true;
-            break;
+            return false;
           }
-          ++it;
           tcgen05_fence_after();
-          const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + buf * 256 + uint32_t(half * kCols);
-          const float2 sc = make_float2(as[qi], as[qi]);
-          float x[2][32];  // a load is under way while the one before it is added
-          tmem_load_16(src, x[0]);
-          tmem_load_16(src + 16, x[0] + 16);
+          src = tmem + (uint32_t(quarter * 32) << 16) + (it & 1u) * 256 + uint32_t(half * kCols);
+          return true;
+        };
+        auto load = [&](int to, int c) {
+          tmem_load_16(src + uint32_t(c), x + to);
+          tmem_load_16(src + uint32_t(c + 16), x + to + 16);
+        };
+        auto add = [&](int qi, int from, int c) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            float* now = x[(c / 32) & 1];
-            float* next = x[(c / 32 + 1) & 1];
-            tmem_load_wait(now);
-            tmem_load_wait(now + 16);
-            if (c + 32 < kCols) {
-              tmem_load_16(src + uint32_t(c + 32), next);
-              tmem_load_16(src + uint32_t(c + 48), next + 16);
-            } else {
-              tcgen05_fence_before();
-              __syncwarp();  // all lanes have read their sums
-              if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * buf, 0));
+          for (int j = 0; j < 32; j += 4) {
+            float f[4] = {x[from + j], x[from + j + 1], x[from + j + 2], x[from + j + 3]};
+            if constexpr (COLS) {
+              const float4 bs = ld_shared_v4(cols + uint32_t(qi * 1024 + (half * kCols + c + j) * 4));
+              f[0] *= bs.x, f[1] *= bs.y, f[2] *= bs.z, f[3] *= bs.w;
             }
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float2 lo = make_float2(now[j], now[j + 1]), hi = make_float2(now[j + 2], now[j + 3]);
-              if constexpr (COLS) {
-                const float4 bs = ld_shared_v4(cols + uint32_t(qi * 1024 + (half * kCols + c + j) * 4));
-                lo = mul2(lo, make_float2(bs.x, bs.y));
-                hi = mul2(hi, make_float2(bs.z, bs.w));
-              }
-              v[(c + j) / 2] = fma2(lo, sc, v[(c + j) / 2]);
-              v[(c + j) / 2 + 1] = fma2(hi, sc, v[(c + j) / 2 + 1]);
-            }
+            for (int i = 0; i < 4; ++i) v[c + j + i] = fmaf(f[i], as[qi], v[c + j + i]);
+          }
+        };
+        if (summed()) {
+          load(0, 0);
+          load(32, 32);
+#pragma unroll
+          for (int qi = 0; qi < kQuad; ++qi) {
+            const uint32_t buf = it & 1u;
+            tmem_load_wait_64(x);
+            add(qi, 0, 0);
+            load(0, 64);
+            add(qi, 32, 32);
+            load(32, 96);
+            tmem_load_wait_64(x);
+            tcgen05_fence_before();
+            __syncwarp();  // all lanes have read their sums
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * buf, 0));
+            ++it;
+            add(qi, 0, 64);
+            add(qi, 32, 96);
+            if (qi + 1 == kQuad || s + qi + 1 >= p.groups || !summed()) break;
+            load(0, 0);
+            load(32, 32);
           }
         }
         __syncwarp();
@@ -632,13 +651,23 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
         if (c >= width) break;
         uint4 u[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float f[E];
+        for (int k = 0; k < 8; ++k) u[k] = Vec16<T>::pack(v + c + E * k);
+        // The copy from this buffer, all but one ago, has left it.
+        const uint32_t buf_out = out_bufs + (piece++ % kPairOut) * kOutBytes;
+        if (lane == 0) bulk_wait_read<kPairOut - 1>();
+        __syncwarp();
+        if (p.y_vec && rows_left >= 32) {
+          // By TMA, from rows of 128 bytes in its swizzle: the warp goes on to the next
+          // tile's sums while the stores of all CTAs, which come at one time, drain.
 #pragma unroll
-          for (int j = 0; j < E; j += 2) f[j] = v[(c + E * k + j) / 2].x, f[j + 1] = v[(c + E * k + j) / 2].y;
-          u[k] = Vec16<T>::pack(f);
-        }
-        if (p.y_vec) {
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(buf_out + lane * 128 + ((k ^ (lane & 7)) * 16),
+                         make_float4(__uint_as_float(u[k].x), __uint_as_float(u[k].y), __uint_as_float(u[k].z),
+                                     __uint_as_float(u[k].w)));
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&map_y, j0 + c, at.row0 + r0, buf_out);
+        } else if (p.y_vec) {
           rows_out(buf_out, lane, u, [&](int, int r, int unit, const uint4& x) {
             const int col = c + unit * E;
             if (r < rows_left && col < width) *reinterpret_cast<uint4*>(out + int64_t(r) * p.N + col) = x;
@@ -648,8 +677,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
             if (r < rows_left && c + k < width) out[int64_t(r) * p.N + c + k] = x;
           });
         }
+        if (lane == 0) bulk_commit();  // of nothing, maybe: buffers and groups take turns alike
       }
     }
+    if (lane == 0) bulk_wait();
   }
   __syncwarp();
   if (__syncthreads_or(failed)) {

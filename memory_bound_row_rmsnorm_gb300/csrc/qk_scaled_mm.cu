@@ -60,11 +60,24 @@ bool make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y in boxes of 32 rows of 128 bytes, for stores.
+bool make_out_map(CUtensorMap* map, const Call& c, int es) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(c.N), cuuint64_t(c.M)};
+  const cuuint64_t strides[1] = {cuuint64_t(c.N) * cuuint64_t(es)};
+  const cuuint32_t box[2] = {cuuint32_t(128 / es), 32}, steps[2] = {1, 1};
+  return encode(map, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.y, dims,
+                strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Once a device and kernel: its shared memory, and whether the launch holds the
 // registers that its warps share out (a build that held less would wait for the
 // rest forever).
 template <typename K>
-qk_status prepare(std::atomic<uint64_t>& prepared, const CurrentDevice& d, K kernel, int smem, int registers) {
+qk_status prepare(std::atomic<uint64_t>& prepared, const CurrentDevice& d, K kernel, int smem, int threads = 0,
+                  int registers = 0) {
   const uint64_t bit = uint64_t(1) << (d.index & 63);
   if (prepared.load(std::memory_order_acquire) & bit) return QK_OK;
   cudaFuncAttributes fa;
@@ -73,7 +86,7 @@ qk_status prepare(std::atomic<uint64_t>& prepared, const CurrentDevice& d, K ker
     cudaGetLastError();
     return QK_ERR_LAUNCH;
   }
-  if (fa.numRegs * kScaledThreads < registers) return QK_ERR_LAUNCH;
+  if (fa.numRegs * threads < registers) return QK_ERR_LAUNCH;
   prepared.fetch_or(bit, std::memory_order_acq_rel);
   return QK_OK;
 }
@@ -102,13 +115,12 @@ ScaledArgs arguments(const Call& c) {
   return p;
 }
 
-template <typename K>
-qk_status launch(const Call& c, K kernel, const CUtensorMap& ma, const CUtensorMap& mb, const ScaledArgs& p,
-                 int64_t grid, int cluster, int smem) {
+template <typename K, typename... A>
+qk_status launch(const Call& c, K kernel, int64_t grid, int threads, int cluster, int smem, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(unsigned(grid), 1, 1);
-  cfg.blockDim = dim3(kScaledThreads, 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = static_cast<cudaStream_t>(c.stream);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -119,7 +131,7 @@ qk_status launch(const Call& c, K kernel, const CUtensorMap& ma, const CUtensorM
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return QK_ERR_LAUNCH;
   }
@@ -132,7 +144,7 @@ template <int TN, typename T>
 qk_status launch_tiles(const Call& c) {
   const auto kernel = scaled_tile_kernel<TN, T>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
-  const qk_status st = prepare(prepared, c.dev, kernel, tile_smem(TN), 0);
+  const qk_status st = prepare(prepared, c.dev, kernel, tile_smem(TN));
   if (st != QK_OK) return st;
   ScaledArgs p = arguments(c);
   p.n_tiles = int32_t(ceil_div(c.N, 128));
@@ -145,15 +157,15 @@ qk_status launch_tiles(const Call& c) {
   CUtensorMap ma, mb;
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, TN) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
     return QK_ERR_LAUNCH;
-  return launch(c, kernel, ma, mb, p, ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, c.dev.sms), ranks,
-                tile_smem(TN));
+  return launch(c, kernel, ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, c.dev.sms), kScaledThreads, ranks,
+                tile_smem(TN), ma, mb, p);
 }
 
 template <bool COLS, typename T>
 qk_status launch_pairs(const Call& c) {
   const auto kernel = scaled_pair_kernel<COLS, T>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
-  const qk_status st = prepare(prepared, c.dev, kernel, pair_smem(COLS), kSplitRegistersPair);
+  const qk_status st = prepare(prepared, c.dev, kernel, pair_smem(COLS), kPairThreads, kSplitRegistersPair);
   if (st != QK_OK) return st;
   ScaledArgs p = arguments(c);
   p.n_tiles = int32_t(ceil_div(c.N, 256));
@@ -163,10 +175,11 @@ qk_status launch_pairs(const Call& c) {
   p.y_vec = c.N * int64_t(sizeof(T)) % 16 == 0 && aligned16(c.y);
   const int64_t tiles = most_tiles(c, 256) * p.n_tiles;
   if (tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
+  CUtensorMap ma, mb, my = {};
+  if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128) ||
+      (p.y_vec && !make_out_map(&my, c, int(sizeof(T)))))
     return QK_ERR_LAUNCH;
-  return launch(c, kernel, ma, mb, p, 2 * std::min<int64_t>(tiles, c.dev.sms / 2), 2, pair_smem(COLS));
+  return launch(c, kernel, 2 * std::min<int64_t>(tiles, c.dev.sms / 2), kPairThreads, 2, pair_smem(COLS), ma, mb, my, p);
 }
 
 // Rows of a and b as TMA reads them, by way of the workspace where K is not a multiple of 16.
