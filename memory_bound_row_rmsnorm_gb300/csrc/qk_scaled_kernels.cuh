@@ -300,11 +300,10 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
             const float4 as = ld_shared_v4(sa + c * 4);
-            // (sum a_scale) b_scale + running sum
-            v[c] = fmaf(x[c] * as.x, bs[qi], v[c]);
-            v[c + 1] = fmaf(x[c + 1] * as.y, bs[qi], v[c + 1]);
-            v[c + 2] = fmaf(x[c + 2] * as.z, bs[qi], v[c + 2]);
-            v[c + 3] = fmaf(x[c + 3] * as.w, bs[qi], v[c + 3]);
+            v[c] = fmaf(x[c], as.x * bs[qi], v[c]);
+            v[c + 1] = fmaf(x[c + 1], as.y * bs[qi], v[c + 1]);
+            v[c + 2] = fmaf(x[c + 2], as.z * bs[qi], v[c + 2]);
+            v[c + 3] = fmaf(x[c + 3], as.w * bs[qi], v[c + 3]);
           }
         }
         __syncwarp();
@@ -578,14 +577,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           failed = true;
           break;
         }
-        const float4 aq = ld_shared_v4(src_s + (quarter * 32 + lane) * 16);
-        const float4 bq = COLS ? make_float4(1.f, 1.f, 1.f, 1.f) : ld_shared_v4(cols + half * 16);
-        const float as[4] = {aq.x * bq.x, aq.y * bq.y, aq.z * bq.z, aq.w * bq.w};
+        const uint32_t own = src_s + (quarter * 32 + lane) * 16;
         // Loads wait for each other, so 64 columns are asked for at a time, the second
         // 64 as the first are added: two trips to TMEM a block.  (16384 x 8192 x 4096: four
         // trips of 32 columns with the next always under way 480 us; 16 warps with four trips
         // of 16 each 500.  Single additions: packed pairs of them take 5 us more.)
-        float x[64];
+        float x[COLS ? 32 : 64];
         uint32_t src = 0;
         auto summed = [&] {  // waits for the next block's sums
           const bool there = wait(done0 + 8 * (it % kStages), (it / kStages) & 1u);
@@ -601,39 +598,58 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tmem_load_16(src + uint32_t(c), x + to);
           tmem_load_16(src + uint32_t(c + 16), x + to + 16);
         };
-        auto add = [&](int qi, int from, int c) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float f[4] = {x[from + j], x[from + j + 1], x[from + j + 2], x[from + j + 3]};
-            if constexpr (COLS) {
-              const float4 bs = ld_shared_v4(cols + uint32_t(qi * 1024 + (half * kCols + c + j) * 4));
-              f[0] *= bs.x, f[1] *= bs.y, f[2] *= bs.z, f[3] *= bs.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[c + j + i] = fmaf(f[i], as[qi], v[c + j + i]);
-          }
+        auto read = [&] {  // all lanes have read their sums
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * (it & 1u), 0));
+          ++it;
         };
-        if (summed()) {
-          load(0, 0);
-          load(32, 32);
+        auto add = [&](float scale, int from, int c) {  // 32 columns
 #pragma unroll
-          for (int qi = 0; qi < kQuad; ++qi) {
-            const uint32_t buf = it & 1u;
-            tmem_load_wait_64(x);
-            add(qi, 0, 0);
-            load(0, 64);
-            add(qi, 32, 32);
-            load(32, 96);
-            tmem_load_wait_64(x);
-            tcgen05_fence_before();
-            __syncwarp();  // all lanes have read their sums
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(free0 + 8 * buf, 0));
-            ++it;
-            add(qi, 0, 64);
-            add(qi, 32, 96);
-            if (qi + 1 == kQuad || s + qi + 1 >= p.groups || !summed()) break;
+          for (int j = 0; j < 32; ++j) v[c + j] = fmaf(x[from + j], scale, v[c + j]);
+        };
+#pragma unroll 1
+        for (int qi = 0; qi < kQuad; ++qi) {
+          if (s + qi >= p.groups || !summed()) break;
+          if constexpr (COLS) {
+            const float scale = ld_shared(own + qi * 4);
+            // 32 columns at a time, and their scales: what is left of the registers.
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) {
+              const uint32_t at_c = cols + uint32_t(qi * 1024 + (half * kCols + c) * 4);
+              float4 bs[4];
+              load(0, c);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) bs[j] = ld_shared_v4(at_c + 16 * j);
+              tmem_load_wait_32(x);
+              if (c + 32 == kCols) read();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float* f = x + 16 * k + 4 * j;
+                  float* o = v + c + 16 * k + 4 * j;
+                  o[0] = fmaf(f[0], bs[j].x * scale, o[0]);
+                  o[1] = fmaf(f[1], bs[j].y * scale, o[1]);
+                  o[2] = fmaf(f[2], bs[j].z * scale, o[2]);
+                  o[3] = fmaf(f[3], bs[j].w * scale, o[3]);
+                  if (k == 0) bs[j] = ld_shared_v4(at_c + 64 + 16 * j);
+                }
+              }
+            }
+          } else {
+            const float scale = ld_shared(own + qi * 4) * ld_shared(cols + half * 16 + qi * 4);
             load(0, 0);
             load(32, 32);
+            tmem_load_wait_64(x);
+            add(scale, 0, 0);
+            load(0, 64);
+            add(scale, 32, 32);
+            load(32, 96);
+            tmem_load_wait_64(x);
+            read();
+            add(scale, 0, 64);
+            add(scale, 32, 96);
           }
         }
         __syncwarp();
