@@ -195,16 +195,15 @@ struct CombineArgs {
   int32_t k;
 };
 
-// E values from p, of which `left` count.
+// A vector of values from p, of which `left` count.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_values(const T* p, int64_t left, float* f) {
+__device__ __forceinline__ uint4 load_raw(const T* p, int64_t left) {
   using V = Vec16<T>;
-  if constexpr (VEC) {
-    V::unpack(*reinterpret_cast<const uint4*>(p), f);
-  } else {
+  if constexpr (VEC) return *reinterpret_cast<const uint4*>(p);
+  float f[V::kElems];
 #pragma unroll
-    for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
-  }
+  for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
+  return V::pack(f);  // exact: the values are T's
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_values(T* p, int64_t left, const float* f) {
@@ -218,6 +217,8 @@ __device__ __forceinline__ void store_values(T* p, int64_t left, const float* f)
   }
 }
 
+constexpr int kAtOnce = 4;  // choices whose rows are loaded together
+
 // A warp forms a piece of a token's row; the sum runs over the choices in order.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
@@ -230,58 +231,95 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
     const int64_t t = u / a.pieces, c = ((u - t * a.pieces) * 32 + lane) * E;
     if (c >= a.N) continue;
     float sum[E] = {};
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t at = a.slot[t * a.k + j];
-      if (at < 0 || at >= a.P) continue;
-      const float w = a.weights != nullptr ? a.weights[t * a.k + j] : 1.f;
-      float f[E];
-      load_values<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at) * a.N + c, a.N - c, f);
+    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+      int32_t at[kAtOnce];
+      float w[kAtOnce];
+      uint4 f[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < E; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+      for (int j = 0; j < kAtOnce; ++j) {
+        at[j] = j0 + j < a.k ? a.slot[t * a.k + j0 + j] : -1;
+        if (at[j] >= a.P) at[j] = -1;
+        w[j] = a.weights != nullptr && at[j] >= 0 ? a.weights[t * a.k + j0 + j] : 1.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (at[j] >= 0) f[j] = load_raw<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N + c, a.N - c);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (at[j] < 0) continue;
+        float v[E];
+        Vec16<T>::unpack(f[j], v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
+      }
     }
     store_values<T, VEC>(static_cast<T*>(a.out) + t * a.N + c, a.N - c, sum);
   }
 }
 
-// A CTA takes a token: its choices one after the other, dy again from L1 or L2.
-template <typename T, bool VEC>
+// THREADS threads take a token, kAtOnce choices at a time: dy and their rows are
+// read together, drows leave at once, and each choice's products are summed over
+// the threads at the end.
+template <typename T, bool VEC, int THREADS>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs a) {
-  constexpr int E = Vec16<T>::kElems;
-  __shared__ float red[8];
+  constexpr int E = Vec16<T>::kElems, kWarps = THREADS / 32, kTokens = 256 / THREADS;
+  __shared__ float red[2][kAtOnce][kWarps];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  const int tid = threadIdx.x % THREADS, warp = tid >> 5, lane = threadIdx.x & 31;
+  int turn = 0;
+  for (int64_t t = int64_t(blockIdx.x) * kTokens + threadIdx.x / THREADS; t < a.T; t += int64_t(gridDim.x) * kTokens) {
     const T* dy = static_cast<const T*>(a.dy) + t * a.N;
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t at = a.slot[t * a.k + j];
-      const bool there = at >= 0 && at < a.P;
-      float dot = 0.f;
-      if (there) {
-        const float w = a.weights[t * a.k + j];
-        const T* row = static_cast<const T*>(a.rows) + int64_t(at) * a.N;
-        T* out = static_cast<T*>(a.out) + int64_t(at) * a.N;
-        for (int64_t c = threadIdx.x * E; c < a.N; c += 256 * E) {
-          float g[E], f[E];
-          load_values<T, VEC>(dy + c, a.N - c, g);
-          load_values<T, VEC>(row + c, a.N - c, f);
+    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+      int32_t at[kAtOnce];
+      float w[kAtOnce], dot[kAtOnce] = {};
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        at[j] = j0 + j < a.k ? a.slot[t * a.k + j0 + j] : -1;
+        if (at[j] >= a.P) at[j] = -1;
+        w[j] = at[j] >= 0 ? a.weights[t * a.k + j0 + j] : 0.f;
+      }
+      for (int64_t c = tid * E; c < a.N; c += THREADS * E) {
+        const uint4 graw = load_raw<T, VEC>(dy + c, a.N - c);
+        uint4 f[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (at[j] >= 0) f[j] = load_raw<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N + c, a.N - c);
+        float g[E];
+        Vec16<T>::unpack(graw, g);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          if (at[j] < 0) continue;
+          float v[E];
+          Vec16<T>::unpack(f[j], v);
 #pragma unroll
           for (int i = 0; i < E; ++i) {
-            dot = fmaf(g[i], f[i], dot);
-            g[i] *= w;
+            dot[j] = fmaf(g[i], v[i], dot[j]);
+            v[i] = g[i] * w[j];
           }
-          store_values<T, VEC>(out + c, a.N - c, g);
+          store_values<T, VEC>(static_cast<T*>(a.out) + int64_t(at[j]) * a.N + c, a.N - c, v);
         }
       }
       if (a.dweights == nullptr) continue;
-      dot = group_sum<32>(dot);
-      __syncthreads();
-      if (lane == 0) red[warp] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int w = 0; w < 8; ++w) s += red[w];
-        a.dweights[t * a.k + j] = there ? s : 0.f;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (j0 + j >= a.k) break;
+        dot[j] = group_sum<32>(dot[j]);
+        if (kWarps > 1 && lane == 0) red[turn][j][warp] = dot[j];
+      }
+      if constexpr (kWarps > 1) {
+        __syncthreads();  // one is enough: the next sums go to the other half
+        if (tid < kAtOnce && j0 + tid < a.k) {
+          float s = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) s += red[turn][tid][i];
+          a.dweights[t * a.k + j0 + tid] = s;
+        }
+        turn ^= 1;
+      } else if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
       }
     }
   }
@@ -322,8 +360,12 @@ template <typename T>
 qk_status launch_combine(const CurrentDevice& d, bool bwd, bool vec, CombineArgs a, void* stream) {
   a.pieces = ceil_div(a.N, 32 * Vec16<T>::kElems);
   if (bwd) {
-    const auto kernel = vec ? combine_bwd_kernel<T, true> : combine_bwd_kernel<T, false>;
-    return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(a.T, int64_t(d.sms) * 32))), 256, 0, stream, a);
+    // A warp a token where a CTA would have less than a vector a thread.
+    const bool narrow = a.N <= 256 * Vec16<T>::kElems / 4;
+    const auto kernel = narrow ? (vec ? combine_bwd_kernel<T, true, 32> : combine_bwd_kernel<T, false, 32>)
+                               : (vec ? combine_bwd_kernel<T, true, 256> : combine_bwd_kernel<T, false, 256>);
+    return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(narrow ? ceil_div(a.T, 8) : a.T, int64_t(d.sms) * 32))), 256, 0,
+                      stream, a);
   }
   const auto kernel = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
   return launch_pdl(kernel, dim3(warps_grid(d, a.T * a.pieces)), 256, 0, stream, a);

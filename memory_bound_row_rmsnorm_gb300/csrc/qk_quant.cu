@@ -14,7 +14,7 @@
 
 #include "../../include/qk.h"
 #include "qk_host.h"
-#include "qk_norm_kernels.cuh"  // EightBits, quotient, quantise2
+#include "qk_norm_kernels.cuh"  // scale_of, quotient, quantise2
 
 namespace qk {
 namespace {
@@ -31,19 +31,61 @@ struct QuantArgs {
   int64_t M, N;
   int64_t col_tiles;
   int32_t block;   // nonzero: a scale a block of 128 x 128
-  int32_t qtype;
   int32_t vec_q, vec_qt;  // rows of q (of qt) are whole 8-byte units
 };
 
-// Bits of |x|, which compare as |x| does, with a NaN above all numbers.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-template <int WIDTH>
-__device__ __forceinline__ uint32_t group_max_bits(uint32_t v) {
-#pragma unroll
-  for (int o = WIDTH / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+// Bits of |x|, which compare as |x| does, with a NaN above all numbers: of four
+// floats, or of bf16 pairs in the halves of a word.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+  return w & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
 }
+template <typename T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) return max(a, b);
+  return __vmaxu2(a, b);
+}
+// The largest of a word's elements, as a float.
+template <typename T>
+__device__ __forceinline__ float widened(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+  return __uint_as_float(max(w & 0xffff0000u, w << 16));
+}
+
+// What the values of one group are divided by: q = (x mul) / den with mul = qmax /
+// 2^k (448 = 7 / 8 2^9, 127 = 127 / 128 2^7) and den = max |x| / 2^k, so that the
+// quotient x qmax / max |x| is formed from exact numbers, not from a rounded scale.
+struct Divisor {
+  float den, inv;
+};
+template <int Q>
+struct EightBitsOf {
+  static constexpr float kMul = Q == QK_E4M3 ? 0.875f : 0.9921875f, kDown = Q == QK_E4M3 ? 0x1p-9f : 0x1p-7f;
+  __device__ __forceinline__ static Divisor divisor(float amax, float* scale) {
+    const bool bad = !(amax < __int_as_float(0x7f800000));
+    *scale = scale_of(amax, bad, Q);
+    const float den = bad ? *scale : fmaxf(amax, kSmallestGroupMax) * kDown;
+    return {den, 1.f / den};
+  }
+  // The quotient, rounded so that rounding it once more to 8 bits gives what the
+  // exact one gives.  bf16: x mul is exact, and a quotient of 11 bits by 8 is a tie or
+  // 2^-13 of itself away from one.  float32: where the rounded quotient is even (a
+  // tie is) and not exact, it moves to the neighbour on the exact one's side.
+  template <typename T>
+  __device__ __forceinline__ static float value(float x, Divisor d) {
+    const float y = x * kMul;
+    const float q = quotient(y, d.den, d.inv);
+    if constexpr (sizeof(T) == 2) return q;
+    const float rest = fmaf(-q, d.den, y) + fmaf(x, kMul, -y);
+    int32_t b = __float_as_int(q);
+    if ((b & 1) == 0 && rest != 0.f && fabsf(q) > 0x1p-24f) b += (rest < 0.f) == (q < 0.f) ? 1 : -1;
+    return __int_as_float(b);
+  }
+  template <typename T>
+  __device__ __forceinline__ static uint32_t two(float a, float b, Divisor d) {
+    return quantise2(value<T>(a, d), value<T>(b, d), Q);
+  }
+};
 
 // One row of `n` (8 or 4) values in 8 bits, from the values as floats.
 template <int E>
@@ -60,17 +102,20 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* words, i
 
 // A thread holds E columns (a 16-byte vector) of R rows that follow each other:
 // 8 x 8 of bf16, 16 x 4 of float32.  A warp has 16 rows of the tile.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kQuantThreads, 2) quant_kernel(const QuantArgs a) {
+template <typename T, int Q, bool VEC>
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_kernel(const QuantArgs a) {
   using V = Vec16<T>;
-  constexpr int E = V::kElems, kLanes = kTile / E, R = 16 * kLanes / 32;
-  __shared__ uint32_t tops[8][kTile];     // largest bits of a warp's rows, by column
+  using B = EightBitsOf<Q>;
+  constexpr int E = V::kElems, kLanes = kTile / E, R = 16 * kLanes / 32;  // R: half of kLanes
+  __shared__ __align__(16) uint4 tops[8][kLanes];   // largest bits of a warp's rows, by column
+  __shared__ uint32_t warp_top[8];
+  __shared__ Divisor columns[kTile];
   __shared__ __align__(16) uint8_t turned[kTile * kTile];
   grid_dependency_wait();
   allow_dependent_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t mt = int64_t(blockIdx.x) / a.col_tiles, nt = int64_t(blockIdx.x) - mt * a.col_tiles;
-  const int64_t i0 = mt * kTile, j0 = nt * kTile;
+  const int64_t i0 = mt * kTile, j0 = nt * kTile, row_tiles = (a.M + kTile - 1) / kTile;
   const int r0 = warp * 16 + (lane / kLanes) * R, c0 = (lane % kLanes) * E;  // this thread's part of the tile
   const int rows = int(min(int64_t(kTile), a.M - i0)), cols = int(min(int64_t(kTile), a.N - j0));
   const T* x = static_cast<const T*>(a.x) + (i0 + r0) * a.N + j0 + c0;
@@ -81,7 +126,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quant_kernel(const QuantArgs
     raw[r] = make_uint4(0, 0, 0, 0);
     if (r0 + r < rows) {
       if constexpr (VEC) {  // N is a multiple of E
-        if (c0 < cols) raw[r] = *reinterpret_cast<const uint4*>(x + r * a.N);
+        if (c0 < cols) raw[r] = __ldcs(reinterpret_cast<const uint4*>(x + r * a.N));
       } else {
         float f[E];
 #pragma unroll
@@ -90,123 +135,132 @@ __global__ void __launch_bounds__(kQuantThreads, 2) quant_kernel(const QuantArgs
       }
     }
   }
-  const EightBits<T> bits(1.f, a.qtype);
-  const int groups = int(a.col_tiles);
 
-  uint32_t row_top[R], col_top[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) col_top[j] = 0;
+  uint32_t row_top[R];
+  uint4 col_top = make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float f[E];
-    V::unpack(raw[r], f);
-    row_top[r] = 0;
+    const uint4 m = make_uint4(magnitudes<T>(raw[r].x), magnitudes<T>(raw[r].y), magnitudes<T>(raw[r].z),
+                               magnitudes<T>(raw[r].w));
+    row_top[r] = larger<T>(larger<T>(m.x, m.y), larger<T>(m.z, m.w));
+    col_top = make_uint4(larger<T>(col_top.x, m.x), larger<T>(col_top.y, m.y), larger<T>(col_top.z, m.z),
+                         larger<T>(col_top.w, m.w));
+  }
+  if (a.qt != nullptr && !a.block) {
+    if constexpr (kLanes == 16) {
+      col_top.x = larger<T>(col_top.x, __shfl_xor_sync(0xffffffffu, col_top.x, 16));
+      col_top.y = larger<T>(col_top.y, __shfl_xor_sync(0xffffffffu, col_top.y, 16));
+      col_top.z = larger<T>(col_top.z, __shfl_xor_sync(0xffffffffu, col_top.z, 16));
+      col_top.w = larger<T>(col_top.w, __shfl_xor_sync(0xffffffffu, col_top.w, 16));
+    }
+    if (lane < kLanes) tops[warp][lane] = col_top;
+  }
+  // The rows' largest over their kLanes lanes: each step hands half of the rows to
+  // the other lane, so that a lane ends with one row (two lanes with the same), R
+  // shuffles instead of R log2(kLanes).
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const uint32_t m = magnitude(f[j]);
-      row_top[r] = max(row_top[r], m);
-      col_top[j] = max(col_top[j], m);
+  for (int n = R / 2, o = kLanes / 2; n >= 1; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t send = upper ? row_top[i] : row_top[i + n], keep = upper ? row_top[i + n] : row_top[i];
+      row_top[i] = larger<T>(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  uint32_t block_top = 0;
-  if (a.block || a.qt != nullptr) {
-    if constexpr (kLanes == 16) {
+  row_top[0] = larger<T>(row_top[0], __shfl_xor_sync(0xffffffffu, row_top[0], 1));
+  const float own = widened<T>(row_top[0]);  // of row (lane % kLanes) / 2 of this group of lanes
+  float scale;
+  Divisor block = {1.f, 1.f};
+  if (a.block) {
+    uint32_t top = __float_as_uint(own);
 #pragma unroll
-      for (int j = 0; j < E; ++j) col_top[j] = max(col_top[j], __shfl_xor_sync(0xffffffffu, col_top[j], 16));
-    }
-    if (lane < kLanes) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) tops[warp][c0 + j] = col_top[j];
-    }
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) warp_top[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-#pragma unroll
-      for (int w = 0; w < 8; ++w) col_top[j] = max(col_top[j], tops[w][c0 + j]);
-      block_top = max(block_top, col_top[j]);
-    }
-    block_top = group_max_bits<kLanes>(block_top);
-  }
-
-  // The largest |x mul|, as EightBits wants it, and what a value is divided by.
-  auto denominator = [&](uint32_t top, float* scale) {
-    float den;
-    *scale = bits.scale(__uint_as_float(top) * bits.mul, a.qtype, &den);
-    return den;
-  };
-  float scale, den_block = 0.f;
-  if (a.block) {
-    den_block = denominator(block_top, &scale);
+    for (int w = 0; w < 8; ++w) top = max(top, warp_top[w]);
+    block = B::divisor(__uint_as_float(top), &scale);
     if (threadIdx.x == 0) {
-      const int64_t row_tiles = (a.M + kTile - 1) / kTile;
-      if (a.q != nullptr) a.scale[mt * groups + nt] = scale;
+      if (a.q != nullptr) a.scale[mt * a.col_tiles + nt] = scale;
       if (a.qt != nullptr) a.scale_t[nt * row_tiles + mt] = scale;
     }
   }
   if (a.q != nullptr) {
+    Divisor mine = block;
+    if (!a.block) {
+      mine = B::divisor(own, &scale);
+      const int row = r0 + (lane % kLanes) / 2;
+      if ((lane & 1) == 0 && row < rows) a.scale[(i0 + row) * a.col_tiles + nt] = scale;
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float den = den_block;
-      if (!a.block) {
-        den = denominator(group_max_bits<kLanes>(row_top[r]), &scale);
-        if (lane % kLanes == 0 && r0 + r < rows) a.scale[(i0 + r0 + r) * groups + nt] = scale;
-      }
-      const float inv = EightBits<T>::inverse(den);
+      const int from = (lane & ~(kLanes - 1)) + 2 * r;
+      const Divisor d = {__shfl_sync(0xffffffffu, mine.den, from), __shfl_sync(0xffffffffu, mine.inv, from)};
       float f[E];
       V::unpack(raw[r], f);
       uint32_t words[E / 4];
 #pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        words[j / 4] = quantise2(quotient(f[j] * bits.mul, den, inv), quotient(f[j + 1] * bits.mul, den, inv), a.qtype) |
-                       quantise2(quotient(f[j + 2] * bits.mul, den, inv), quotient(f[j + 3] * bits.mul, den, inv), a.qtype) << 16;
-      }
+      for (int j = 0; j < E; j += 4)
+        words[j / 4] = B::template two<T>(f[j], f[j + 1], d) | B::template two<T>(f[j + 2], f[j + 3], d) << 16;
       if (r0 + r < rows) store_bytes<E>(a.q + (i0 + r0 + r) * a.N + j0 + c0, words, cols - c0, a.vec_q);
     }
   }
-  if (a.qt != nullptr) {
-    const int64_t row_tiles = (a.M + kTile - 1) / kTile;
-    // Columns as rows of bytes.  Units of 8 rows are XORed with the columns' number
-    // / 8: lanes of one store hit different banks, and so do those of one load.
+  if (a.qt == nullptr) return;
+  if (!a.block) {
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+      const int c = threadIdx.x;
+      uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      float den = den_block;
-      if (!a.block) {
-        den = denominator(col_top[j], &scale);
-        if (r0 == 0 && c0 + j < cols) a.scale_t[(j0 + c0 + j) * row_tiles + mt] = scale;
+      for (int w = 0; w < 8; ++w) {
+        if constexpr (sizeof(T) == 4) top = max(top, reinterpret_cast<const uint32_t*>(tops[w])[c]);
+        else top = max(top, uint32_t(reinterpret_cast<const uint16_t*>(tops[w])[c]) << 16);
       }
-      const float inv = EightBits<T>::inverse(den);
-      const int unit_key = (c0 + j) >> 3;
-#pragma unroll
-      for (int u = 0; u < R / 8; ++u) {
-        uint32_t words[2] = {0, 0};
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          float f[E], g[E];
-          V::unpack(raw[u * 8 + r], f);
-          V::unpack(raw[u * 8 + r + 1], g);
-          words[r / 4] |= quantise2(quotient(f[j] * bits.mul, den, inv), quotient(g[j] * bits.mul, den, inv), a.qtype)
-                          << (8 * (r % 4));
-        }
-        const int unit = (r0 >> 3) + u;
-        *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + ((unit ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
-      }
+      columns[c] = B::divisor(__uint_as_float(top), &scale);
+      if (c < cols) a.scale_t[(j0 + c) * row_tiles + mt] = scale;
     }
     __syncthreads();
+  }
+  // Columns as rows of bytes.  Units of 8 rows are XORed with the columns' number
+  // / 8: lanes of one store hit different banks, and so do those of one load.
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int col = k * 16 + warp * 2 + (lane >> 4), unit = lane & 15;
-      const uint2 w = *reinterpret_cast<const uint2*>(turned + col * kTile + ((unit ^ (col >> 3)) & 15) * 8);
-      const uint32_t words[2] = {w.x, w.y};
-      if (col < cols && unit * 8 < rows)
-        store_bytes<8>(a.qt + (j0 + col) * a.M + i0 + unit * 8, words, rows - unit * 8, a.vec_qt);
+  for (int j = 0; j < E; ++j) {
+    const Divisor d = a.block ? block : columns[c0 + j];
+    const int unit_key = (c0 + j) >> 3;
+#pragma unroll
+    for (int u = 0; u < R / 8; ++u) {
+      uint32_t words[2] = {0, 0};
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        float f[E], g[E];
+        V::unpack(raw[u * 8 + r], f);
+        V::unpack(raw[u * 8 + r + 1], g);
+        words[r / 4] |= B::template two<T>(f[j], g[j], d) << (8 * (r % 4));
+      }
+      const int unit = (r0 >> 3) + u;
+      *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + ((unit ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
     }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int col = k * 16 + warp * 2 + (lane >> 4), unit = lane & 15;
+    const uint2 w = *reinterpret_cast<const uint2*>(turned + col * kTile + ((unit ^ (col >> 3)) & 15) * 8);
+    const uint32_t words[2] = {w.x, w.y};
+    if (col < cols && unit * 8 < rows)
+      store_bytes<8>(a.qt + (j0 + col) * a.M + i0 + unit * 8, words, rows - unit * 8, a.vec_qt);
   }
 }
 
-template <typename T>
+template <typename T, int Q>
 qk_status launch_quant(const QuantArgs& a, bool vec, int64_t tiles, void* stream) {
-  const auto kernel = vec ? quant_kernel<T, true> : quant_kernel<T, false>;
+  const auto kernel = vec ? quant_kernel<T, Q, true> : quant_kernel<T, Q, false>;
   return launch_pdl(kernel, dim3(unsigned(tiles)), kQuantThreads, 0, stream, a);
+}
+template <typename T>
+qk_status launch_quant(const QuantArgs& a, int qtype, bool vec, int64_t tiles, void* stream) {
+  return qtype == QK_E4M3 ? launch_quant<T, QK_E4M3>(a, vec, tiles, stream)
+                          : launch_quant<T, QK_INT8>(a, vec, tiles, stream);
 }
 
 }  // namespace
@@ -250,10 +304,9 @@ extern "C" qk_status qk_quant_fwd(const void* x, void* q, float* scale, void* qt
   a.N = N;
   a.col_tiles = col_tiles;
   a.block = block_rows == 128;
-  a.qtype = qtype;
   a.vec_q = N % 8 == 0 && aligned_to(q, 8);
   a.vec_qt = M % 8 == 0 && aligned_to(qt, 8);
   const bool vec = N * int64_t(es) % 16 == 0 && aligned16(x);
-  return dtype == QK_F32 ? launch_quant<float>(a, vec, row_tiles * col_tiles, stream)
-                         : launch_quant<__nv_bfloat16>(a, vec, row_tiles * col_tiles, stream);
+  return dtype == QK_F32 ? launch_quant<float>(a, qtype, vec, row_tiles * col_tiles, stream)
+                         : launch_quant<__nv_bfloat16>(a, qtype, vec, row_tiles * col_tiles, stream);
 }
