@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/qk.h"
 #include "qk_device.cuh"
@@ -152,9 +153,11 @@ struct GatherArgs {
   int32_t k, groups;
 };
 
+constexpr int kGatherWords = 8;  // words of a lane: 4 KB a warp (16384 x 4 of 4096 bf16: 103 us, with 4 105)
+
 template <typename W>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
-  constexpr int kUnroll = 4;
+  constexpr int kUnroll = kGatherWords;
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
@@ -199,11 +202,14 @@ struct CombineArgs {
 template <typename T, bool VEC>
 __device__ __forceinline__ uint4 load_raw(const T* p, int64_t left) {
   using V = Vec16<T>;
-  if constexpr (VEC) return *reinterpret_cast<const uint4*>(p);
-  float f[V::kElems];
+  if constexpr (VEC) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else {
+    float f[V::kElems];
 #pragma unroll
-  for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
-  return V::pack(f);  // exact: the values are T's
+    for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
+    return V::pack(f);  // exact: the values are T's
+  }
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_values(T* p, int64_t left, const float* f) {
@@ -217,7 +223,9 @@ __device__ __forceinline__ void store_values(T* p, int64_t left, const float* f)
   }
 }
 
-constexpr int kAtOnce = 4;  // choices whose rows are loaded together
+// Choices whose rows are loaded together.  16384 tokens of 4096 bf16, forward: four
+// choices 113 us with 4, 126 with 2 (and 127 one after the other).
+constexpr int kAtOnce = 4;
 
 // A warp forms a piece of a token's row; the sum runs over the choices in order.
 template <typename T, bool VEC>
@@ -257,38 +265,40 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   }
 }
 
-// THREADS threads take a token, kAtOnce choices at a time: dy and their rows are
-// read together, drows leave at once, and each choice's products are summed over
-// the threads at the end.
-template <typename T, bool VEC, int THREADS>
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs a) {
+// THREADS threads take a token, AT choices at a time: dy and their rows are read
+// together, drows leave at once, and each choice's products are summed over the
+// threads at the end.  The registers are held down for the sake of CTAs an SM
+// (16384 tokens of 4096 bf16, two choices: 142 us with three, 115 with five, 111
+// with six and AT = 2; four choices: 201, 183, 189).
+template <typename T, bool VEC, int THREADS, int AT>
+__global__ void __launch_bounds__(256, AT == 2 ? 6 : 5) combine_bwd_kernel(const CombineArgs a) {
   constexpr int E = Vec16<T>::kElems, kWarps = THREADS / 32, kTokens = 256 / THREADS;
-  __shared__ float red[2][kAtOnce][kWarps];
+  __shared__ float red[2][AT][kWarps];
   grid_dependency_wait();
   allow_dependent_launch();
   const int tid = threadIdx.x % THREADS, warp = tid >> 5, lane = threadIdx.x & 31;
   int turn = 0;
   for (int64_t t = int64_t(blockIdx.x) * kTokens + threadIdx.x / THREADS; t < a.T; t += int64_t(gridDim.x) * kTokens) {
     const T* dy = static_cast<const T*>(a.dy) + t * a.N;
-    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
-      int32_t at[kAtOnce];
-      float w[kAtOnce], dot[kAtOnce] = {};
+    for (int j0 = 0; j0 < a.k; j0 += AT) {
+      int32_t at[AT];
+      float w[AT], dot[AT] = {};
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < AT; ++j) {
         at[j] = j0 + j < a.k ? a.slot[t * a.k + j0 + j] : -1;
         if (at[j] >= a.P) at[j] = -1;
         w[j] = at[j] >= 0 ? a.weights[t * a.k + j0 + j] : 0.f;
       }
       for (int64_t c = tid * E; c < a.N; c += THREADS * E) {
         const uint4 graw = load_raw<T, VEC>(dy + c, a.N - c);
-        uint4 f[kAtOnce];
+        uint4 f[AT];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
+        for (int j = 0; j < AT; ++j)
           if (at[j] >= 0) f[j] = load_raw<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N + c, a.N - c);
         float g[E];
         Vec16<T>::unpack(graw, g);
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < AT; ++j) {
           if (at[j] < 0) continue;
           float v[E];
           Vec16<T>::unpack(f[j], v);
@@ -302,14 +312,14 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs a) {
       }
       if (a.dweights == nullptr) continue;
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < AT; ++j) {
         if (j0 + j >= a.k) break;
         dot[j] = group_sum<32>(dot[j]);
         if (kWarps > 1 && lane == 0) red[turn][j][warp] = dot[j];
       }
       if constexpr (kWarps > 1) {
         __syncthreads();  // one is enough: the next sums go to the other half
-        if (tid < kAtOnce && j0 + tid < a.k) {
+        if (tid < AT && j0 + tid < a.k) {
           float s = 0.f;
 #pragma unroll
           for (int i = 0; i < kWarps; ++i) s += red[turn][tid][i];
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs a) {
         turn ^= 1;
       } else if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
+        for (int j = 0; j < AT; ++j)
           if (j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
       }
     }
@@ -362,8 +372,12 @@ qk_status launch_combine(const CurrentDevice& d, bool bwd, bool vec, CombineArgs
   if (bwd) {
     // A warp a token where a CTA would have less than a vector a thread.
     const bool narrow = a.N <= 256 * Vec16<T>::kElems / 4;
-    const auto kernel = narrow ? (vec ? combine_bwd_kernel<T, true, 32> : combine_bwd_kernel<T, false, 32>)
-                               : (vec ? combine_bwd_kernel<T, true, 256> : combine_bwd_kernel<T, false, 256>);
+    const auto pick = [&](auto at) {
+      constexpr int AT = decltype(at)::value;
+      return narrow ? (vec ? combine_bwd_kernel<T, true, 32, AT> : combine_bwd_kernel<T, false, 32, AT>)
+                    : (vec ? combine_bwd_kernel<T, true, 256, AT> : combine_bwd_kernel<T, false, 256, AT>);
+    };
+    const auto kernel = a.k <= 2 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 4>());
     return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(narrow ? ceil_div(a.T, 8) : a.T, int64_t(d.sms) * 32))), 256, 0,
                       stream, a);
   }
@@ -461,7 +475,7 @@ qk_status qk_expert_gather_fwd(const void* x, const float* scale, const int32_t*
   // The widest word that rows consist of.
   const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | uintptr_t(row_bytes);
   auto launch = [&](auto kernel, int64_t word) {
-    a.pieces = ceil_div(row_bytes / word, 128);
+    a.pieces = ceil_div(row_bytes / word, 32 * kGatherWords);
     return launch_pdl(kernel, dim3(warps_grid(d, T * a.pieces)), 256, 0, stream, a);
   };
   if (all % 16 == 0) return launch(gather_kernel<uint4>, 16);

@@ -19,8 +19,10 @@
 namespace qk {
 namespace {
 
-constexpr int kQuantThreads = 256;
 constexpr int kTile = 128;
+constexpr int kRows = 8;  // rows of a thread: with a 16-byte vector of each, 8 x 8 of bf16 or 8 x 4 of float32
+template <typename T>
+__host__ __device__ constexpr int quant_threads() { return kTile * kTile / kRows / (16 / int(sizeof(T))); }
 
 struct QuantArgs {
   const void* x;   // [M, N]
@@ -81,8 +83,18 @@ struct EightBitsOf {
     if ((b & 1) == 0 && rest != 0.f && fabsf(q) > 0x1p-24f) b += (rest < 0.f) == (q < 0.f) ? 1 : -1;
     return __int_as_float(b);
   }
+  // Two values in 8 bits.  float32: from products with the rounded reciprocal, off by
+  // less than 2^-22, where all that lies within 2^-21 of them rounds alike (all but
+  // one value in 30000), else from the quotients (16384 x 4096 both ways with half
+  // the threads: 139 us, from the quotients always 152).
   template <typename T>
   __device__ __forceinline__ static uint32_t two(float a, float b, Divisor d) {
+    if constexpr (sizeof(T) == 4) {
+      const float inv = kMul * d.inv, below = 1.f - 0x1p-21f, above = 1.f + 0x1p-21f;
+      const float qa = a * inv, qb = b * inv;
+      const uint32_t w = quantise2(qa * below, qb * below, Q);
+      if (w == quantise2(qa * above, qb * above, Q)) return w;
+    }
     return quantise2(value<T>(a, d), value<T>(b, d), Q);
   }
 };
@@ -100,15 +112,16 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* words, i
     if (j < left) p[j] = uint8_t(words[j / 4] >> (8 * (j % 4)));
 }
 
-// A thread holds E columns (a 16-byte vector) of R rows that follow each other:
-// 8 x 8 of bf16, 16 x 4 of float32.  A warp has 16 rows of the tile.
+// The registers of a thread are held down to 64 (bf16: 62 us at 16384 x 4096 both
+// ways, 66 with 85 and three CTAs an SM).
 template <typename T, int Q, bool VEC>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>()) quant_kernel(const QuantArgs a) {
   using V = Vec16<T>;
   using B = EightBitsOf<Q>;
-  constexpr int E = V::kElems, kLanes = kTile / E, R = 16 * kLanes / 32;  // R: half of kLanes
-  __shared__ __align__(16) uint4 tops[8][kLanes];   // largest bits of a warp's rows, by column
-  __shared__ uint32_t warp_top[8];
+  constexpr int E = V::kElems, kLanes = kTile / E, R = kRows, kWarps = quant_threads<T>() / 32;
+  constexpr int kShare = kLanes / R;  // lanes that end with one row's largest
+  __shared__ __align__(16) uint4 tops[kWarps][kLanes];   // largest bits of a warp's rows, by column
+  __shared__ uint32_t warp_top[kWarps];
   __shared__ Divisor columns[kTile];
   __shared__ __align__(16) uint8_t turned[kTile * kTile];
   grid_dependency_wait();
@@ -116,7 +129,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t mt = int64_t(blockIdx.x) / a.col_tiles, nt = int64_t(blockIdx.x) - mt * a.col_tiles;
   const int64_t i0 = mt * kTile, j0 = nt * kTile, row_tiles = (a.M + kTile - 1) / kTile;
-  const int r0 = warp * 16 + (lane / kLanes) * R, c0 = (lane % kLanes) * E;  // this thread's part of the tile
+  const int r0 = (warp * (32 / kLanes) + lane / kLanes) * R, c0 = (lane % kLanes) * E;  // this thread's part of the tile
   const int rows = int(min(int64_t(kTile), a.M - i0)), cols = int(min(int64_t(kTile), a.N - j0));
   const T* x = static_cast<const T*>(a.x) + (i0 + r0) * a.N + j0 + c0;
 
@@ -156,8 +169,8 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
     if (lane < kLanes) tops[warp][lane] = col_top;
   }
   // The rows' largest over their kLanes lanes: each step hands half of the rows to
-  // the other lane, so that a lane ends with one row (two lanes with the same), R
-  // shuffles instead of R log2(kLanes).
+  // the other lane, so that kShare lanes end with one row, in some R shuffles
+  // instead of R log2(kLanes).
 #pragma unroll
   for (int n = R / 2, o = kLanes / 2; n >= 1; n /= 2, o /= 2) {
     const bool upper = (lane & o) != 0;
@@ -167,8 +180,9 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
       row_top[i] = larger<T>(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  row_top[0] = larger<T>(row_top[0], __shfl_xor_sync(0xffffffffu, row_top[0], 1));
-  const float own = widened<T>(row_top[0]);  // of row (lane % kLanes) / 2 of this group of lanes
+#pragma unroll
+  for (int o = kShare / 2; o >= 1; o /= 2) row_top[0] = larger<T>(row_top[0], __shfl_xor_sync(0xffffffffu, row_top[0], o));
+  const float own = widened<T>(row_top[0]);  // of row (lane % kLanes) / kShare of this group of lanes
   float scale;
   Divisor block = {1.f, 1.f};
   if (a.block) {
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
     if (lane == 0) warp_top[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = max(top, warp_top[w]);
+    for (int w = 0; w < kWarps; ++w) top = max(top, warp_top[w]);
     block = B::divisor(__uint_as_float(top), &scale);
     if (threadIdx.x == 0) {
       if (a.q != nullptr) a.scale[mt * a.col_tiles + nt] = scale;
@@ -189,12 +203,12 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
     Divisor mine = block;
     if (!a.block) {
       mine = B::divisor(own, &scale);
-      const int row = r0 + (lane % kLanes) / 2;
-      if ((lane & 1) == 0 && row < rows) a.scale[(i0 + row) * a.col_tiles + nt] = scale;
+      const int row = r0 + (lane % kLanes) / kShare;
+      if (lane % kShare == 0 && row < rows) a.scale[(i0 + row) * a.col_tiles + nt] = scale;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int from = (lane & ~(kLanes - 1)) + 2 * r;
+      const int from = (lane & ~(kLanes - 1)) + kShare * r;
       const Divisor d = {__shfl_sync(0xffffffffu, mine.den, from), __shfl_sync(0xffffffffu, mine.inv, from)};
       float f[E];
       V::unpack(raw[r], f);
@@ -212,7 +226,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
       const int c = threadIdx.x;
       uint32_t top = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         if constexpr (sizeof(T) == 4) top = max(top, reinterpret_cast<const uint32_t*>(tops[w])[c]);
         else top = max(top, uint32_t(reinterpret_cast<const uint16_t*>(tops[w])[c]) << 16);
       }
@@ -227,24 +241,20 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
   for (int j = 0; j < E; ++j) {
     const Divisor d = a.block ? block : columns[c0 + j];
     const int unit_key = (c0 + j) >> 3;
+    uint32_t words[2] = {0, 0};
 #pragma unroll
-    for (int u = 0; u < R / 8; ++u) {
-      uint32_t words[2] = {0, 0};
-#pragma unroll
-      for (int r = 0; r < 8; r += 2) {
-        float f[E], g[E];
-        V::unpack(raw[u * 8 + r], f);
-        V::unpack(raw[u * 8 + r + 1], g);
-        words[r / 4] |= B::template two<T>(f[j], g[j], d) << (8 * (r % 4));
-      }
-      const int unit = (r0 >> 3) + u;
-      *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + ((unit ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
+    for (int r = 0; r < R; r += 2) {
+      float f[E], g[E];
+      V::unpack(raw[r], f);
+      V::unpack(raw[r + 1], g);
+      words[r / 4] |= B::template two<T>(f[j], g[j], d) << (8 * (r % 4));
     }
+    *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + (((r0 >> 3) ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int col = k * 16 + warp * 2 + (lane >> 4), unit = lane & 15;
+  for (int k = 0; k < kTile / 2 / kWarps; ++k) {
+    const int col = (k * kWarps + warp) * 2 + (lane >> 4), unit = lane & 15;
     const uint2 w = *reinterpret_cast<const uint2*>(turned + col * kTile + ((unit ^ (col >> 3)) & 15) * 8);
     const uint32_t words[2] = {w.x, w.y};
     if (col < cols && unit * 8 < rows)
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2) quant_k
 template <typename T, int Q>
 qk_status launch_quant(const QuantArgs& a, bool vec, int64_t tiles, void* stream) {
   const auto kernel = vec ? quant_kernel<T, Q, true> : quant_kernel<T, Q, false>;
-  return launch_pdl(kernel, dim3(unsigned(tiles)), kQuantThreads, 0, stream, a);
+  return launch_pdl(kernel, dim3(unsigned(tiles)), quant_threads<T>(), 0, stream, a);
 }
 template <typename T>
 qk_status launch_quant(const QuantArgs& a, int qtype, bool vec, int64_t tiles, void* stream) {

@@ -185,21 +185,20 @@ qk_status launch_pairs(const Call& c) {
 // Rows of a and b as TMA reads them, by way of the workspace where K is not a multiple of 16.
 qk_status pad_operands(Call& c, void* workspace) {
   if (c.ld == c.K) return QK_OK;
-  char* at = static_cast<char*>(workspace);
-  const struct {
-    const void** p;
-    int64_t rows;
-  } parts[] = {{&c.b, c.N * c.experts}, {&c.a, c.M}};
-  for (const auto& part : parts) {
-    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(part.rows, 8), 16 * c.dev.sms));
-    const qk_status st =
-        launch_pdl(pad_rows_kernel, dim3(grid), 256, 0, c.stream, static_cast<const uint8_t*>(*part.p), part.rows,
-                   int32_t(c.K), reinterpret_cast<uint8_t*>(at), int32_t(c.ld));
-    if (st != QK_OK) return st;
-    *part.p = at;
-    at += part.rows * c.ld;
-  }
-  return QK_OK;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  PadArgs p = {};
+  p.rows[0] = c.N * c.experts;
+  p.rows[1] = c.M;
+  p.in[0] = static_cast<const uint8_t*>(c.b);
+  p.in[1] = static_cast<const uint8_t*>(c.a);
+  p.out[0] = at;
+  p.out[1] = at + p.rows[0] * c.ld;
+  p.cols = int32_t(c.K);
+  p.ld = int32_t(c.ld);
+  c.b = p.out[0];
+  c.a = p.out[1];
+  const unsigned grid = unsigned(std::min<int64_t>(ceil_div(p.rows[0] + p.rows[1], 8), 16 * c.dev.sms));
+  return launch_pdl(pad_rows_kernel, dim3(grid), 256, 0, c.stream, p);
 }
 
 template <typename T>
