@@ -8,6 +8,8 @@
 // with its two scales and add it to the running sum in registers, to nearest.
 #pragma once
 
+#include <type_traits>
+
 #include "qk_internal.h"
 #include "qk_rows_out.cuh"
 #include "qk_tensor.cuh"
@@ -106,17 +108,21 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
     scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const ScaledArgs p) {
   constexpr int kStages = tile_stages(TN), kStageBytes = tile_stage_bytes(TN), kSlotBytes = tile_slot_bytes(TN);
-  constexpr int kBufs = 4;
-  constexpr uint32_t kColumns = kBufs * TN;
+  // A product of few columns waits for the one before it on the same sums, some 125
+  // cycles where its own work is 16 to 64.  So kGroup steps, each with its own sums, are
+  // worked on in turns: their first 32 k, their second, and so on (16 x 8192 x 4096:
+  // 11.3 us without, 9.9 with).  TMEM holds two such groups.
+  constexpr int kGroup = TN <= 64 ? kQuad : 2;
+  constexpr uint32_t kColumns = 2 * kGroup * TN;
   constexpr int kCols = TN / 2 < 16 ? 16 : TN / 2, kReaders = 4 * (TN / kCols);
   extern __shared__ unsigned char dynamic_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kBufs + 2 * kScaleSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + 2 * kScaleSlots];
   __shared__ uint32_t tmem_at;
   __shared__ ExpertTable table;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kStages, done0 = full0 + 16 * kStages,
-                 free0 = done0 + 8 * kBufs, sfull0 = free0 + 8 * kBufs, sempty0 = sfull0 + 8 * kScaleSlots;
+                 free0 = done0 + 16, sfull0 = free0 + 16, sempty0 = sfull0 + 8 * kScaleSlots;
   const uint32_t ring = (smem_addr(dynamic_smem) + 1023u) & ~1023u;
   const uint32_t slots = ring + uint32_t(kStages * kStageBytes);
 
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int i = 0; i < kBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(done0 + 8 * i, 1);
       mbar_init(free0 + 8 * i, kReaders);
     }
@@ -198,25 +204,45 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
     if (failed)  // leave once the loads in flight have landed
       for (int64_t i = max(int64_t(0), q - kStages); i < q; ++i)
         mbar_wait<false>(full0 + 8 * uint32_t(i % kStages), uint32_t(i / kStages) & 1u, p.timeout_ns);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---- products ----
     constexpr uint32_t idesc = instruction_desc_e4m3(128, TN);
     int st = 0;
     uint32_t turn = 0, it = 0;
     for (int32_t t = first; t < tiles && !failed; t += step) {
-      for (int32_t s = s0; s < s1; ++s, ++it) {
-        const uint32_t buf = it % kBufs;
-        if (!wait(free0 + 8 * buf, ((it / kBufs) & 1u) ^ 1u)) break;
-        if (!wait(full0 + 8 * st, turn)) break;
+      for (int32_t s = s0; s < s1; s += kGroup, ++it) {
+        const int n = min(kGroup, s1 - s);
+        const uint32_t set = it & 1u;
+        bool ok = wait(free0 + 8 * set, ((it >> 1) & 1u) ^ 1u);
+        int last = st;
+        uint32_t its_turn = turn;
+        for (int q = 0; q < n && ok; ++q) {
+          ok = wait(full0 + 8 * last, its_turn);
+          if (++last == kStages) last = 0, its_turn ^= 1u;
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
         tcgen05_fence_after();
-        const uint32_t sb = ring + uint32_t(st) * kStageBytes;
-        const uint64_t db = operand_desc(sb, 0), da = operand_desc(sb + 128 * kScaledStepK, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kScaledStepK / 32; ++k)
-          mma_e4m3(tmem + buf * TN, db + uint64_t(2 * k), da + uint64_t(2 * k), idesc, k > 0);
-        mma_commit(empty0 + 8 * st);
-        mma_commit(done0 + 8 * buf);
-        if (++st == kStages) st = 0, turn ^= 1u;
+          for (int k = 0; k < kScaledStepK / 32; ++k) {
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q) {
+              if (q >= n) break;
+              const int at = st + q < kStages ? st + q : st + q - kStages;
+              const uint32_t sb = ring + uint32_t(at) * kStageBytes;
+              mma_e4m3(tmem + (set * kGroup + q) * TN, operand_desc(sb, 0) + uint64_t(2 * k),
+                       operand_desc(sb + 128 * kScaledStepK, 0) + uint64_t(2 * k), idesc, k > 0);
+            }
+          }
+          mma_commit(done0 + 8 * set);
+          for (int q = 0; q < n; ++q) mma_commit(empty0 + 8 * (st + q < kStages ? st + q : st + q - kStages));
+        }
+        __syncwarp();
+        st = last;
+        turn = its_turn;
       }
     }
   } else if (warp == 2 || warp == 3) {
@@ -277,33 +303,47 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
         const float4 bq = ld_shared_v4(src_s + (quarter * 32 + lane) * 16);
         const float bs[4] = {bq.x, bq.y, bq.z, bq.w};
 #pragma unroll
-        for (int qi = 0; qi < kQuad; ++qi) {
-          if (q0 + qi >= s1) break;
-          const uint32_t buf = it % kBufs;
-          ok = wait(done0 + 8 * buf, (it / kBufs) & 1u);
+        for (int g = 0; g < kQuad; g += kGroup) {
+          if (q0 + g >= s1) break;
+          const uint32_t set = it & 1u;
+          ok = wait(done0 + 8 * set, (it >> 1) & 1u);
           if (!__all_sync(0xffffffffu, ok)) {
             failed = true;
             break;
           }
           ++it;
           tcgen05_fence_after();
-          float x[kCols];
-          const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + buf * TN + uint32_t(half * kCols);
+          const uint32_t src = tmem + (uint32_t(quarter * 32) << 16) + set * (kGroup * TN) + uint32_t(half * kCols);
+          // All of a group's sums at one trip where they fit the registers.
+          constexpr int kAtOnce = kCols == 16 ? kGroup : kCols == 32 ? 2 : 1;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) tmem_load_16(src + uint32_t(c), x + c);
+          for (int q1 = 0; q1 < kGroup; q1 += kAtOnce) {
+            float x[kAtOnce * kCols];  // of a step that there is not: whatever TMEM holds, not used
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) tmem_load_wait(x + c);
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(free0 + 8 * buf);
-          const uint32_t sa = src_s + 128 * 16 + qi * (TN * 4) + half * (kCols * 4);
+            for (int c = 0; c < kAtOnce * kCols; c += 16)
+              tmem_load_16(src + uint32_t((q1 + c / kCols) * TN + c % kCols), x + c);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 as = ld_shared_v4(sa + c * 4);
-            v[c] = fmaf(x[c], as.x * bs[qi], v[c]);
-            v[c + 1] = fmaf(x[c + 1], as.y * bs[qi], v[c + 1]);
-            v[c + 2] = fmaf(x[c + 2], as.z * bs[qi], v[c + 2]);
-            v[c + 3] = fmaf(x[c + 3], as.w * bs[qi], v[c + 3]);
+            for (int c = 0; c < kAtOnce * kCols; c += 16) tmem_load_wait(x + c);
+            if (q1 + kAtOnce == kGroup) {
+              tcgen05_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(free0 + 8 * set);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+              const int qi = g + q1 + q;
+              if (q0 + qi >= s1) break;
+              const uint32_t sa = src_s + 128 * 16 + qi * (TN * 4) + half * (kCols * 4);
+#pragma unroll
+              for (int c = 0; c < kCols; c += 4) {
+                const float4 as = ld_shared_v4(sa + c * 4);
+                const float* f = x + q * kCols + c;
+                v[c] = fmaf(f[0], as.x * bs[qi], v[c]);
+                v[c + 1] = fmaf(f[1], as.y * bs[qi], v[c + 1]);
+                v[c + 2] = fmaf(f[2], as.z * bs[qi], v[c + 2]);
+                v[c + 3] = fmaf(f[3], as.w * bs[qi], v[c + 3]);
+              }
+            }
           }
         }
         __syncwarp();
@@ -340,15 +380,27 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
     if (first < tiles && !failed && warp >= 4) {
       e = 0;
       const At at = tile(first, e);
-      const int col = int(threadIdx.x) - 128;
-      const int32_t n = at.n0 + (col & 127);
-      // rank r takes tokens r, r + ranks, ...; two tokens at a time on 256 threads
-      for (int j = (int(cluster_ctarank()) + (col >> 7) * ranks); j < at.rows; j += 2 * ranks) {
-        float sum = 0.f;
-        for (int32_t r = 0; r < ranks; ++r)
-          sum += ld_shared_cluster(map_to_rank(ring + uint32_t(j * 128 + (col & 127)) * 4, uint32_t(r)));
-        if (n < p.N) Vec16<T>::store1(static_cast<T*>(p.y) + int64_t(at.row0 + j) * p.N + n, sum);
-      }
+      const int id = int(threadIdx.x) - 128;
+      auto join = [&](auto count) {  // four neighbours of a token a thread, eight tokens at a time
+        constexpr int kRanks = decltype(count)::value;
+        const int32_t n = at.n0 + (id & 31) * 4;
+        for (int j = int(cluster_ctarank()) + (id >> 5) * kRanks; j < at.rows; j += 8 * kRanks) {
+          const uint32_t own = ring + uint32_t(j * 128 + (id & 31) * 4) * 4;
+          float4 f[kRanks];
+#pragma unroll
+          for (int r = 0; r < kRanks; ++r) f[r] = ld_shared_cluster_v4(map_to_rank(own, uint32_t(r)));
+          float sum[4] = {f[0].x, f[0].y, f[0].z, f[0].w};
+#pragma unroll
+          for (int r = 1; r < kRanks; ++r) sum[0] += f[r].x, sum[1] += f[r].y, sum[2] += f[r].z, sum[3] += f[r].w;
+          T* y = static_cast<T*>(p.y) + int64_t(at.row0 + j) * p.N + n;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) Vec16<T>::store1(y + i, sum[i]);
+        }
+      };
+      if (ranks == 2) join(std::integral_constant<int, 2>());
+      else if (ranks == 4) join(std::integral_constant<int, 4>());
+      else join(std::integral_constant<int, 8>());
     }
     __syncwarp();
     cluster_sync_all();  // the others have read this CTA's sums
@@ -714,7 +766,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // (a multiple of 16) that start on 16: what TMA can read.  Bytes behind a row are
 // whatever stands behind it, which TMA reads as zero.  A thread makes 16 bytes
 // from the five words that they lie in, or from single bytes where a word would
-// reach out of the matrix (2047 and 1001 rows of 1023: 3.2 us, from bytes %s).
+// reach out of the matrix (1001 x 2047 x 1023 in all: 25 us, from bytes and in two launches 28).
 struct PadArgs {
   const uint8_t* in[2];
   uint8_t* out[2];

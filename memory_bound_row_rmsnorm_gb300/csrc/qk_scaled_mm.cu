@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/qk.h"
@@ -140,25 +141,96 @@ qk_status launch(const Call& c, K kernel, int64_t grid, int threads, int cluster
 
 constexpr int64_t kMostTiles = int64_t(1) << 30;  // tile numbers are 32-bit
 
+// Clusters of 2, 4 and 8 CTAs of a tile kernel that a device holds at a time
+// (clusters lie within a GPC, so 8 take fewer of the SMs).
+struct Clusters {
+  std::atomic<int> most[3] = {{0}, {0}, {0}};
+};
+template <typename K>
+int most_clusters(Clusters& known, const CurrentDevice& d, K kernel, int log2_size, int smem) {
+  std::atomic<int>& slot = known.most[log2_size - 1];
+  int n = slot.load(std::memory_order_relaxed);  // devices of one kind: what one answers holds for all
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(unsigned(d.sms / 8 * 8), 1, 1);
+    cfg.blockDim = dim3(kScaledThreads, 1, 1);
+    cfg.dynamicSmemBytes = size_t(smem);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << log2_size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    n = std::max(n, 1);
+    slot.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// How the tile kernel of TN columns would do a call, and about how long it would take.
+struct TilePlan {
+  qk_status status;
+  int64_t tiles;  // at most
+  int ranks;      // CTAs that share a tile's k
+  double us;
+};
+
+// Tiles of `rows` rows that M rows in groups of unknown sizes make, about: half of
+// the groups that have rows have a tile more than their share, and each has one.
+double likely_tiles(const Call& c, int64_t rows) {
+  if (c.offsets == nullptr) return double(ceil_div(c.M, rows));
+  const double active = double(std::min(c.M, c.experts));
+  return std::max(active, double(c.M) / double(rows) + 0.5 * active);
+}
+
+// Microseconds: a launch, and a step and an end for each tile that an SM does one
+// after the other.  Measured over 1 to 2048 rows x 200 to 8192 x 1024 to 8192, and
+// 2 to 16384 rows of 32 experts x 4096 x 2048 and 2048 x 4096, in a graph.
+constexpr double kTileLaunch = 5.2, kPairLaunch = 4.4, kPairStep = 0.40, kPairStepRows = 0.62, kPairEnd = 1.7;
+template <int TN>
+constexpr double tile_step() { return TN == 16 ? 0.24 : TN == 32 ? 0.25 : TN == 64 ? 0.29 : 0.43; }
+template <int TN>
+constexpr double tile_end() { return TN == 16 ? 0.8 : TN == 32 ? 1.0 : TN == 64 ? 1.1 : 3.2; }
+
 template <int TN, typename T>
-qk_status launch_tiles(const Call& c) {
+TilePlan plan_tiles(const Call& c) {
   const auto kernel = scaled_tile_kernel<TN, T>;
   static std::atomic<uint64_t> prepared{0};  // one bit a device
-  const qk_status st = prepare(prepared, c.dev, kernel, tile_smem(TN));
-  if (st != QK_OK) return st;
+  static Clusters known;
+  TilePlan plan = {};
+  plan.status = prepare(prepared, c.dev, kernel, tile_smem(TN));
+  if (plan.status != QK_OK) return plan;
+  const int64_t n_tiles = ceil_div(c.N, 128), groups = ceil_div(c.K, kScaledStepK);
+  plan.tiles = most_tiles(c, TN) * n_tiles;
+  // Where the tiles leave SMs idle, a cluster shares a tile's k: the largest of
+  // which all run at one time (1 x 2048 x 8192: 12.9 us with 16 clusters of 8, of
+  // which not all do, 9.1 with clusters of 4).
+  int log2_ranks = 0;
+  while (log2_ranks < 3 && groups >= 2 << log2_ranks && plan.tiles * (2 << log2_ranks) <= c.dev.sms &&
+         plan.tiles <= most_clusters(known, c.dev, kernel, log2_ranks + 1, tile_smem(TN)))
+    ++log2_ranks;
+  plan.ranks = 1 << log2_ranks;
+  const double waves = std::ceil(likely_tiles(c, TN) * double(n_tiles) * plan.ranks / c.dev.sms);
+  plan.us = kTileLaunch + waves * (double(ceil_div(groups, plan.ranks)) * tile_step<TN>() + tile_end<TN>());
+  return plan;
+}
+
+template <int TN, typename T>
+qk_status launch_tiles(const Call& c, const TilePlan& plan) {
+  if (plan.tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
   ScaledArgs p = arguments(c);
   p.n_tiles = int32_t(ceil_div(c.N, 128));
-  const int64_t tiles = most_tiles(c, TN) * p.n_tiles;
-  if (tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
-  // Where the tiles leave SMs idle, a cluster shares a tile's k.
-  int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= c.dev.sms && p.groups >= ranks * 2) ranks *= 2;
-  p.split_steps = int32_t(ceil_div(p.groups, ranks));
+  p.split_steps = int32_t(ceil_div(p.groups, plan.ranks));
   CUtensorMap ma, mb;
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, TN) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
     return QK_ERR_LAUNCH;
-  return launch(c, kernel, ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, c.dev.sms), kScaledThreads, ranks,
-                tile_smem(TN), ma, mb, p);
+  const int64_t grid = plan.ranks > 1 ? plan.tiles * plan.ranks : std::min<int64_t>(plan.tiles, c.dev.sms);
+  return launch(c, scaled_tile_kernel<TN, T>, grid, kScaledThreads, plan.ranks, tile_smem(TN), ma, mb, p);
 }
 
 template <bool COLS, typename T>
@@ -203,12 +275,22 @@ qk_status pad_operands(Call& c, void* workspace) {
 
 template <typename T>
 qk_status product(const Call& c) {
-  const int64_t mean = ceil_div(c.M, c.experts);  // rows of a group, as far as the host knows
-  if (mean <= 16) return launch_tiles<16, T>(c);
-  if (mean <= 32) return launch_tiles<32, T>(c);
-  if (mean <= 64) return launch_tiles<64, T>(c);
-  if (mean <= 256) return launch_tiles<128, T>(c);
-  return c.b_rows == 1 ? launch_pairs<true, T>(c) : launch_pairs<false, T>(c);
+  const TilePlan plans[] = {plan_tiles<16, T>(c), plan_tiles<32, T>(c), plan_tiles<64, T>(c), plan_tiles<128, T>(c)};
+  const double waves = std::ceil(likely_tiles(c, 256) * double(ceil_div(c.N, 256)) / (c.dev.sms / 2));
+  const double step = c.b_rows == 1 ? kPairStepRows : kPairStep;
+  double best = kPairLaunch + waves * (double(ceil_div(c.K, kScaledStepK)) * step + kPairEnd);
+  int pick = -1;
+  for (int i = 0; i < 4; ++i) {
+    if (plans[i].status != QK_OK) return plans[i].status;
+    if (plans[i].us < best && plans[i].tiles <= kMostTiles) best = plans[i].us, pick = i;
+  }
+  switch (pick) {
+    case 0: return launch_tiles<16, T>(c, plans[0]);
+    case 1: return launch_tiles<32, T>(c, plans[1]);
+    case 2: return launch_tiles<64, T>(c, plans[2]);
+    case 3: return launch_tiles<128, T>(c, plans[3]);
+    default: return c.b_rows == 1 ? launch_pairs<true, T>(c) : launch_pairs<false, T>(c);
+  }
 }
 
 }  // namespace
