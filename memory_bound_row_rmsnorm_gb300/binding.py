@@ -784,6 +784,22 @@ def quant_fwd(x, block_rows: int = 1, qdtype=None, want_q: bool = True, want_t: 
     return q, scale, qt, scale_t
 
 
+def _scaled_mm_check(a, a_scale, b, b_scale, offsets, K, N, G, rows, experts, dev):
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if a.dim() < 1 or b.dim() != (2 if offsets is None else 3):
+        raise ValueError("b must be [N, K], or [experts, N, K] with offsets")
+    if offsets is not None and a.dim() != 2:
+        raise ValueError("a must be [rows, K] with offsets")
+    _same("a", a, a.shape, e4m3, dev)
+    _same("b", b, b.shape[:-1] + (K,), e4m3, dev)
+    _same("a_scale", a_scale, a.shape[:-1] + (G,), f32, dev)
+    if rows != N and rows != _blocks(N):
+        raise ValueError(f"b_scale must have {_blocks(N)} or {N} rows")
+    _same("b_scale", b_scale, b.shape[:-2] + (rows, G), f32, dev)
+    if offsets is not None:
+        _same("offsets", offsets, (experts + 1,), torch.int32, dev)
+
+
 def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None, stream=None):
     """The product a @ b.T of 8-bit values (torch.float8_e4m3fn) with a scale for
     each block of 128 of the last axis: a [..., K] with a_scale [..., blocks], b
@@ -796,25 +812,19 @@ def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None
     if stream is not None:
         return _on(stream, scaled_mm_fwd, a, a_scale, b, b_scale, offsets, out_dtype, out)
     dev = _device(a)
-    e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    if a.dim() < 1 or b.dim() != (2 if offsets is None else 3):
-        raise ValueError("b must be [N, K], or [experts, N, K] with offsets")
     shape = a.shape
-    K, N = shape[-1], b.shape[-2]
-    M = a.numel() // max(K, 1)
-    experts = 1 if offsets is None else b.shape[0]
-    _same("a", a, shape, e4m3, dev)
-    _same("b", b, b.shape[:-1] + (K,), e4m3, dev)
-    G = _blocks(K)
-    _same("a_scale", a_scale, shape[:-1] + (G,), f32, dev)
+    K, N = shape[-1] if shape else 0, b.shape[-2] if b.dim() > 1 else 0
+    M, G = a.numel() // max(K, 1), -(-K // 128)
     rows = b_scale.shape[-2] if b_scale.dim() > 1 else -1
-    if rows != N and rows != _blocks(N):
-        raise ValueError(f"b_scale must have {_blocks(N)} or {N} rows")
-    _same("b_scale", b_scale, b.shape[:-2] + (rows, G), f32, dev)
-    if offsets is not None:
-        if a.dim() != 2:
-            raise ValueError("a must be [rows, K] with offsets")
-        _same("offsets", offsets, (experts + 1,), torch.int32, dev)
+    experts = 1 if offsets is None else b.shape[0]
+    # What most calls are, in a few comparisons; the full checks name what is wrong with others.
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if not (a.dtype is e4m3 and b.dtype is e4m3 and a_scale.dtype is f32 and b_scale.dtype is f32 and K
+            and shape == (M, K) and b.shape == (N, K) and a_scale.shape == (M, G) and b_scale.shape == (rows, G)
+            and (rows == -(-N // 128) or rows == N) and offsets is None and a.is_contiguous() and b.is_contiguous()
+            and a_scale.is_contiguous() and b_scale.is_contiguous() and b.get_device() == dev
+            and a_scale.get_device() == dev and b_scale.get_device() == dev):
+        _scaled_mm_check(a, a_scale, b, b_scale, offsets, K, N, G, rows, experts, dev)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     if out_dtype is torch.bfloat16:
@@ -823,7 +833,7 @@ def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None
         code = QK_F32
     else:
         raise TypeError(f"unsupported out_dtype {out_dtype}: float32 or bfloat16 expected")
-    y_shape = shape[:-1] + (N,)
+    y_shape = (M, N) if len(shape) == 2 else shape[:-1] + (N,)
     y = torch.empty(y_shape, dtype=out_dtype, device=a.device) if out is None else _same("out", out, y_shape,
                                                                                         out_dtype, dev)
     nbytes = 0 if K % 16 == 0 else _workspace_bytes(qk_scaled_mm_workspace_size, dev, M, N, K, experts)
@@ -856,10 +866,12 @@ def expert_sort(experts, num_experts: int, stream=None):
 
 
 def _choices(slot, T, dev):
-    if slot.dim() != 2 or slot.shape[0] != T:
+    shape = slot.shape
+    if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"slot must be [{T}, k]")
-    _same("slot", slot, slot.shape, torch.int32, dev)
-    return slot.shape[1]
+    if slot.dtype is not torch.int32 or not slot.is_contiguous() or slot.get_device() != dev:
+        _same("slot", slot, shape, torch.int32, dev)
+    return shape[1]
 
 
 def expert_gather_fwd(x, slot, scale=None, out=None, out_scale=None, stream=None):
