@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[c + j] = fmaf(x[from + j], scale, v[c + j]);
         };
-#pragma unroll 1
+#pragma unroll
         for (int qi = 0; qi < kQuad; ++qi) {
           if (s + qi >= p.groups || !summed()) break;
           if constexpr (COLS) {
