@@ -415,6 +415,15 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
 // Tiles of 256 rows of a x 256 rows of b, a pair of CTAs each: a on TMEM's lanes,
 // so a thread multiplies with one scale of a and, where b's scales are of blocks
 // (!COLS), one of b: a block's sums cost a fused multiply-add each.
+//
+// What bounds it: the way of a block through TMEM, which holds two.  From a
+// product's issue to its sums' sight 1100 cycles (512 of them work), 370 to read
+// them, 350 until the issuing thread knows that they are read: 1900 for two blocks,
+// where the tensor cores would need 1024 (clock64 marks in one CTA, 4096 x 4864 x
+// 4096).  A block in two halves of 128 columns, read and freed each by itself, takes
+// longer, 543 us for 398 at 16384 x 8192 x 4096: narrow products are issued too slowly.
+// Then the tiles' ends: all CTAs write 128 KB a pair at about one time, 1.7 us a tile.
+// 16384 x 8192 x 4096: 398 us alone, 440 in a long run, 2500 to 2760 TFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kPairStages = 4, kPairStageBytes = 2 * 128 * kScaledStepK;  // one CTA's 128 rows of a and of b
 constexpr int kPairScaleSlots = 2;
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t idesc = instruction_desc_e4m3(256, at.n < p.n_full ? 256u : uint32_t(p.last_n));
         for (int32_t s = 0; s < p.groups; ++s, ++it) {
           const uint32_t buf = it & 1u;
-          const bool ok = wait(free0 + 8 * buf, ((it >> 1) & 1u) ^ 1u) && wait(full0 + 8 * st, turn);
+          const bool ok = wait(full0 + 8 * st, turn) && wait(free0 + 8 * buf, ((it >> 1) & 1u) ^ 1u);  // full long before
           if (!__all_sync(0xffffffffu, ok)) {
             failed = true;
             break;
