@@ -431,8 +431,8 @@ QK_API qk_status qk_linear_xent_bwd(const void* h, const void* w, const int64_t*
  * (The article names no 8-bit types; q and scale are as in qk_rmsnorm_quant_fwd.)
  * For each group, with qmax = 448 (QK_E4M3) or 127 (QK_INT8):
  *   scale = max(max |x| of the group, 2^-100) / qmax,
- *   q     = x / scale, rounded to nearest even (bfloat16: of the exact quotient
- *           x qmax / max |x|, so that what lies on a tie goes to even).
+ *   q     = x / scale: the quotient x qmax / max |x| as a rounded float32, rounded
+ *           to nearest even (what lies on a tie goes to even).
  * A group with an infinite or NaN x gets scale = NaN, and so does everything
  * that its q stand for.
  *

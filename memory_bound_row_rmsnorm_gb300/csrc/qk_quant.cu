@@ -56,7 +56,8 @@ __device__ __forceinline__ float widened(uint32_t w) {
 
 // What the values of one group are divided by: q = (x mul) / den with mul = qmax /
 // 2^k (448 = 7 / 8 2^9, 127 = 127 / 128 2^7) and den = max |x| / 2^k, so that the
-// quotient x qmax / max |x| is formed from exact numbers, not from a rounded scale.
+// quotient x qmax / max |x| is formed from exact numbers, not from a rounded scale,
+// which would move one float32 value in a million to the other side of a tie.
 struct Divisor {
   float den, inv;
 };
@@ -69,19 +70,15 @@ struct EightBitsOf {
     const float den = bad ? *scale : fmaxf(amax, kSmallestGroupMax) * kDown;
     return {den, 1.f / den};
   }
-  // The quotient, rounded so that rounding it once more to 8 bits gives what the
-  // exact one gives.  bf16: x mul is exact, and a quotient of 11 bits by 8 is a tie or
-  // 2^-13 of itself away from one.  float32: where the rounded quotient is even (a
-  // tie is) and not exact, it moves to the neighbour on the exact one's side.
+  // The quotient x qmax / max |x|, rounded to float32: what is rounded to 8 bits.  bf16:
+  // x mul is exact.  float32: what its rounding left out joins the division's remainder,
+  // so that the quotient is the rounded one all the same.
   template <typename T>
   __device__ __forceinline__ static float value(float x, Divisor d) {
     const float y = x * kMul;
     const float q = quotient(y, d.den, d.inv);
     if constexpr (sizeof(T) == 2) return q;
-    const float rest = fmaf(-q, d.den, y) + fmaf(x, kMul, -y);
-    int32_t b = __float_as_int(q);
-    if ((b & 1) == 0 && rest != 0.f && fabsf(q) > 0x1p-24f) b += (rest < 0.f) == (q < 0.f) ? 1 : -1;
-    return __int_as_float(b);
+    return fmaf(fmaf(-q, d.den, y) + fmaf(x, kMul, -y), d.inv, q);
   }
   // Two values in 8 bits.  float32: from products with the rounded reciprocal, off by
   // less than 2^-22, where all that lies within 2^-21 of them rounds alike (all but
