@@ -36,21 +36,23 @@ struct QuantArgs {
   int32_t vec_q, vec_qt;  // rows of q (of qt) are whole 8-byte units
 };
 
-// Bits of |x|, which compare as |x| does, with a NaN above all numbers: of four
-// floats, or of bf16 pairs in the halves of a word.
-template <typename T>
-__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
-  return w & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
-}
+// The larger magnitude of two words of elements, a float or a bf16 pair, whatever
+// its sign bits (magnitude() takes them off at the end); a NaN is larger than all.
 template <typename T>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
-  if constexpr (sizeof(T) == 4) return max(a, b);
-  return __vmaxu2(a, b);
+  uint32_t d;
+  if constexpr (sizeof(T) == 4) {
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  } else {
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  }
+  return d;
 }
-// The largest of a word's elements, as a float.
+// The largest magnitude among a word's elements, as a float.
 template <typename T>
-__device__ __forceinline__ float widened(uint32_t w) {
-  if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+__device__ __forceinline__ float magnitude(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w & 0x7fffffffu);
+  w &= 0x7fff7fffu;
   return __uint_as_float(max(w & 0xffff0000u, w << 16));
 }
 
@@ -80,30 +82,51 @@ struct EightBitsOf {
     if constexpr (sizeof(T) == 2) return q;
     return fmaf(fmaf(-q, d.den, y) + fmaf(x, kMul, -y), d.inv, q);
   }
-  // Two values in 8 bits.  float32: from products with the rounded reciprocal, off by
+  // Four floats in 8 bits, the first in the low byte.
+  __device__ __forceinline__ static uint32_t packed(const float* f) {
+    if constexpr (Q == QK_INT8) return quantise2(f[0], f[1], Q) | quantise2(f[2], f[3], Q) << 16;
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
+    return w;
+  }
+  // Four values of a group.  float32: from products with the rounded reciprocal, off by
   // less than 2^-22, where all that lies within 2^-21 of them rounds alike (all but
   // one value in 30000), else from the quotients (16384 x 4096 both ways with half
   // the threads: 139 us, from the quotients always 152).
   template <typename T>
-  __device__ __forceinline__ static uint32_t two(float a, float b, Divisor d) {
+  __device__ __forceinline__ static uint32_t four(const float* x, Divisor d) {
+    float f[4];
     if constexpr (sizeof(T) == 4) {
-      const float inv = kMul * d.inv, below = 1.f - 0x1p-21f, above = 1.f + 0x1p-21f;
-      const float qa = a * inv, qb = b * inv;
-      const uint32_t w = quantise2(qa * below, qb * below, Q);
-      if (w == quantise2(qa * above, qb * above, Q)) return w;
+      const float inv = kMul * d.inv;
+      float g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float q = x[i] * inv;
+        f[i] = q * (1.f - 0x1p-21f);
+        g[i] = q * (1.f + 0x1p-21f);
+      }
+      const uint32_t w = packed(f);
+      if (w == packed(g)) return w;
     }
-    return quantise2(value<T>(a, d), value<T>(b, d), Q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = value<T>(x[i], d);
+    return packed(f);
   }
 };
 
-// One row of `n` (8 or 4) values in 8 bits, from the values as floats.
+// E (8 or 4) values in 8 bits, of which `left` count.
+template <int E>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t* words) {
+  if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(words[0], words[1]);
+  else *reinterpret_cast<uint32_t*>(p) = words[0];
+}
 template <int E>
 __device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* words, int left, bool vec) {
-  if (vec && left >= E) {
-    if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(words[0], words[1]);
-    else *reinterpret_cast<uint32_t*>(p) = words[0];
-    return;
-  }
+  if (vec && left >= E) return store_words<E>(p, words);
 #pragma unroll
   for (int j = 0; j < E; ++j)
     if (j < left) p[j] = uint8_t(words[j / 4] >> (8 * (j % 4)));
@@ -150,8 +173,7 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
   uint4 col_top = make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint4 m = make_uint4(magnitudes<T>(raw[r].x), magnitudes<T>(raw[r].y), magnitudes<T>(raw[r].z),
-                               magnitudes<T>(raw[r].w));
+    const uint4 m = raw[r];
     row_top[r] = larger<T>(larger<T>(m.x, m.y), larger<T>(m.z, m.w));
     col_top = make_uint4(larger<T>(col_top.x, m.x), larger<T>(col_top.y, m.y), larger<T>(col_top.z, m.z),
                          larger<T>(col_top.w, m.w));
@@ -179,7 +201,7 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
   }
 #pragma unroll
   for (int o = kShare / 2; o >= 1; o /= 2) row_top[0] = larger<T>(row_top[0], __shfl_xor_sync(0xffffffffu, row_top[0], o));
-  const float own = widened<T>(row_top[0]);  // of row (lane % kLanes) / kShare of this group of lanes
+  const float own = magnitude<T>(row_top[0]);  // of row (lane % kLanes) / kShare of this group of lanes
   float scale;
   Divisor block = {1.f, 1.f};
   if (a.block) {
@@ -203,17 +225,19 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
       const int row = r0 + (lane % kLanes) / kShare;
       if (lane % kShare == 0 && row < rows) a.scale[(i0 + row) * a.col_tiles + nt] = scale;
     }
+    uint8_t* q = a.q + (i0 + r0) * a.N + j0 + c0;
+    const bool inside = a.vec_q && rows == kTile && cols == kTile;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r, q += a.N) {
       const int from = (lane & ~(kLanes - 1)) + kShare * r;
       const Divisor d = {__shfl_sync(0xffffffffu, mine.den, from), __shfl_sync(0xffffffffu, mine.inv, from)};
       float f[E];
       V::unpack(raw[r], f);
       uint32_t words[E / 4];
 #pragma unroll
-      for (int j = 0; j < E; j += 4)
-        words[j / 4] = B::template two<T>(f[j], f[j + 1], d) | B::template two<T>(f[j + 2], f[j + 3], d) << 16;
-      if (r0 + r < rows) store_bytes<E>(a.q + (i0 + r0 + r) * a.N + j0 + c0, words, cols - c0, a.vec_q);
+      for (int j = 0; j < E; j += 4) words[j / 4] = B::template four<T>(f + j, d);
+      if (inside) store_words<E>(q, words);
+      else if (r0 + r < rows) store_bytes<E>(q, words, cols - c0, a.vec_q);
     }
   }
   if (a.qt == nullptr) return;
@@ -224,8 +248,8 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
       uint32_t top = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if constexpr (sizeof(T) == 4) top = max(top, reinterpret_cast<const uint32_t*>(tops[w])[c]);
-        else top = max(top, uint32_t(reinterpret_cast<const uint16_t*>(tops[w])[c]) << 16);
+        if constexpr (sizeof(T) == 4) top = max(top, reinterpret_cast<const uint32_t*>(tops[w])[c] & 0x7fffffffu);
+        else top = max(top, (uint32_t(reinterpret_cast<const uint16_t*>(tops[w])[c]) & 0x7fffu) << 16);
       }
       columns[c] = B::divisor(__uint_as_float(top), &scale);
       if (c < cols) a.scale_t[(j0 + c) * row_tiles + mt] = scale;
@@ -238,24 +262,31 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
   for (int j = 0; j < E; ++j) {
     const Divisor d = a.block ? block : columns[c0 + j];
     const int unit_key = (c0 + j) >> 3;
-    uint32_t words[2] = {0, 0};
+    uint32_t words[2];
 #pragma unroll
-    for (int r = 0; r < R; r += 2) {
-      float f[E], g[E];
-      V::unpack(raw[r], f);
-      V::unpack(raw[r + 1], g);
-      words[r / 4] |= B::template two<T>(f[j], g[j], d) << (8 * (r % 4));
+    for (int r = 0; r < R; r += 4) {
+      float column[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[E];
+        V::unpack(raw[r + i], f);
+        column[i] = f[j];
+      }
+      words[r / 4] = B::template four<T>(column, d);
     }
     *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + (((r0 >> 3) ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
   }
   __syncthreads();
+  const int unit = lane & 15, first = warp * 2 + (lane >> 4);
+  uint8_t* qt = a.qt + (j0 + first) * a.M + i0 + unit * 8;
+  const bool inside = a.vec_qt && rows == kTile && cols == kTile;
 #pragma unroll
-  for (int k = 0; k < kTile / 2 / kWarps; ++k) {
-    const int col = (k * kWarps + warp) * 2 + (lane >> 4), unit = lane & 15;
+  for (int k = 0; k < kTile / 2 / kWarps; ++k, qt += 2 * kWarps * a.M) {
+    const int col = first + k * 2 * kWarps;
     const uint2 w = *reinterpret_cast<const uint2*>(turned + col * kTile + ((unit ^ (col >> 3)) & 15) * 8);
     const uint32_t words[2] = {w.x, w.y};
-    if (col < cols && unit * 8 < rows)
-      store_bytes<8>(a.qt + (j0 + col) * a.M + i0 + unit * 8, words, rows - unit * 8, a.vec_qt);
+    if (inside) store_words<8>(qt, words);
+    else if (col < cols && unit * 8 < rows) store_bytes<8>(qt, words, rows - unit * 8, a.vec_qt);
   }
 }
 
