@@ -104,16 +104,26 @@ struct EightBitsOf {
       const float inv = kMul * d.inv;
       float g[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float q = x[i] * inv;
-        f[i] = q * (1.f - 0x1p-21f);
-        g[i] = q * (1.f + 0x1p-21f);
+      for (int i = 0; i < 4; i += 2) {
+        const float2 q = mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv));
+        const float2 lo = mul2(q, make_float2(1.f - 0x1p-21f, 1.f - 0x1p-21f)),
+                     hi = mul2(q, make_float2(1.f + 0x1p-21f, 1.f + 0x1p-21f));
+        f[i] = lo.x, f[i + 1] = lo.y, g[i] = hi.x, g[i + 1] = hi.y;
       }
       const uint32_t w = packed(f);
       if (w == packed(g)) return w;
     }
+    if constexpr (sizeof(T) == 2) {  // value() in packed pairs: what bounds the kernel is the number of instructions
+      const float2 mul = make_float2(kMul, kMul), inv = make_float2(d.inv, d.inv), less = make_float2(-d.den, -d.den);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = value<T>(x[i], d);
+      for (int i = 0; i < 4; i += 2) {
+        const float2 y = mul2(make_float2(x[i], x[i + 1]), mul), q = mul2(y, inv), r = fma2(fma2(q, less, y), inv, q);
+        f[i] = r.x, f[i + 1] = r.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = value<T>(x[i], d);
+    }
     return packed(f);
   }
 };
