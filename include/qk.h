@@ -469,7 +469,7 @@ QK_API qk_status qk_quant_fwd(const void* x, void* q, float* scale, void* qt, fl
  *              scratch; may be NULL when that is 0.  It is 0 when K is a multiple of
  *              16; a and b must then be 16-byte aligned.  Otherwise a and b go
  *              through it, in rows that start on 16 bytes.
- *   M, N, K at most 2^31 - 16, experts at most 1024 (QK_ERR_UNSUPPORTED beyond).
+ *   M, N, K at most 2^31 - 1024, experts at most 1024 (QK_ERR_UNSUPPORTED beyond).
  *   A block's sum is float32, is multiplied with the product of its two scales
  *   and added to nearest in float32.  Results do not change from run to run.  A
  *   NaN value or scale reaches the outputs of its row (of its column) only.  Where

@@ -854,6 +854,8 @@ def expert_sort(experts, num_experts: int, stream=None):
     dev = _device(experts)
     if experts.dim() != 2 or not experts.is_contiguous() or experts.dtype not in (torch.int32, torch.int64):
         raise ValueError("experts must be a contiguous int32 or int64 tensor [T, k]")
+    if num_experts < 1:
+        raise ValueError("num_experts must be positive")
     T, k = experts.shape
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=experts.device)
     slot = torch.empty((T, k), dtype=torch.int32, device=experts.device)

@@ -344,8 +344,8 @@ qk_status check_choices(int64_t T, int64_t k) {
   if (T > kMaxChoices / k) return QK_ERR_UNSUPPORTED;
   return QK_OK;
 }
-// CTAs of a sort of n choices.  Up to 2048 one, in one launch (4096: 6.2 us, 4.7 in two
-// launches of 8).  Beyond, each CTA adds up the counts of all: 32 CTAs where 1024 choices
+// CTAs of a sort of n choices.  Up to 2048 one, in one launch (4096: 6.2 us, 5.0 in two
+// launches of 4).  Beyond, each CTA adds up the counts of all: 32 CTAs where 1024 choices
 // each are enough (16384: 5.5 us, with 2048 or 4096 each 6.1 and 7.8), 128 at most (65536:
 // 7.2 us with 32 CTAs, 7.6 with 64; 524288: 13.3 with 128, 14.6 with 152).
 int64_t sort_blocks(int64_t n) {

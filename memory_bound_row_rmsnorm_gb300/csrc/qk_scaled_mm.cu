@@ -17,7 +17,8 @@
 namespace qk {
 namespace {
 
-constexpr int64_t kMaxDim = INT32_MAX - 15;  // TMA coordinates, and rows padded to 16, are 32-bit
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;  // TMA coordinates, a tile's behind the last row too, are 32-bit
+constexpr int64_t kMostTiles = int64_t(1) << 30;         // and so are tile numbers
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
@@ -39,6 +40,7 @@ qk_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t experts) {
   if (M < 0 || N <= 0 || K <= 0 || experts <= 0) return QK_ERR_INVALID_ARG;
   if (M > kMaxDim || N > kMaxDim || K > kMaxDim || experts > kMaxExperts) return QK_ERR_UNSUPPORTED;
   if (std::max(M, N * experts) > INT64_MAX / 1024 / std::max(N, K)) return QK_ERR_UNSUPPORTED;  // byte offsets fit int64
+  if (ceil_div(N, 256) > kMostTiles / (ceil_div(M, 256) + experts)) return QK_ERR_UNSUPPORTED;
   return QK_OK;
 }
 
@@ -139,8 +141,6 @@ qk_status launch(const Call& c, K kernel, int64_t grid, int threads, int cluster
   return QK_OK;
 }
 
-constexpr int64_t kMostTiles = int64_t(1) << 30;  // tile numbers are 32-bit
-
 // Clusters of 2, 4 and 8 CTAs of a tile kernel that a device holds at a time
 // (clusters lie within a GPC, so 8 take fewer of the SMs).
 struct Clusters {
@@ -222,7 +222,6 @@ TilePlan plan_tiles(const Call& c) {
 
 template <int TN, typename T>
 qk_status launch_tiles(const Call& c, const TilePlan& plan) {
-  if (plan.tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
   ScaledArgs p = arguments(c);
   p.n_tiles = int32_t(ceil_div(c.N, 128));
   p.split_steps = int32_t(ceil_div(p.groups, plan.ranks));
@@ -246,7 +245,6 @@ qk_status launch_pairs(const Call& c) {
   p.n_full = p.last_n == 256 ? p.n_tiles : p.n_tiles - 1;
   p.y_vec = c.N * int64_t(sizeof(T)) % 16 == 0 && aligned16(c.y);
   const int64_t tiles = most_tiles(c, 256) * p.n_tiles;
-  if (tiles > kMostTiles) return QK_ERR_UNSUPPORTED;
   CUtensorMap ma, mb, my = {};
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128) ||
       (p.y_vec && !make_out_map(&my, c, int(sizeof(T)))))

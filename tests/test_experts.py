@@ -274,7 +274,7 @@ def test_helper_refusals(cuda):
     x, slot = torch.zeros(4, 8, device=DEV), torch.zeros(4, 2, dtype=torch.int32, device=DEV)
     w = torch.zeros(4, 2, device=DEV)
     rows = torch.zeros(8, 8, device=DEV)
-    for call in (lambda: qb.expert_sort(slot.float(), 4), lambda: qb.expert_sort(slot[0], 4),
+    for call in (lambda: qb.expert_sort(slot.float(), 4), lambda: qb.expert_sort(slot, 0), lambda: qb.expert_sort(slot[0], 4),
                  lambda: qb.expert_sort(slot.T, 4), lambda: qb.expert_sort(slot.cpu(), 4),
                  lambda: qb.expert_gather_fwd(x, slot[:3]), lambda: qb.expert_gather_fwd(x, slot.long()),
                  lambda: qb.expert_gather_fwd(x.T, slot), lambda: qb.expert_gather_fwd(x, slot, out=rows.double()),

@@ -269,6 +269,7 @@ def test_refusals(lib):
     assert call(y=A) == bad and call(y=A + (3 << 24)) == bad
     assert call(offsets=A + (5 << 24), experts=1025) == qb.QK_ERR_UNSUPPORTED
     assert call(M=2 ** 31) == qb.QK_ERR_UNSUPPORTED
+    assert call(M=2 ** 31 - 2000, N=2 ** 31 - 2000, K=16) == qb.QK_ERR_UNSUPPORTED  # more tiles than are counted
     assert call(M=0, a=None, y=None) == qb.QK_OK
     assert qb.qk_scaled_mm_workspace_size(5, 7, 100, 3) == (5 + 21) * 112
     assert qb.qk_scaled_mm_workspace_size(5, 7, 160, 3) == 0
