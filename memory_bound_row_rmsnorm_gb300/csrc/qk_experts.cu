@@ -152,11 +152,8 @@ struct GatherArgs {
   int32_t k, groups;
 };
 
-constexpr int kGatherWords = 8;  // words of a lane: 4 KB a warp (16384 x 4 of 4096 bf16: 103 us, with 4 105)
-
-template <typename W>
+template <typename W, int WORDS>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
-  constexpr int kUnroll = kGatherWords;
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
@@ -164,21 +161,31 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
     const int64_t t = u / a.pieces, piece = u - t * a.pieces;
     const W* src = reinterpret_cast<const W*>(a.x + t * a.row_bytes);
-    const int64_t w0 = piece * (32 * kUnroll) + lane;
-    W v[kUnroll];
+    const int64_t w0 = piece * (32 * WORDS) + lane;
+    W v[WORDS];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
+    for (int i = 0; i < WORDS; ++i)
       if (w0 + 32 * i < words) v[i] = src[w0 + 32 * i];
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t at = a.slot[t * a.k + j];
-      if (at < 0 || at >= a.P) continue;
-      W* dst = reinterpret_cast<W*>(a.rows + int64_t(at) * a.row_bytes);
+    for (int j0 = 0; j0 < a.k; j0 += 32) {  // the places of 32 choices, a lane each
+      const int count = min(32, a.k - j0);
+      const int32_t place = lane < count ? a.slot[t * a.k + j0 + lane] : -1;
+      for (int j = 0; j < count; ++j) {
+        const int32_t at = __shfl_sync(0xffffffffu, place, j);
+        if (at < 0 || at >= a.P) continue;
+        W* dst = reinterpret_cast<W*>(a.rows + int64_t(at) * a.row_bytes);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
-        if (w0 + 32 * i < words) dst[w0 + 32 * i] = v[i];
-      if (piece == 0)
-        for (int g = lane; g < a.groups; g += 32)
-          a.row_scale[int64_t(at) * a.groups + g] = a.scale[t * a.groups + g];
+        for (int i = 0; i < WORDS; ++i)
+          if (w0 + 32 * i < words) dst[w0 + 32 * i] = v[i];
+      }
+      if (piece != 0) continue;
+      for (int g0 = 0; g0 < a.groups; g0 += 32) {
+        const int g = g0 + lane;
+        const float s = g < a.groups ? a.scale[t * a.groups + g] : 0.f;
+        for (int j = 0; j < count; ++j) {
+          const int32_t at = __shfl_sync(0xffffffffu, place, j);
+          if (at >= 0 && at < a.P && g < a.groups) a.row_scale[int64_t(at) * a.groups + g] = s;
+        }
+      }
     }
   }
 }
@@ -480,14 +487,19 @@ qk_status qk_expert_gather_fwd(const void* x, const float* scale, const int32_t*
                   T, P, row_bytes, 0, int32_t(k), int32_t(groups)};
   // The widest word that rows consist of.
   const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | uintptr_t(row_bytes);
-  auto launch = [&](auto kernel, int64_t word) {
-    a.pieces = ceil_div(row_bytes / word, 32 * kGatherWords);
-    return launch_pdl(kernel, dim3(warps_grid(d, T * a.pieces)), 256, 0, stream, a);
+  auto launch = [&](auto many, auto few, int64_t word) {
+    // Eight words a lane where that fills the GPU (16384 x 4 of 4096 bf16: 103 us, with four
+    // words 105); two for a few rows, whose time is latency (16 x 4 of 4096 bytes:
+    // 2.6 us, with eight 4.0).
+    const int64_t words = row_bytes / word;
+    const bool wide = T * ceil_div(words, 256) >= int64_t(d.sms) * 8;
+    a.pieces = ceil_div(words, wide ? 256 : 64);
+    return launch_pdl(wide ? many : few, dim3(warps_grid(d, T * a.pieces)), 256, 0, stream, a);
   };
-  if (all % 16 == 0) return launch(gather_kernel<uint4>, 16);
-  if (all % 4 == 0) return launch(gather_kernel<uint32_t>, 4);
-  if (all % 2 == 0) return launch(gather_kernel<uint16_t>, 2);
-  return launch(gather_kernel<uint8_t>, 1);
+  if (all % 16 == 0) return launch(gather_kernel<uint4, 8>, gather_kernel<uint4, 2>, 16);
+  if (all % 4 == 0) return launch(gather_kernel<uint32_t, 8>, gather_kernel<uint32_t, 2>, 4);
+  if (all % 2 == 0) return launch(gather_kernel<uint16_t, 8>, gather_kernel<uint16_t, 2>, 2);
+  return launch(gather_kernel<uint8_t, 8>, gather_kernel<uint8_t, 2>, 1);
 }
 
 qk_status qk_expert_combine_fwd(const void* rows, const int32_t* slot, const float* weights, void* y, int64_t T,
