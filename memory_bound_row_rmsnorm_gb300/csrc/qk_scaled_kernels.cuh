@@ -416,14 +416,14 @@ __global__ void __launch_bounds__(kScaledThreads, 1)
 // so a thread multiplies with one scale of a and, where b's scales are of blocks
 // (!COLS), one of b: a block's sums cost a fused multiply-add each.
 //
-// What bounds it: the way of a block through TMEM, which holds two.  From a
-// product's issue to its sums' sight 1100 cycles (512 of them work), 370 to read
-// them, 350 until the issuing thread knows that they are read: 1900 for two blocks,
+// What bounds it: the way of a block through TMEM, which holds two.  From a block's
+// first product to its sums' sight 740 cycles (512 of them work), 340 to read them,
+// 600 until the issuing thread knows that all 16 warps have: 1680 for two blocks,
 // where the tensor cores would need 1024 (clock64 marks in one CTA, 4096 x 4864 x
 // 4096).  A block in two halves of 128 columns, read and freed each by itself, takes
-// longer, 543 us for 398 at 16384 x 8192 x 4096: narrow products are issued too slowly.
+// longer, 543 us for 398 at 16384 x 8192 x 4096.
 // Then the tiles' ends: all CTAs write 128 KB a pair at about one time, 1.7 us a tile.
-// 16384 x 8192 x 4096: 398 us alone, 440 in a long run, 2500 to 2760 TFLOP/s.
+// 16384 x 8192 x 4096: 396 us alone, 436 in a long run, 2520 to 2780 TFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kPairStages = 4, kPairStageBytes = 2 * 128 * kScaledStepK;  // one CTA's 128 rows of a and of b
 constexpr int kPairScaleSlots = 2;
