@@ -87,7 +87,11 @@ def run(a, sa, b, sb, out, offsets=None, off=0):
 SIZES = [(1, 1, 1), (1, 128, 128), (2, 5, 3), (1, 4096, 512), (3, 300, 16), (7, 129, 1040), (15, 127, 17), (16, 256, 256),
          (17, 64, 4096), (31, 1000, 100), (33, 130, 384), (64, 512, 640), (65, 96, 127), (100, 16, 2048), (127, 200, 129),
          (128, 128, 128), (129, 257, 255), (200, 1023, 272), (255, 255, 1000), (256, 256, 512), (257, 385, 513),
-         (300, 700, 1152), (513, 40, 96), (700, 2000, 144), (1030, 1100, 320)]
+         (300, 700, 1152), (513, 40, 96), (700, 2000, 144), (1030, 1100, 320),
+         # pairs of CTAs: odd rows, last column tiles of every width class, steps that are no whole quads
+         (520, 2089, 640), (777, 2112, 1040), (1025, 1184, 129), (600, 2337, 100), (1500, 1600, 272), (1001, 2047, 1023),
+         # tiles of 128 rows of a, alone and with k shared by a cluster
+         (374, 1801, 4144), (218, 3612, 3950), (256, 4096, 4096)]
 
 
 @gpu
@@ -116,10 +120,7 @@ GROUPS = [([1], 0, 0), ([0, 0, 3], 0, 0), ([5, 0, 16, 17, 1], 0, 4), ([0, 0, 0],
           ([700, 2], 0, 1), ([3] * 40, 1, 2), ([1, 0] * 100, 0, 0), ([257, 256, 255, 0, 1], 0, 0)]
 
 
-@gpu
-@pytest.mark.parametrize("counts,before,behind", GROUPS)
-@pytest.mark.parametrize("N,K", [(200, 144), (384, 1280), (129, 77)])
-def test_rows_by_expert(cuda, counts, before, behind, N, K):
+def rows_by_expert(counts, before, behind, N, K):
     offsets, end = cut(counts, before)
     M, E = end + behind, len(counts)
     for b_rows in (128, 1):
@@ -131,6 +132,43 @@ def test_rows_by_expert(cuda, counts, before, behind, N, K):
             assert torch.equal(y[lo:hi].double(), ref), f"expert {e} of {counts}"
         left = torch.cat([y[:before], y[end:]]).view(torch.uint8)
         assert (left == 0xA5).all(), "rows of no expert were written"
+
+
+@gpu
+@pytest.mark.parametrize("counts,before,behind", GROUPS)
+@pytest.mark.parametrize("N,K", [(200, 144), (384, 1280), (129, 77)])
+def test_rows_by_expert(cuda, counts, before, behind, N, K):
+    rows_by_expert(counts, before, behind, N, K)
+
+
+MANY = [([700, 257, 0, 900, 31], 3, 2, 2080, 1280), ([300] * 6, 0, 5, 2200, 1100), ([513, 40, 800], 1, 0, 1999, 384),
+        ([129, 256, 1, 700], 0, 0, 2600, 200), ([120] * 8, 2, 2, 2050, 1500), ([180, 155], 0, 1, 2391, 4128),
+        ([700, 600, 65, 0, 300], 0, 0, 1500, 640)]
+
+
+@gpu
+@pytest.mark.parametrize("counts,before,behind,N,K", MANY)
+def test_many_rows_by_expert(cuda, counts, before, behind, N, K):
+    rows_by_expert(counts, before, behind, N, K)
+
+
+@gpu
+def test_operands_beyond_32_bits(cuda):
+    K, N = 16384, 72
+    a, sa, b, sb = make(1000, N, K, 71, whole=True)
+    M = 270000  # 4.4e9 bytes of a
+    big, scales = a.repeat(M // 1000, 1), sa.repeat(M // 1000, 1)
+    y = qb.scaled_mm_fwd(big, scales, b, sb, out_dtype=torch.float32)
+    ref = reference(a, sa, b, sb)[0]
+    for first in (0, 130000, M - 1000):
+        assert torch.equal(y[first:first + 1000].double(), ref)
+    del big, scales, y
+    E, N = 70, 4096  # 4.7e9 bytes of b
+    a, sa, b, sb = make(9, N, K, 72, whole=True)
+    offsets = torch.zeros(E + 1, dtype=torch.int32)
+    offsets[1:], offsets[E] = 4, 9  # the first expert and the last
+    y = qb.scaled_mm_fwd(a, sa, b.expand(E, N, K).contiguous(), sb.expand(E, *sb.shape).contiguous(), offsets.to(DEV))
+    assert torch.equal(y, reference(a, sa, b, sb)[0].to(y.dtype))
 
 
 @gpu
