@@ -204,28 +204,56 @@ struct CombineArgs {
   int32_t k;
 };
 
-// A vector of values from p, of which `left` count.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_raw(const T* p, int64_t left) {
-  using V = Vec16<T>;
-  if constexpr (VEC) {
-    return *reinterpret_cast<const uint4*>(p);
+// A lane's 16 bytes of a row of N values, from a warp's piece of 512 bytes that begins at
+// value `piece`: one vector where rows consist of those (WORD 16; the caller leaves
+// lanes behind the row out), else words of 4 or 2 bytes.  ACROSS: a warp's lanes have
+// neighbouring words, so that stores touch whole sectors (16384 x 4 of 4095 bf16,
+// backward: 367 us, with a lane's words side by side 799).  Side by side suits
+// loads of 2 bytes, whose first brings what the others need (forward: 220 and 313 us).
+template <typename T, int WORD>
+using Word = std::conditional_t<WORD == 16, uint4, std::conditional_t<WORD == 4, uint32_t, uint16_t>>;
+template <typename T, int WORD, bool ACROSS>
+__device__ __forceinline__ int word_at(int lane, int i) {  // the i-th word's first value in the piece
+  constexpr int kWords = 16 / WORD, kValues = WORD / int(sizeof(T));
+  return (ACROSS ? lane + 32 * i : kWords * lane + i) * kValues;
+}
+template <typename T, int WORD, bool ACROSS>
+__device__ __forceinline__ uint4 load_raw(const T* row, int64_t piece, int lane, int64_t N) {
+  using W = Word<T, WORD>;
+  const T* p = row + piece;
+  if constexpr (WORD == 16) {
+    return *reinterpret_cast<const W*>(p + word_at<T, WORD, ACROSS>(lane, 0));
   } else {
-    float f[V::kElems];
+    const int left = int(min(int64_t(512 / sizeof(T)), N - piece));  // values of the piece
+    W v[16 / WORD];
 #pragma unroll
-    for (int j = 0; j < V::kElems; ++j) f[j] = j < left ? V::load1(p + j) : 0.f;
-    return V::pack(f);  // exact: the values are T's
+    for (int i = 0; i < 16 / WORD; ++i) {
+      const int at = word_at<T, WORD, ACROSS>(lane, i);
+      v[i] = at < left ? *reinterpret_cast<const W*>(p + at) : W(0);
+    }
+    if constexpr (WORD == 4) return make_uint4(v[0], v[1], v[2], v[3]);
+    else
+      return make_uint4(v[0] | uint32_t(v[1]) << 16, v[2] | uint32_t(v[3]) << 16, v[4] | uint32_t(v[5]) << 16,
+                        v[6] | uint32_t(v[7]) << 16);
   }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_values(T* p, int64_t left, const float* f) {
-  using V = Vec16<T>;
-  if constexpr (VEC) {
-    *reinterpret_cast<uint4*>(p) = V::pack(f);
+template <typename T, int WORD, bool ACROSS>
+__device__ __forceinline__ void store_raw(T* row, int64_t piece, int lane, int64_t N, const float* f) {
+  using W = Word<T, WORD>;
+  const uint4 v = Vec16<T>::pack(f);
+  T* p = row + piece;
+  if constexpr (WORD == 16) {
+    *reinterpret_cast<W*>(p + word_at<T, WORD, ACROSS>(lane, 0)) = v;
   } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int left = int(min(int64_t(512 / sizeof(T)), N - piece));
 #pragma unroll
-    for (int j = 0; j < V::kElems; ++j)
-      if (j < left) V::store1(p + j, f[j]);
+    for (int i = 0; i < 16 / WORD; ++i) {
+      const int at = word_at<T, WORD, ACROSS>(lane, i);
+      if (at >= left) continue;
+      if constexpr (WORD == 4) *reinterpret_cast<W*>(p + at) = w[i];
+      else *reinterpret_cast<W*>(p + at) = W(w[i / 2] >> (16 * (i & 1)));
+    }
   }
 }
 
@@ -234,16 +262,17 @@ __device__ __forceinline__ void store_values(T* p, int64_t left, const float* f)
 constexpr int kAtOnce = 4;
 
 // A warp forms a piece of a token's row; the sum runs over the choices in order.
-template <typename T, bool VEC>
+template <typename T, int WORD>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   constexpr int E = Vec16<T>::kElems;
+  constexpr bool ACROSS = WORD != 2;
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
   const int64_t units = a.T * a.pieces;
   for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
-    const int64_t t = u / a.pieces, c = ((u - t * a.pieces) * 32 + lane) * E;
-    if (c >= a.N) continue;
+    const int64_t t = u / a.pieces, piece = (u - t * a.pieces) * (32 * E);
+    if (WORD == 16 && piece + lane * E >= a.N) continue;
     float sum[E] = {};
     for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
       int32_t at[kAtOnce];
@@ -257,7 +286,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
-        if (at[j] >= 0) f[j] = load_raw<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N + c, a.N - c);
+        if (at[j] >= 0) f[j] = load_raw<T, WORD, ACROSS>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N, piece, lane, a.N);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         if (at[j] < 0) continue;
@@ -267,7 +296,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
         for (int i = 0; i < E; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
       }
     }
-    store_values<T, VEC>(static_cast<T*>(a.out) + t * a.N + c, a.N - c, sum);
+    store_raw<T, WORD, ACROSS>(static_cast<T*>(a.out) + t * a.N, piece, lane, a.N, sum);
   }
 }
 
@@ -276,7 +305,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
 // threads at the end.  The registers are held down for the sake of CTAs an SM
 // (16384 tokens of 4096 bf16, two choices: 142 us with three, 115 with five, 111
 // with six and AT = 2; four choices: 201, 183, 189).
-template <typename T, bool VEC, int THREADS, int AT>
+template <typename T, int WORD, int THREADS, int AT>
 __global__ void __launch_bounds__(256, AT == 2 ? 6 : 5) combine_bwd_kernel(const CombineArgs a) {
   constexpr int E = Vec16<T>::kElems, kWarps = THREADS / 32, kTokens = 256 / THREADS;
   __shared__ float red[2][AT][kWarps];
@@ -295,12 +324,13 @@ __global__ void __launch_bounds__(256, AT == 2 ? 6 : 5) combine_bwd_kernel(const
         if (at[j] >= a.P) at[j] = -1;
         w[j] = at[j] >= 0 ? a.weights[t * a.k + j0 + j] : 0.f;
       }
-      for (int64_t c = tid * E; c < a.N; c += THREADS * E) {
-        const uint4 graw = load_raw<T, VEC>(dy + c, a.N - c);
+      for (int64_t piece = warp * (32 * E); piece < a.N; piece += THREADS * E) {
+        if (WORD == 16 && piece + lane * E >= a.N) break;
+        const uint4 graw = load_raw<T, WORD, true>(dy, piece, lane, a.N);
         uint4 f[AT];
 #pragma unroll
         for (int j = 0; j < AT; ++j)
-          if (at[j] >= 0) f[j] = load_raw<T, VEC>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N + c, a.N - c);
+          if (at[j] >= 0) f[j] = load_raw<T, WORD, true>(static_cast<const T*>(a.rows) + int64_t(at[j]) * a.N, piece, lane, a.N);
         float g[E];
         Vec16<T>::unpack(graw, g);
 #pragma unroll
@@ -313,7 +343,7 @@ __global__ void __launch_bounds__(256, AT == 2 ? 6 : 5) combine_bwd_kernel(const
             dot[j] = fmaf(g[i], v[i], dot[j]);
             v[i] = g[i] * w[j];
           }
-          store_values<T, VEC>(static_cast<T*>(a.out) + int64_t(at[j]) * a.N + c, a.N - c, v);
+          store_raw<T, WORD, true>(static_cast<T*>(a.out) + int64_t(at[j]) * a.N, piece, lane, a.N, v);
         }
       }
       if (a.dweights == nullptr) continue;
@@ -379,23 +409,26 @@ bool any_overlap(const Buffer (&out)[NO], const Buffer (&in)[NI]) {
   return false;
 }
 
+template <typename T, int WORD>
+qk_status launch_combine(const CurrentDevice& d, bool bwd, const CombineArgs& a, void* stream) {
+  if (!bwd) return launch_pdl(combine_kernel<T, WORD>, dim3(warps_grid(d, a.T * a.pieces)), 256, 0, stream, a);
+  // A warp a token where a CTA would have less than a vector a thread.
+  const bool narrow = a.N <= 256 * Vec16<T>::kElems / 4;
+  const auto kernel = a.k <= 2 ? (narrow ? combine_bwd_kernel<T, WORD, 32, 2> : combine_bwd_kernel<T, WORD, 256, 2>)
+                               : (narrow ? combine_bwd_kernel<T, WORD, 32, 4> : combine_bwd_kernel<T, WORD, 256, 4>);
+  const int64_t blocks = narrow ? ceil_div(a.T, 8) : a.T;
+  return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(blocks, int64_t(d.sms) * 32))), 256, 0, stream, a);
+}
+// By the widest word that all rows consist of.
 template <typename T>
-qk_status launch_combine(const CurrentDevice& d, bool bwd, bool vec, CombineArgs a, void* stream) {
+qk_status launch_combine(const CurrentDevice& d, bool bwd, CombineArgs a, void* stream) {
   a.pieces = ceil_div(a.N, 32 * Vec16<T>::kElems);
-  if (bwd) {
-    // A warp a token where a CTA would have less than a vector a thread.
-    const bool narrow = a.N <= 256 * Vec16<T>::kElems / 4;
-    const auto pick = [&](auto at) {
-      constexpr int AT = decltype(at)::value;
-      return narrow ? (vec ? combine_bwd_kernel<T, true, 32, AT> : combine_bwd_kernel<T, false, 32, AT>)
-                    : (vec ? combine_bwd_kernel<T, true, 256, AT> : combine_bwd_kernel<T, false, 256, AT>);
-    };
-    const auto kernel = a.k <= 2 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 4>());
-    return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(narrow ? ceil_div(a.T, 8) : a.T, int64_t(d.sms) * 32))), 256, 0,
-                      stream, a);
-  }
-  const auto kernel = vec ? combine_kernel<T, true> : combine_kernel<T, false>;
-  return launch_pdl(kernel, dim3(warps_grid(d, a.T * a.pieces)), 256, 0, stream, a);
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.rows) |
+                        reinterpret_cast<uintptr_t>(a.out) | uintptr_t(a.N) * sizeof(T);
+  if (all % 16 == 0) return launch_combine<T, 16>(d, bwd, a, stream);
+  if constexpr (sizeof(T) == 2)
+    if (all % 4 != 0) return launch_combine<T, 2>(d, bwd, a, stream);
+  return launch_combine<T, 4>(d, bwd, a, stream);
 }
 
 }  // namespace
@@ -521,9 +554,7 @@ qk_status qk_expert_combine_fwd(const void* rows, const int32_t* slot, const flo
   st = current_device(&d);
   if (st != QK_OK) return st;
   const CombineArgs a = {nullptr, rows, slot, weights, y, nullptr, T, P, N, 0, int32_t(k)};
-  const bool vec = N * int64_t(es) % 16 == 0 && aligned16(rows) && aligned16(y);
-  return dtype == QK_F32 ? launch_combine<float>(d, false, vec, a, stream)
-                         : launch_combine<__nv_bfloat16>(d, false, vec, a, stream);
+  return dtype == QK_F32 ? launch_combine<float>(d, false, a, stream) : launch_combine<__nv_bfloat16>(d, false, a, stream);
 }
 
 qk_status qk_expert_combine_bwd(const void* dy, const void* rows, const int32_t* slot, const float* weights,
@@ -550,9 +581,7 @@ qk_status qk_expert_combine_bwd(const void* dy, const void* rows, const int32_t*
   st = current_device(&d);
   if (st != QK_OK) return st;
   const CombineArgs a = {dy, rows, slot, weights, drows, dweights, T, P, N, 0, int32_t(k)};
-  const bool vec = N * int64_t(es) % 16 == 0 && aligned16(rows) && aligned16(drows) && aligned16(dy);
-  return dtype == QK_F32 ? launch_combine<float>(d, true, vec, a, stream)
-                         : launch_combine<__nv_bfloat16>(d, true, vec, a, stream);
+  return dtype == QK_F32 ? launch_combine<float>(d, true, a, stream) : launch_combine<__nv_bfloat16>(d, true, a, stream);
 }
 
 }  // extern "C"
