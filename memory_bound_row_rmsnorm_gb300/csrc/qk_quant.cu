@@ -128,18 +128,38 @@ struct EightBitsOf {
   }
 };
 
-// E (8 or 4) values in 8 bits, of which `left` count.
+// E (8 or 4) values in 8 bits.
 template <int E>
 __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t* words) {
   if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(words[0], words[1]);
   else *reinterpret_cast<uint32_t*>(p) = words[0];
 }
-template <int E>
-__device__ __forceinline__ void store_bytes(uint8_t* p, const uint32_t* words, int left, bool vec) {
-  if (vec && left >= E) return store_words<E>(p, words);
-#pragma unroll
-  for (int j = 0; j < E; ++j)
-    if (j < left) p[j] = uint8_t(words[j / 4] >> (8 * (j % 4)));
+
+// A row of n <= 128 bytes that starts anywhere, by a warp: words where the memory has
+// them, bytes at the ends.  word(i) is the row's i-th word in shared memory
+// (16384 x 4095 bf16, straight: 95 us, 128 with bytes; 16383 x 4096 turned: 62 and 100).
+template <typename F>
+__device__ __forceinline__ void store_row(uint8_t* p, int n, int lane, F word) {
+  const int lead = min(n, int(-reinterpret_cast<uintptr_t>(p) & 3)), words = (n - lead) >> 2, tail = lead + 4 * words;
+  auto byte = [&](int i) { return uint8_t(word(i >> 2) >> (8 * (i & 3))); };
+  if (lane < words)
+    *reinterpret_cast<uint32_t*>(p + lead + 4 * lane) =
+        __funnelshift_r(word(lane), lead == 0 || lane == 31 ? 0u : word(lane + 1), 8 * lead);
+  if (lane < lead) p[lane] = byte(lane);
+  if (tail + lane < n) p[tail + lane] = byte(tail + lane);
+}
+
+// 16 bytes from anywhere in [lo, hi), from the words that they lie in, which the matrix
+// has to hold; false where it does not.
+__device__ __forceinline__ bool load_across(const void* p, uintptr_t lo, uintptr_t hi, uint4* v) {
+  const uintptr_t s = reinterpret_cast<uintptr_t>(p), s4 = s & ~uintptr_t(3);
+  const uint32_t shift = uint32_t(s & 3) * 8;
+  if (s4 < lo || s4 + (shift == 0 ? 16 : 20) > hi) return false;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(s4);
+  const uint32_t a = w[0], b = w[1], c = w[2], d = w[3], e = shift == 0 ? 0 : w[4];
+  *v = make_uint4(__funnelshift_r(a, b, shift), __funnelshift_r(b, c, shift), __funnelshift_r(c, d, shift),
+                  __funnelshift_r(d, e, shift));
+  return true;
 }
 
 // The registers of a thread are held down to 64 (bf16: 62 us at 16384 x 4096 both
@@ -171,10 +191,13 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
       if constexpr (VEC) {  // N is a multiple of E
         if (c0 < cols) raw[r] = __ldcs(reinterpret_cast<const uint4*>(x + r * a.N));
       } else {
-        float f[E];
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(a.x), hi = lo + uintptr_t(a.M) * uintptr_t(a.N) * sizeof(T);
+        if (sizeof(T) == 4 || c0 + E > cols || !load_across(x + r * a.N, lo, hi, &raw[r])) {
+          float f[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = c0 + j < cols ? V::load1(x + r * a.N + j) : 0.f;
-        raw[r] = V::pack(f);  // exact: the values are T's
+          for (int j = 0; j < E; ++j) f[j] = c0 + j < cols ? V::load1(x + r * a.N + j) : 0.f;
+          raw[r] = V::pack(f);  // exact: the values are T's
+        }
       }
     }
   }
@@ -246,8 +269,22 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
       uint32_t words[E / 4];
 #pragma unroll
       for (int j = 0; j < E; j += 4) words[j / 4] = B::template four<T>(f + j, d);
-      if (inside) store_words<E>(q, words);
-      else if (r0 + r < rows) store_bytes<E>(q, words, cols - c0, a.vec_q);
+      if (inside || (a.vec_q && r0 + r < rows && c0 < cols)) {
+        store_words<E>(q, words);  // N is a multiple of 8
+      } else if (!a.vec_q && sizeof(T) == 2) {
+        store_words<E>(turned + (r0 + r) * kTile + c0, words);
+      } else if (!a.vec_q && r0 + r < rows) {  // float32's four bytes a thread: 79 us at 16384 x 4095, by way of the tile 99
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (c0 + j < cols) q[j] = uint8_t(words[j / 4] >> (8 * (j % 4)));
+      }
+    }
+    if (!a.vec_q && sizeof(T) == 2) {
+      __syncthreads();
+      for (int row = warp; row < rows; row += kWarps)
+        store_row(a.q + (i0 + row) * a.N + j0, cols, lane,
+                  [&](int i) { return reinterpret_cast<const uint32_t*>(turned + row * kTile)[i]; });
+      __syncthreads();
     }
   }
   if (a.qt == nullptr) return;
@@ -287,16 +324,22 @@ __global__ void __launch_bounds__(quant_threads<T>(), 1024 / quant_threads<T>())
     *reinterpret_cast<uint2*>(turned + (c0 + j) * kTile + (((r0 >> 3) ^ unit_key) & 15) * 8) = make_uint2(words[0], words[1]);
   }
   __syncthreads();
+  if (!a.vec_qt) {
+    for (int col = warp; col < cols; col += kWarps)
+      store_row(a.qt + (j0 + col) * a.M + i0, rows, lane, [&](int i) {
+        return *reinterpret_cast<const uint32_t*>(turned + col * kTile + (((i >> 1) ^ (col >> 3)) & 15) * 8 + (i & 1) * 4);
+      });
+    return;
+  }
   const int unit = lane & 15, first = warp * 2 + (lane >> 4);
   uint8_t* qt = a.qt + (j0 + first) * a.M + i0 + unit * 8;
-  const bool inside = a.vec_qt && rows == kTile && cols == kTile;
+  const bool inside = rows == kTile && cols == kTile;
 #pragma unroll
   for (int k = 0; k < kTile / 2 / kWarps; ++k, qt += 2 * kWarps * a.M) {
     const int col = first + k * 2 * kWarps;
     const uint2 w = *reinterpret_cast<const uint2*>(turned + col * kTile + ((unit ^ (col >> 3)) & 15) * 8);
     const uint32_t words[2] = {w.x, w.y};
-    if (inside) store_words<8>(qt, words);
-    else if (col < cols && unit * 8 < rows) store_bytes<8>(qt, words, rows - unit * 8, a.vec_qt);
+    if (inside || (col < cols && unit * 8 < rows)) store_words<8>(qt, words);  // M is a multiple of 8
   }
 }
 
