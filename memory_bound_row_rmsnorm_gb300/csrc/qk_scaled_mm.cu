@@ -191,9 +191,9 @@ double likely_tiles(const Call& c, int64_t rows) {
 // Microseconds: a launch, and a step and an end for each tile that an SM does one
 // after the other.  Measured over 1 to 2048 rows x 200 to 8192 x 1024 to 8192, and
 // 2 to 16384 rows of 32 experts x 4096 x 2048 and 2048 x 4096, in a graph.
-constexpr double kTileLaunch = 5.2, kPairLaunch = 4.4, kPairStep = 0.40, kPairStepRows = 0.62, kPairEnd = 1.7;
+constexpr double kTileLaunch = 5.2, kPairLaunch = 4.4, kPairStep = 0.40, kPairStepRows = 0.59, kPairEnd = 1.7;
 template <int TN>
-constexpr double tile_step() { return TN == 16 ? 0.24 : TN == 32 ? 0.25 : TN == 64 ? 0.29 : 0.43; }
+constexpr double tile_step() { return TN == 16 ? 0.24 : TN == 32 ? 0.25 : TN == 64 ? 0.28 : 0.41; }
 template <int TN>
 constexpr double tile_end() { return TN == 16 ? 0.8 : TN == 32 ? 1.0 : TN == 64 ? 1.1 : 3.2; }
 
