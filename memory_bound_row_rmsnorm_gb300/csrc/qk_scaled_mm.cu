@@ -191,7 +191,10 @@ double likely_tiles(const Call& c, int64_t rows) {
 // Microseconds: a launch, and a step and an end for each tile that an SM does one
 // after the other.  Measured over 1 to 2048 rows x 200 to 8192 x 1024 to 8192, and
 // 2 to 16384 rows of 32 experts x 4096 x 2048 and 2048 x 4096, in a graph.
-constexpr double kTileLaunch = 5.2, kPairLaunch = 4.4, kPairStep = 0.40, kPairStepRows = 0.59, kPairEnd = 1.7;
+constexpr double kTileLaunch = 5.2, kPairLaunch = 4.4, kPairStep = 0.40, kPairStepRows = 0.59;
+constexpr double kTileEndF32 = 1.45;  // times the end in bf16
+// A pair's tile's end, bf16 and float32: rows of y on 16 bytes, which leave by TMA, and off them.
+constexpr double kPairEnd[2] = {1.7, 3.0}, kPairEndOff[2] = {3.2, 5.2};
 template <int TN>
 constexpr double tile_step() { return TN == 16 ? 0.24 : TN == 32 ? 0.25 : TN == 64 ? 0.28 : 0.41; }
 template <int TN>
@@ -216,7 +219,7 @@ TilePlan plan_tiles(const Call& c) {
     ++log2_ranks;
   plan.ranks = 1 << log2_ranks;
   const double waves = std::ceil(likely_tiles(c, TN) * double(n_tiles) * plan.ranks / c.dev.sms);
-  plan.us = kTileLaunch + waves * (double(ceil_div(groups, plan.ranks)) * tile_step<TN>() + tile_end<TN>());
+  plan.us = kTileLaunch + waves * (double(ceil_div(groups, plan.ranks)) * tile_step<TN>() + tile_end<TN>() * (sizeof(T) == 4 ? kTileEndF32 : 1.0));
   return plan;
 }
 
@@ -232,6 +235,12 @@ qk_status launch_tiles(const Call& c, const TilePlan& plan) {
   return launch(c, scaled_tile_kernel<TN, T>, grid, kScaledThreads, plan.ranks, tile_smem(TN), ma, mb, p);
 }
 
+// Rows of y are whole 16-byte vectors, which leave by TMA.
+template <typename T>
+bool whole_rows(const Call& c) {
+  return c.N * int64_t(sizeof(T)) % 16 == 0 && aligned16(c.y);
+}
+
 template <bool COLS, typename T>
 qk_status launch_pairs(const Call& c) {
   const auto kernel = scaled_pair_kernel<COLS, T>;
@@ -243,7 +252,7 @@ qk_status launch_pairs(const Call& c) {
   // The last column tile as a product of the columns it has: halves of whole 8-row groups of b.
   p.last_n = int32_t(std::min<int64_t>(256, round_up(c.N - int64_t(p.n_tiles - 1) * 256, 32)));
   p.n_full = p.last_n == 256 ? p.n_tiles : p.n_tiles - 1;
-  p.y_vec = c.N * int64_t(sizeof(T)) % 16 == 0 && aligned16(c.y);
+  p.y_vec = whole_rows<T>(c);
   const int64_t tiles = most_tiles(c, 256) * p.n_tiles;
   CUtensorMap ma, mb, my = {};
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128) ||
@@ -276,7 +285,8 @@ qk_status product(const Call& c) {
   const TilePlan plans[] = {plan_tiles<16, T>(c), plan_tiles<32, T>(c), plan_tiles<64, T>(c), plan_tiles<128, T>(c)};
   const double waves = std::ceil(likely_tiles(c, 256) * double(ceil_div(c.N, 256)) / (c.dev.sms / 2));
   const double step = c.b_rows == 1 ? kPairStepRows : kPairStep;
-  double best = kPairLaunch + waves * (double(ceil_div(c.K, kScaledStepK)) * step + kPairEnd);
+  const double end = (whole_rows<T>(c) ? kPairEnd : kPairEndOff)[sizeof(T) == 4];
+  double best = kPairLaunch + waves * (double(ceil_div(c.K, kScaledStepK)) * step + end);
   int pick = -1;
   for (int i = 0; i < 4; ++i) {
     if (plans[i].status != QK_OK) return plans[i].status;
