@@ -91,7 +91,7 @@ SIZES = [(1, 1, 1), (1, 128, 128), (2, 5, 3), (1, 4096, 512), (3, 300, 16), (7, 
          # pairs of CTAs: odd rows, last column tiles of every width class, steps that are no whole quads
          (520, 2089, 640), (777, 2112, 1040), (1025, 1184, 129), (600, 2337, 100), (1500, 1600, 272), (1001, 2047, 1023),
          # tiles of 128 rows of a, alone and with k shared by a cluster
-         (374, 1801, 4144), (218, 3612, 3950), (256, 4096, 4096)]
+         (374, 1801, 4144), (218, 3612, 3950), (256, 4096, 4096), (500, 2557, 3968)]
 
 
 @gpu
