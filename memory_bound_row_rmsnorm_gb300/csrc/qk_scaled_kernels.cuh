@@ -782,19 +782,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // whatever stands behind it, which TMA reads as zero.  A thread makes 16 bytes
 // from the five words that they lie in, or from single bytes where a word would
 // reach out of the matrix (1001 x 2047 x 1023 in all: 25 us, from bytes and in two launches 28).
+// Sorted rows: only those between the first expert's and the last one's, and the
+// weights of experts whose offsets rise, which all that have rows are among
+// (one token's 8 choices of 64 experts, 4096 x 4095: 89 us, with all weights 422).
+// What a tile reads beyond them ends in rows that it does not store.
 struct PadArgs {
-  const uint8_t* in[2];
+  const uint8_t* in[2];  // b, a
   uint8_t* out[2];
   int64_t rows[2];
+  const int32_t* offsets;  // [experts + 1], null: all rows
+  int32_t experts;
+  int32_t expert_rows;     // rows of b of one expert
   int32_t cols, ld;
 };
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
+  auto offset = [&](int32_t e) { return min(max(int64_t(a.offsets[e]), int64_t(0)), a.rows[1]); };
+  int64_t end = -1;  // of the last expert's rows: the largest offset, found by the first row of a
   for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows[0] + a.rows[1]; r += int64_t(gridDim.x) * 8) {
     const int which = r >= a.rows[0];
     const int64_t row = which ? r - a.rows[0] : r;
+    if (a.offsets != nullptr) {
+      if (which) {
+        if (end < 0) {
+          int32_t top = 0;
+          for (int32_t e = lane; e <= a.experts; e += 32) top = max(top, int32_t(offset(e)));
+          end = __reduce_max_sync(0xffffffffu, top);
+        }
+        if (row < offset(0) || row >= end) continue;
+      } else {
+        const int32_t e = int32_t(row / a.expert_rows);
+        if (offset(e + 1) <= offset(e)) continue;
+      }
+    }
     const uint8_t* in = a.in[which];
     const uintptr_t lo = reinterpret_cast<uintptr_t>(in), hi = lo + uintptr_t(a.rows[which]) * uintptr_t(a.cols);
     uint8_t* dst = a.out[which] + row * a.ld;

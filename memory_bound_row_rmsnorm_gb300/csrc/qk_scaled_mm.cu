@@ -272,6 +272,9 @@ qk_status pad_operands(Call& c, void* workspace) {
   p.in[1] = static_cast<const uint8_t*>(c.a);
   p.out[0] = at;
   p.out[1] = at + p.rows[0] * c.ld;
+  p.offsets = c.offsets;
+  p.experts = int32_t(c.experts);
+  p.expert_rows = int32_t(c.N);
   p.cols = int32_t(c.K);
   p.ld = int32_t(c.ld);
   c.b = p.out[0];
