@@ -467,9 +467,10 @@ QK_API qk_status qk_quant_fwd(const void* x, void* q, float* scale, void* qt, fl
  *   y        [M, N] out_dtype; overlaps no other buffer.
  *   workspace  at least qk_scaled_mm_workspace_size() bytes, 256-byte aligned,
  *              scratch; may be NULL when that is 0.  It is 0 when K is a multiple of
- *              16; a and b must then be 16-byte aligned.  Otherwise a and b go
- *              through it, in rows that start on 16 bytes (with offsets, the experts'
- *              rows and the b of those that have any).
+ *              16; of a and b that are not 16-byte aligned it has to hold the M K and
+ *              experts N K bytes then (QK_ERR_MISALIGNED otherwise).  Where K is not a
+ *              multiple of 16, a and b go through it, in rows that start on 16 bytes
+ *              (with offsets, the experts' rows and the b of those that have any).
  *   M, N, K at most 2^31 - 1024, experts at most 1024 (QK_ERR_UNSUPPORTED beyond).
  *   A block's sum is float32, is multiplied with the product of its two scales
  *   and added to nearest in float32.  Results do not change from run to run.  A

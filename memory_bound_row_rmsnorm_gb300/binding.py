@@ -808,7 +808,8 @@ def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None
     offsets[e] ... offsets[e + 1] - 1 are multiplied with b[e].T; rows behind
     the last are left as they were in `out`, and not written in a new tensor.
     The output is out_dtype, or out's (torch.bfloat16 or torch.float32; bfloat16
-    when neither is given)."""
+    when neither is given).  Operands that start off 16 bytes, or whose K is no
+    multiple of 16, are copied on the way."""
     if stream is not None:
         return _on(stream, scaled_mm_fwd, a, a_scale, b, b_scale, offsets, out_dtype, out)
     dev = _device(a)
@@ -836,10 +837,14 @@ def scaled_mm_fwd(a, a_scale, b, b_scale, offsets=None, out_dtype=None, out=None
     y_shape = (M, N) if len(shape) == 2 else shape[:-1] + (N,)
     y = torch.empty(y_shape, dtype=out_dtype, device=a.device) if out is None else _same("out", out, y_shape,
                                                                                         out_dtype, dev)
-    nbytes = 0 if K % 16 == 0 else _workspace_bytes(qk_scaled_mm_workspace_size, dev, M, N, K, experts)
+    pa, pb, nbytes = a.data_ptr(), b.data_ptr(), 0
+    if K % 16:
+        nbytes = _workspace_bytes(qk_scaled_mm_workspace_size, dev, M, N, K, experts)
+    elif (pa | pb) & 15:  # what starts off 16 bytes is copied
+        nbytes = (a.numel() if pa & 15 else 0) + (b.numel() if pb & 15 else 0)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=a.device) if nbytes else None
     _check(load_library().qk_scaled_mm_fwd(
-        a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+        pa, a_scale.data_ptr(), pb, b_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), y.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, M, N,
         K, experts, 1 if rows == N else 128, code, _current_stream(dev)), "qk_scaled_mm_fwd")
     return y

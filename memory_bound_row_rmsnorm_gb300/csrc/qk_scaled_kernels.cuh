@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 struct PadArgs {
   const uint8_t* in[2];  // b, a
   uint8_t* out[2];
-  int64_t rows[2];
+  int64_t rows[2];         // 0: this one is read where it is
+  int64_t M;               // what offsets lie within
   const int32_t* offsets;  // [experts + 1], null: all rows
   int32_t experts;
   int32_t expert_rows;     // rows of b of one expert
@@ -799,7 +800,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
-  auto offset = [&](int32_t e) { return min(max(int64_t(a.offsets[e]), int64_t(0)), a.rows[1]); };
+  auto offset = [&](int32_t e) { return min(max(int64_t(a.offsets[e]), int64_t(0)), a.M); };
   int64_t end = -1;  // of the last expert's rows: the largest offset, found by the first row of a
   for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < a.rows[0] + a.rows[1]; r += int64_t(gridDim.x) * 8) {
     const int which = r >= a.rows[0];

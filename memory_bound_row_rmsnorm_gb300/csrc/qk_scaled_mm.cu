@@ -44,9 +44,11 @@ qk_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t experts) {
   return QK_OK;
 }
 
-// Rows that TMA cannot read where they are go through the workspace.
-int64_t copy_bytes(int64_t M, int64_t N, int64_t K, int64_t experts) {
-  return K % 16 == 0 ? 0 : (M + N * experts) * round_up(K, 16);
+// Rows that TMA cannot read where they are go through the workspace: all where K is
+// not a multiple of 16, else those of an operand that starts off 16 bytes.
+bool copied(const void* operand, int64_t K) { return K % 16 != 0 || !aligned16(operand); }
+int64_t copy_bytes(const void* a, const void* b, int64_t M, int64_t N, int64_t K, int64_t experts) {
+  return ((copied(a, K) ? M : 0) + (copied(b, K) ? N * experts : 0)) * round_up(K, 16);
 }
 
 // Rows of bytes [planes][rows][ld] of which the first `inner` count, in boxes of
@@ -261,24 +263,26 @@ qk_status launch_pairs(const Call& c) {
   return launch(c, kernel, 2 * std::min<int64_t>(tiles, c.dev.sms / 2), kPairThreads, 2, pair_smem(COLS), ma, mb, my, p);
 }
 
-// Rows of a and b as TMA reads them, by way of the workspace where K is not a multiple of 16.
+// Rows of a and b as TMA reads them, by way of the workspace where it has to be.
 qk_status pad_operands(Call& c, void* workspace) {
-  if (c.ld == c.K) return QK_OK;
+  const bool copy_a = copied(c.a, c.K), copy_b = copied(c.b, c.K);
+  if (!copy_a && !copy_b) return QK_OK;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   PadArgs p = {};
-  p.rows[0] = c.N * c.experts;
-  p.rows[1] = c.M;
+  p.rows[0] = copy_b ? c.N * c.experts : 0;
+  p.rows[1] = copy_a ? c.M : 0;
   p.in[0] = static_cast<const uint8_t*>(c.b);
   p.in[1] = static_cast<const uint8_t*>(c.a);
   p.out[0] = at;
   p.out[1] = at + p.rows[0] * c.ld;
   p.offsets = c.offsets;
+  p.M = c.M;
   p.experts = int32_t(c.experts);
   p.expert_rows = int32_t(c.N);
   p.cols = int32_t(c.K);
   p.ld = int32_t(c.ld);
-  c.b = p.out[0];
-  c.a = p.out[1];
+  if (copy_b) c.b = p.out[0];
+  if (copy_a) c.a = p.out[1];
   const unsigned grid = unsigned(std::min<int64_t>(ceil_div(p.rows[0] + p.rows[1], 8), 16 * c.dev.sms));
   return launch_pdl(pad_rows_kernel, dim3(grid), 256, 0, c.stream, p);
 }
@@ -315,7 +319,7 @@ qk_status qk_scaled_mm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t e
   if (bytes == nullptr) return QK_ERR_INVALID_ARG;
   *bytes = 0;
   const qk_status st = check_sizes(M, N, K, experts);
-  if (st == QK_OK && M > 0) *bytes = size_t(copy_bytes(M, N, K, experts));
+  if (st == QK_OK && M > 0) *bytes = size_t(copy_bytes(nullptr, nullptr, M, N, K, experts));
   return st;
 }
 
@@ -334,10 +338,10 @@ qk_status qk_scaled_mm_fwd(const void* a, const float* a_scale, const void* b, c
   const size_t es = size_t(elem_size(out_dtype));
   if (!aligned_to(y, es) || !aligned_to(a_scale, 4) || !aligned_to(b_scale, 4) || !aligned_to(offsets, 4))
     return QK_ERR_MISALIGNED;
-  if (K % 16 == 0 && (!aligned16(a) || !aligned16(b))) return QK_ERR_MISALIGNED;
-  const int64_t need = copy_bytes(M, N, K, experts), groups = ceil_div(K, kScaledStepK);
+  const int64_t need = copy_bytes(a, b, M, N, K, experts), groups = ceil_div(K, kScaledStepK);
   if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < size_t(need)) return QK_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < size_t(need))
+      return K % 16 == 0 ? QK_ERR_MISALIGNED : QK_ERR_INVALID_ARG;
     if (!aligned_to(workspace, 256)) return QK_ERR_MISALIGNED;
   }
   const struct {
