@@ -485,6 +485,20 @@ QK_API qk_status qk_scaled_mm_fwd(const void* a, const float* a_scale, const voi
                                   const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes,
                                   int64_t M, int64_t N, int64_t K, int64_t experts, int64_t b_block_rows,
                                   qk_dtype out_dtype, void* stream);
+/*
+ * Fills *plan with what qk_scaled_mm_fwd with these arguments would launch on the
+ * current device (zeros where that is nothing).  Of offsets only whether it is NULL
+ * counts, of y its alignment (NULL: aligned); neither is read.
+ */
+typedef struct qk_scaled_mm_plan {
+  int32_t rows;    /* rows of a of a tile: 16, 32, 64, 128, or 256 by a pair of CTAs */
+  int32_t columns; /* rows of b of a tile: 128, or 256 by a pair */
+  int32_t ctas;    /* CTAs of a tile: the pair's 2, or the 1, 2, 4 or 8 that share its k */
+  int32_t grid;    /* CTAs in all */
+} qk_scaled_mm_plan;
+QK_API qk_status qk_scaled_mm_get_plan(const int32_t* offsets, const void* y, int64_t M, int64_t N, int64_t K,
+                                       int64_t experts, int64_t b_block_rows, qk_dtype out_dtype,
+                                       qk_scaled_mm_plan* plan);
 
 /*
  * Tokens sorted by expert.  Each of T tokens has k choices; a choice outside

@@ -46,7 +46,7 @@ _EXPORTS = (
     "qk_add_rmsnorm_bwd", "qk_add_rmsnorm_bwd_workspace_size", "qk_rmsnorm_quant_fwd",
     "qk_linear_xent_fwd", "qk_linear_xent_fwd_workspace_size", "qk_linear_xent_bwd",
     "qk_linear_xent_bwd_workspace_size", "qk_quant_fwd", "qk_scaled_mm_fwd",
-    "qk_scaled_mm_workspace_size", "qk_expert_sort", "qk_expert_sort_workspace_size",
+    "qk_scaled_mm_workspace_size", "qk_scaled_mm_get_plan", "qk_expert_sort", "qk_expert_sort_workspace_size",
     "qk_expert_gather_fwd", "qk_expert_combine_fwd", "qk_expert_combine_bwd",
 )
 
@@ -60,6 +60,10 @@ class QkError(RuntimeError):
 class qk_xent_options(ctypes.Structure):
     _fields_ = [("has_ignore_index", ctypes.c_int32), ("z_loss", ctypes.c_float),
                 ("ignore_index", ctypes.c_int64)]
+
+
+class qk_scaled_mm_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "columns", "ctas", "grid")]
 
 
 class qk_plan(ctypes.Structure):
@@ -123,6 +127,7 @@ def load_library(path: str = LIBRARY):
         sz = ctypes.c_size_t
         lib.qk_quant_fwd.argtypes = [vp] * 5 + [i64, i64, i64, i32, i32, vp]
         lib.qk_scaled_mm_workspace_size.argtypes = [i64, i64, i64, i64, sp]
+        lib.qk_scaled_mm_get_plan.argtypes = [vp] * 2 + [i64] * 5 + [i32, ctypes.POINTER(qk_scaled_mm_plan)]
         lib.qk_scaled_mm_fwd.argtypes = [vp] * 7 + [sz, i64, i64, i64, i64, i64, i32, vp]
         lib.qk_expert_sort_workspace_size.argtypes = [i64, i64, i64, sp]
         lib.qk_expert_sort.argtypes = [vp, i64, vp, vp, vp, sz, i64, i64, i64, vp]
@@ -136,7 +141,7 @@ def load_library(path: str = LIBRARY):
                      "qk_layernorm_fwd", "qk_add_rmsnorm_fwd", "qk_add_rmsnorm_bwd_workspace_size",
                      "qk_add_rmsnorm_bwd", "qk_rmsnorm_quant_fwd", "qk_linear_xent_fwd_workspace_size",
                      "qk_linear_xent_fwd", "qk_linear_xent_bwd_workspace_size", "qk_linear_xent_bwd",
-                     "qk_quant_fwd", "qk_scaled_mm_workspace_size", "qk_scaled_mm_fwd",
+                     "qk_quant_fwd", "qk_scaled_mm_workspace_size", "qk_scaled_mm_get_plan", "qk_scaled_mm_fwd",
                      "qk_expert_sort_workspace_size", "qk_expert_sort", "qk_expert_gather_fwd",
                      "qk_expert_combine_fwd", "qk_expert_combine_bwd"):
             getattr(lib, name).restype = i32
@@ -325,6 +330,14 @@ def qk_scaled_mm_fwd(a, a_scale, b, b_scale, offsets, y, workspace, workspace_by
     _check(load_library().qk_scaled_mm_fwd(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(offsets), _ptr(y),
                                            _ptr(workspace), int(workspace_bytes), M, N, K, experts, b_block_rows,
                                            out_dtype, _stream(stream)), "qk_scaled_mm_fwd")
+
+
+def qk_scaled_mm_get_plan(offsets, y, M: int, N: int, K: int, experts: int, b_block_rows: int,
+                          out_dtype: int) -> dict:
+    p = qk_scaled_mm_plan()
+    _check(load_library().qk_scaled_mm_get_plan(_ptr(offsets), _ptr(y), M, N, K, experts, b_block_rows, out_dtype,
+                                                ctypes.byref(p)), "qk_scaled_mm_get_plan")
+    return {n: getattr(p, n) for n, _ in qk_scaled_mm_plan._fields_}
 
 
 def qk_expert_sort_workspace_size(T: int, k: int, num_experts: int) -> int:

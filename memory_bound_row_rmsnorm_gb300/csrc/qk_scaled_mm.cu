@@ -44,6 +44,15 @@ qk_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t experts) {
   return QK_OK;
 }
 
+qk_status check_call(const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t experts, int64_t b_block_rows,
+                     qk_dtype out_dtype) {
+  const qk_status st = check_sizes(M, N, K, experts);
+  if (st != QK_OK) return st;
+  if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
+  if (b_block_rows != 1 && b_block_rows != 128) return QK_ERR_INVALID_ARG;
+  return offsets == nullptr && experts != 1 ? QK_ERR_INVALID_ARG : QK_OK;
+}
+
 // Rows that TMA cannot read where they are go through the workspace: all where K is
 // not a multiple of 16, else those of an operand that starts off 16 bytes.
 bool copied(const void* operand, int64_t K) { return K % 16 != 0 || !aligned16(operand); }
@@ -225,6 +234,13 @@ TilePlan plan_tiles(const Call& c) {
   return plan;
 }
 
+int64_t tiles_grid(const Call& c, const TilePlan& plan) {
+  return plan.ranks > 1 ? plan.tiles * plan.ranks : std::min<int64_t>(plan.tiles, c.dev.sms);
+}
+int64_t pairs_grid(const Call& c) {
+  return 2 * std::min<int64_t>(most_tiles(c, 256) * ceil_div(c.N, 256), c.dev.sms / 2);
+}
+
 template <int TN, typename T>
 qk_status launch_tiles(const Call& c, const TilePlan& plan) {
   ScaledArgs p = arguments(c);
@@ -233,8 +249,7 @@ qk_status launch_tiles(const Call& c, const TilePlan& plan) {
   CUtensorMap ma, mb;
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, TN) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128))
     return QK_ERR_LAUNCH;
-  const int64_t grid = plan.ranks > 1 ? plan.tiles * plan.ranks : std::min<int64_t>(plan.tiles, c.dev.sms);
-  return launch(c, scaled_tile_kernel<TN, T>, grid, kScaledThreads, plan.ranks, tile_smem(TN), ma, mb, p);
+  return launch(c, scaled_tile_kernel<TN, T>, tiles_grid(c, plan), kScaledThreads, plan.ranks, tile_smem(TN), ma, mb, p);
 }
 
 // Rows of y are whole 16-byte vectors, which leave by TMA.
@@ -255,12 +270,11 @@ qk_status launch_pairs(const Call& c) {
   p.last_n = int32_t(std::min<int64_t>(256, round_up(c.N - int64_t(p.n_tiles - 1) * 256, 32)));
   p.n_full = p.last_n == 256 ? p.n_tiles : p.n_tiles - 1;
   p.y_vec = whole_rows<T>(c);
-  const int64_t tiles = most_tiles(c, 256) * p.n_tiles;
   CUtensorMap ma, mb, my = {};
   if (!make_map(&ma, c.a, c.K, c.M, 1, c.ld, 128) || !make_map(&mb, c.b, c.K, c.N, c.experts, c.ld, 128) ||
       (p.y_vec && !make_out_map(&my, c, int(sizeof(T)))))
     return QK_ERR_LAUNCH;
-  return launch(c, kernel, 2 * std::min<int64_t>(tiles, c.dev.sms / 2), kPairThreads, 2, pair_smem(COLS), ma, mb, my, p);
+  return launch(c, kernel, pairs_grid(c), kPairThreads, 2, pair_smem(COLS), ma, mb, my, p);
 }
 
 // Rows of a and b as TMA reads them, by way of the workspace where it has to be.
@@ -287,23 +301,38 @@ qk_status pad_operands(Call& c, void* workspace) {
   return launch_pdl(pad_rows_kernel, dim3(grid), 256, 0, c.stream, p);
 }
 
+// Which kernel does a call: a plan of tiles, or pairs (pick -1).
+struct Choice {
+  qk_status status;
+  int pick;
+  TilePlan plans[4];  // 16, 32, 64 and 128 rows of a
+};
 template <typename T>
-qk_status product(const Call& c) {
-  const TilePlan plans[] = {plan_tiles<16, T>(c), plan_tiles<32, T>(c), plan_tiles<64, T>(c), plan_tiles<128, T>(c)};
+Choice choose(const Call& c) {
+  Choice r = {QK_OK, -1, {plan_tiles<16, T>(c), plan_tiles<32, T>(c), plan_tiles<64, T>(c), plan_tiles<128, T>(c)}};
   const double waves = std::ceil(likely_tiles(c, 256) * double(ceil_div(c.N, 256)) / (c.dev.sms / 2));
   const double step = c.b_rows == 1 ? kPairStepRows : kPairStep;
   const double end = (whole_rows<T>(c) ? kPairEnd : kPairEndOff)[sizeof(T) == 4];
   double best = kPairLaunch + waves * (double(ceil_div(c.K, kScaledStepK)) * step + end);
-  int pick = -1;
   for (int i = 0; i < 4; ++i) {
-    if (plans[i].status != QK_OK) return plans[i].status;
-    if (plans[i].us < best && plans[i].tiles <= kMostTiles) best = plans[i].us, pick = i;
+    if (r.plans[i].status != QK_OK) {
+      r.status = r.plans[i].status;
+      return r;
+    }
+    if (r.plans[i].us < best && r.plans[i].tiles <= kMostTiles) best = r.plans[i].us, r.pick = i;
   }
-  switch (pick) {
-    case 0: return launch_tiles<16, T>(c, plans[0]);
-    case 1: return launch_tiles<32, T>(c, plans[1]);
-    case 2: return launch_tiles<64, T>(c, plans[2]);
-    case 3: return launch_tiles<128, T>(c, plans[3]);
+  return r;
+}
+
+template <typename T>
+qk_status product(const Call& c) {
+  const Choice r = choose<T>(c);
+  if (r.status != QK_OK) return r.status;
+  switch (r.pick) {
+    case 0: return launch_tiles<16, T>(c, r.plans[0]);
+    case 1: return launch_tiles<32, T>(c, r.plans[1]);
+    case 2: return launch_tiles<64, T>(c, r.plans[2]);
+    case 3: return launch_tiles<128, T>(c, r.plans[3]);
     default: return c.b_rows == 1 ? launch_pairs<true, T>(c) : launch_pairs<false, T>(c);
   }
 }
@@ -323,16 +352,33 @@ qk_status qk_scaled_mm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t e
   return st;
 }
 
+qk_status qk_scaled_mm_get_plan(const int32_t* offsets, const void* y, int64_t M, int64_t N, int64_t K,
+                                int64_t experts, int64_t b_block_rows, qk_dtype out_dtype, qk_scaled_mm_plan* plan) {
+  if (plan == nullptr) return QK_ERR_INVALID_ARG;
+  *plan = {};
+  qk_status st = check_call(offsets, M, N, K, experts, b_block_rows, out_dtype);
+  if (st != QK_OK || M == 0) return st;
+  CurrentDevice d;
+  st = current_device(&d);
+  if (st != QK_OK) return st;
+  const Call c = {nullptr, nullptr, nullptr, nullptr, offsets, const_cast<void*>(y), M, N, K, experts, b_block_rows,
+                  round_up(K, 16), nullptr, d};
+  const Choice r = out_dtype == QK_F32 ? choose<float>(c) : choose<__nv_bfloat16>(c);
+  if (r.status != QK_OK) return r.status;
+  const bool pairs = r.pick < 0;
+  plan->rows = pairs ? 256 : 16 << r.pick;
+  plan->columns = pairs ? 256 : 128;
+  plan->ctas = pairs ? 2 : r.plans[r.pick].ranks;
+  plan->grid = int32_t(pairs ? pairs_grid(c) : tiles_grid(c, r.plans[r.pick]));
+  return QK_OK;
+}
+
 qk_status qk_scaled_mm_fwd(const void* a, const float* a_scale, const void* b, const float* b_scale,
                            const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes, int64_t M,
                            int64_t N, int64_t K, int64_t experts, int64_t b_block_rows, qk_dtype out_dtype,
                            void* stream) {
-  qk_status st = check_sizes(M, N, K, experts);
-  if (st != QK_OK) return st;
-  if (out_dtype != QK_F32 && out_dtype != QK_BF16) return QK_ERR_INVALID_ARG;
-  if (b_block_rows != 1 && b_block_rows != 128) return QK_ERR_INVALID_ARG;
-  if (offsets == nullptr && experts != 1) return QK_ERR_INVALID_ARG;
-  if (M == 0) return QK_OK;
+  qk_status st = check_call(offsets, M, N, K, experts, b_block_rows, out_dtype);
+  if (st != QK_OK || M == 0) return st;
   if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || y == nullptr)
     return QK_ERR_INVALID_ARG;
   const size_t es = size_t(elem_size(out_dtype));
