@@ -439,6 +439,8 @@ QK_API qk_status qk_linear_xent_bwd(const void* h, const void* w, const int64_t*
  *   x        [M, N] dtype, read once.
  *   q        [M, N] bytes, or NULL.  Groups are 128 columns of a row (block_rows
  *            1) or blocks of 128 x 128 (block_rows 128); the last may be short.
+ *            Blocks count from the first row: of matrices stacked to one, each has
+ *            blocks of its own only where its rows are a multiple of 128.
  *   scale    [M, ceil(N / 128)] or [ceil(M / 128), ceil(N / 128)] float32; NULL with q.
  *   qt       [N, M] bytes, or NULL: x^T in 8 bits, its groups 128 rows of a
  *            column of x (block_rows 1) or the same blocks.

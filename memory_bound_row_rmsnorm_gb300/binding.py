@@ -764,6 +764,8 @@ def quant_fwd(x, block_rows: int = 1, qdtype=None, want_q: bool = True, want_t: 
     (block_rows 1) or each block of 128 x 128 (block_rows 128, x of two
     dimensions); returns (q, scale, qt, scale_t).  qt, with want_t, is x
     transposed in 8 bits (x of two dimensions), its scales along x's columns.
+    Blocks count from x's first row: matrices stacked to one (experts' weights)
+    have blocks of their own where each one's rows are a multiple of 128.
     What is not wanted is None.  qdtype as in rmsnorm_quant_fwd."""
     if stream is not None:
         return _on(stream, quant_fwd, x, block_rows, qdtype, want_q, want_t)
