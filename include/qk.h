@@ -476,9 +476,11 @@ QK_API qk_status qk_quant_fwd(const void* x, void* q, float* scale, void* qt, fl
  *   M, N, K at most 2^31 - 1024, experts at most 1024 (QK_ERR_UNSUPPORTED beyond).
  *   A block's sum is float32, is multiplied with the product of its two scales
  *   and added to nearest in float32.  Results do not change from run to run.  A
- *   NaN value or scale reaches the outputs of its row (of its column) only.  Where
- *   the product of two scales leaves float32's normal range, 2^-126 to 2^128,
- *   digits are lost or y overflows.
+ *   NaN value of a or b and a NaN or infinite scale of a reach the outputs of their
+ *   row or column only; such a scale of b reaches the columns of its block (up to
+ *   128 with b_block_rows 128), by expert in that expert's rows.  Where the product
+ *   of two scales leaves float32's normal range, 2^-126 to 2^128, digits are lost or
+ *   y overflows.
  *   The gradient for a is the product of y's gradient, quantised, with b turned
  *   (qk_quant_fwd's qt with block_rows 128), with the same offsets.
  */
