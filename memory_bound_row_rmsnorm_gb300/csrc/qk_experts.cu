@@ -412,8 +412,13 @@ bool any_overlap(const Buffer (&out)[NO], const Buffer (&in)[NI]) {
 template <typename T, int WORD>
 qk_status launch_combine(const CurrentDevice& d, bool bwd, const CombineArgs& a, void* stream) {
   if (!bwd) return launch_pdl(combine_kernel<T, WORD>, dim3(warps_grid(d, a.T * a.pieces)), 256, 0, stream, a);
-  // A warp a token where a CTA would have less than a vector a thread.
-  const bool narrow = a.N <= 256 * Vec16<T>::kElems / 4;
+  // A warp a token for rows of at most two vectors a lane, and of at most four where there
+  // are 16 tokens for each SM; else a CTA.  us, bf16 with four choices, a warp and a CTA:
+  // 9728 tokens of 512 14.0 and 31.4, of 1024 31.9 and 42.8, of 1536 46.6 and 50.6, of 2048
+  // 61.1 and 59.1; 2432 of 1024 6.8 and 8.7, of 1023 20.4 and 21.1, of 1536 9.1 and 9.9; 608 of
+  // 1024 4.8 and 3.5, of 512 3.5 and 3.1.
+  const int64_t warp_values = 32 * Vec16<T>::kElems;
+  const bool narrow = a.N <= 2 * warp_values || (a.N <= 4 * warp_values && a.T >= 16 * int64_t(d.sms));
   const auto kernel = a.k <= 2 ? (narrow ? combine_bwd_kernel<T, WORD, 32, 2> : combine_bwd_kernel<T, WORD, 256, 2>)
                                : (narrow ? combine_bwd_kernel<T, WORD, 32, 4> : combine_bwd_kernel<T, WORD, 256, 4>);
   const int64_t blocks = narrow ? ceil_div(a.T, 8) : a.T;
