@@ -10,6 +10,7 @@ from test_scaled_mm import make, run
 gpu = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
 
+
 # narrow tiles, tiles whose k is shared, wide ones, pairs
 @gpu
 @pytest.mark.parametrize("M,N,K", [(5, 700, 384), (3, 300, 4096), (100, 515, 640), (300, 1800, 2048), (1500, 1600, 272)])
@@ -27,6 +28,7 @@ def test_scales_that_are_not_finite(cuda, M, N, K, b_rows, scale, out):
     hit[:, slice(256, 384) if b_rows == 128 else slice(2, 3)] = True
     assert not y[hit].isfinite().any()  # a block's sum times infinity, or 0 times it
     assert torch.equal(y[~hit], want[~hit])
+
 
 @gpu
 @pytest.mark.parametrize("counts", [[3, 5, 2, 40], [130, 70, 0, 9], [300, 257, 31, 500]])
