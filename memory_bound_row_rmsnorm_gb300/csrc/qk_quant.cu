@@ -72,15 +72,19 @@ struct EightBitsOf {
     const float den = bad ? *scale : fmaxf(amax, kSmallestGroupMax) * kDown;
     return {den, 1.f / den};
   }
-  // The quotient x qmax / max |x|, rounded to float32: what is rounded to 8 bits.  bf16:
-  // x mul is exact.  float32: what its rounding left out joins the division's remainder,
-  // so that the quotient is the rounded one all the same.
-  template <typename T>
+  // The quotient x qmax / max |x| of a float32 x, rounded to float32: what is rounded to 8
+  // bits.  What x mul's rounding left out joins the division's remainder; both are exact,
+  // their sum and den's reciprocal to 2^-24.  So the rounded quotient is a or b, from
+  // remainders 2^-20 apart on either side.  Where these are neighbours, what remains at the
+  // point halfway between them decides, and is exact too: the quotient may be that point (3 as
+  // a group's largest value has 33 such x beside ties of e4m3), and is the even one then.
   __device__ __forceinline__ static float value(float x, Divisor d) {
-    const float y = x * kMul;
-    const float q = quotient(y, d.den, d.inv);
-    if constexpr (sizeof(T) == 2) return q;
-    return fmaf(fmaf(-q, d.den, y) + fmaf(x, kMul, -y), d.inv, q);
+    const float y = x * kMul, q = quotient(y, d.den, d.inv);
+    const float rem = fmaf(-q, d.den, y), low = fmaf(x, kMul, -y), s = rem + low;
+    const float a = fmaf(s, d.inv * (1.f - 0x1p-20f), q), b = fmaf(s, d.inv * (1.f + 0x1p-20f), q);
+    if (a == b) return a;
+    const float left = fmaf(-((a - q) + 0.5f * (b - a)), d.den, rem) + low;
+    return left > 0.f ? fmaxf(a, b) : left < 0.f ? fminf(a, b) : __float_as_uint(a) & 1u ? b : a;
   }
   // Four floats in 8 bits, the first in the low byte.
   __device__ __forceinline__ static uint32_t packed(const float* f) {
@@ -113,7 +117,9 @@ struct EightBitsOf {
       const uint32_t w = packed(f);
       if (w == packed(g)) return w;
     }
-    if constexpr (sizeof(T) == 2) {  // value() in packed pairs: what bounds the kernel is the number of instructions
+    if constexpr (sizeof(T) == 2) {
+      // quotient() in packed pairs, as what bounds the kernel is the number of instructions.
+      // x mul is exact, and no quotient of two float32 numbers is a halfway point.
       const float2 mul = make_float2(kMul, kMul), inv = make_float2(d.inv, d.inv), less = make_float2(-d.den, -d.den);
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
@@ -121,8 +127,12 @@ struct EightBitsOf {
         f[i] = r.x, f[i + 1] = r.y;
       }
     } else {
+      // Small groups are taken 2^64 times as large, so that no remainder underflows.
+      const bool small = d.den < 0x1p-60f;
+      const float up = small ? 0x1p64f : 1.f;
+      const Divisor e = {d.den * up, small ? d.inv * 0x1p-64f : d.inv};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = value<T>(x[i], d);
+      for (int i = 0; i < 4; ++i) f[i] = value(x[i] * up, e);
     }
     return packed(f);
   }
